@@ -66,10 +66,14 @@ typedef enum {
     MT_VARIANT_TC16 = 3       /* tcgen05 kind::f16 on 16-bit inputs (mt_gemm_mixed* only) */
 } mt_variant;
 
-/* Storage type of A and B in the mt_gemm_mixed* entry points. */
+/* Storage types: of A and B in the mt_gemm_mixed* entry points (the 16-bit
+ * ones), and of the operators in mt_layers.h. */
 typedef enum {
     MT_DTYPE_F16 = 1,         /* IEEE 754 binary16 */
-    MT_DTYPE_BF16 = 2         /* bfloat16: the upper 16 bits of a binary32 */
+    MT_DTYPE_BF16 = 2,        /* bfloat16: the upper 16 bits of a binary32 */
+    MT_DTYPE_F32 = 3,         /* IEEE 754 binary32 (mt_layers.h only) */
+    MT_DTYPE_E4M3 = 4         /* 8-bit float, 4 exponent and 3 mantissa bits, no
+                                 infinities, largest value 448 (mt_layers.h only) */
 } mt_dtype;
 
 /* Optional launch choices.  Zero-initialise for "automatic". */

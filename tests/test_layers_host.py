@@ -1,0 +1,109 @@
+"""Host-side checks of the feed-forward operators' C entry points: argument
+errors and aliasing are refused before anything is launched (the pointers
+here are never dereferenced), and without a GPU a valid call reports that."""
+import ctypes
+
+import pytest
+
+import tiled_fp32_gemm_gb300 as mt
+from tiled_fp32_gemm_gb300 import build as mt_build
+
+try:
+    import torch
+    HAS_GPU = torch.cuda.is_available()
+except Exception:  # pragma: no cover
+    HAS_GPU = False
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    mt_build.build()
+    return mt.lib()
+
+
+def norm_args(**change):
+    a = mt.mt_rms_norm_args(rows=4, d=16, x=0x10000, ldx=16, residual=0x20000, ldr=16,
+                            weight=0x30000, h=0x40000, ldh=16, y=0x50000, ldy=16, scale=None,
+                            rstd=0x60000, eps=1e-6, dtype=mt.MT_DTYPE_BF16,
+                            out_dtype=mt.MT_DTYPE_BF16, weight_dtype=mt.MT_DTYPE_F32)
+    for k, v in change.items():
+        setattr(a, k, v)
+    return a
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("change", [
+    dict(rows=-1), dict(d=-1), dict(rows=1 << 31), dict(d=1 << 31), dict(x=None), dict(y=None),
+    dict(ldx=15), dict(ldr=15), dict(ldh=15), dict(ldy=15), dict(dtype=0), dict(dtype=9),
+    dict(dtype=mt.MT_DTYPE_E4M3), dict(out_dtype=mt.MT_DTYPE_F16), dict(out_dtype=0),
+    dict(weight_dtype=mt.MT_DTYPE_F16), dict(eps=-1e-6), dict(eps=INF), dict(eps=NAN),
+    dict(scale=0x70000), dict(out_dtype=mt.MT_DTYPE_E4M3), dict(x=0x10001), dict(weight=0x30002),
+    dict(rstd=0x60002), dict(ldx=1 << 60), dict(out_dtype=mt.MT_DTYPE_E4M3, scale=0x70002)])
+def test_norm_refuses_invalid_arguments(change):
+    assert mt.mt_rms_norm(norm_args(**change)) == mt.MT_ERR_INVALID_ARG
+
+
+def test_norm_refuses_no_arguments():
+    assert mt.lib().mt_rms_norm(None, None) == mt.MT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [
+    dict(h=0x10002), dict(h=0x20010), dict(h=0x20000, ldh=32), dict(y=0x20000), dict(y=0x40000),
+    dict(y=0x10010), dict(h=0x30000), dict(y=0x30010), dict(rstd=0x50000), dict(rstd=0x10004),
+    dict(out_dtype=mt.MT_DTYPE_E4M3, scale=0x60000),
+    dict(out_dtype=mt.MT_DTYPE_E4M3, scale=0x70000, y=0x10000, ldy=16)])
+def test_norm_refuses_overlap(change):
+    assert mt.mt_rms_norm(norm_args(**change)) == mt.MT_ERR_ALIAS
+
+
+@pytest.mark.skipif(HAS_GPU, reason="made-up addresses")
+@pytest.mark.parametrize("change", [dict(), dict(h=0x20000), dict(h=0x10000), dict(y=0x10000),
+                                    dict(residual=None, h=None, weight=None, rstd=None),
+                                    dict(out_dtype=mt.MT_DTYPE_E4M3, scale=0x70000)])
+def test_norm_without_a_device(change):
+    assert mt.mt_rms_norm(norm_args(**change)) == mt.MT_ERR_NO_DEVICE
+
+
+def test_norm_of_no_rows_is_nothing():
+    assert mt.mt_rms_norm(norm_args(rows=0)) == mt.MT_OK
+
+
+def test_packed_arguments_match_the_structure():
+    """The binding's one-call packing lays the fields out as the structure."""
+    from tiled_fp32_gemm_gb300 import layers
+    for cls in (mt.mt_rms_norm_args,):
+        values = [i + 1 for i in range(len(cls._fields_))]
+        a = cls.from_buffer_copy(layers._packer(cls)(*values))
+        for (name, _), v in zip(cls._fields_, values):
+            assert getattr(a, name) == v, name
+
+
+def test_arguments_have_the_c_layout(tmp_path):
+    """sizeof and every field offset agree with the C header."""
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        pytest.skip("no C compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(mt_build.nvcc())), "include")
+    classes = (mt.mt_rms_norm_args,)
+    lines, want = [], []
+    for cls in classes:
+        n = cls.__name__
+        lines.append(f'printf("%zu\\n", sizeof({n}));')
+        want.append(ctypes.sizeof(cls))
+        for f, _ in cls._fields_:
+            lines.append(f'printf("%zu\\n", offsetof({n}, {f}));')
+            want.append(getattr(cls, f).offset)
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "mt_layers.h"\n'
+                   'int main(void) {' + "\n".join(lines) + 'return 0; }\n')
+    exe = tmp_path / "layout"
+    subprocess.run([cc, "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"),
+                    "-I", cuda, str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+    assert [int(v) for v in out.split()] == want

@@ -17,7 +17,9 @@ by ``tiled_fp32_gemm_gb300.build``).  This module only marshals arguments:
   names, taking plain integers for pointers and streams;
 * ``sgemm(a, b, out=None, **choices)`` — the same call on torch CUDA tensors
   (torch supplies device memory and the current stream; nothing else);
-  ``gemm`` for the general form and ``gemm_mixed`` for 16-bit inputs.
+  ``gemm`` for the general form and ``gemm_mixed`` for 16-bit inputs;
+* the feed-forward operators of ``layers`` (include/mt_layers.h):
+  ``rms_norm``.
 
 There is no CPU fallback: if the library is missing, every call raises.
 """
@@ -136,6 +138,12 @@ SIGNATURES = {
     "mt_status_string": (ctypes.c_char_p, [_I]),
     "mt_version": (_I, []),
 }
+
+from .layers import (MT_DTYPE_E4M3, MT_DTYPE_F32, MT_E4M3_MAX,  # noqa: E402,F401
+                     MT_SCALE_MIN, mt_rms_norm, mt_rms_norm_args, rms_norm)
+from .layers import SIGNATURES as _LAYER_SIGNATURES  # noqa: E402
+
+SIGNATURES.update(_LAYER_SIGNATURES)
 
 _lock = threading.Lock()
 _lib = None

@@ -12,23 +12,19 @@
 #include <cuda_runtime.h>
 
 #include "device_util.cuh"
+#include "host.h"
 #include "kernels.h"
 #include "mt_sgemm.h"
 #include "smem_layout.cuh"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
+using namespace mt::host;
+
 // K depth of the 3xTF32 kernel when the caller does not choose: 16 for
 // 256-wide tiles (a 4-stage ring instead of 2), 32 for narrower tiles (3 or
 // 4 stages, half the barrier round trips) — the faster of the two on GB300.
 int tf32x3_default_bk(int bn) { return bn == 256 ? 16 : 32; }
-
-struct DeviceInfo {
-  int sms = 0;
-  int smem_optin = 0;  // max dynamic shared memory per block with opt-in
-  bool valid = false;
-};
 
 std::mutex g_mutex;
 DeviceInfo g_devices[kMaxDevices];
@@ -36,7 +32,9 @@ DeviceInfo g_devices[kMaxDevices];
 std::unordered_set<const void*> g_attr_done[kMaxDevices];
 cudaMemPool_t g_pools[kMaxDevices];
 
-mt_status current_device(int* dev, DeviceInfo* info) {
+}  // namespace
+
+mt_status mt::host::current_device(int* dev, DeviceInfo* info) {
   int d = -1;
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) {
     cudaGetLastError();
@@ -58,16 +56,7 @@ mt_status current_device(int* dev, DeviceInfo* info) {
   return MT_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-bool overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  if (a_bytes <= 0 || b_bytes <= 0 || !a || !b) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + static_cast<uintptr_t>(b_bytes) && b0 < a0 + static_cast<uintptr_t>(a_bytes);
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+namespace {
 
 // Row pitch (floats) of an operand copied for the FFMA kernel's 16-byte
 // staging: whole 128-byte lines, so every staged row segment starts on a
@@ -134,12 +123,6 @@ mt_status check_dims(int64_t M, int64_t N, int64_t K) {
   const int64_t lim = (INT64_MAX / 4) >> 1;
   if ((M && N > lim / M) || (M && K > lim / M) || (K && N > lim / K)) return MT_ERR_INVALID_ARG;
   return MT_OK;
-}
-
-// Bytes from the first to one past the last element of a rows x cols view
-// with row stride ld and elements of `elem` bytes.
-int64_t extent_bytes(int64_t rows, int64_t cols, int64_t ld, int elem = 4) {
-  return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * elem : 0;
 }
 
 // Leading dimensions: each stored row must hold its logical row.
@@ -324,9 +307,9 @@ __device__ mt::BoundsRecord g_bounds;
 mt::BoundsRecord* g_bounds_ptr[kMaxDevices];
 #endif
 
-// The record the current device's kernels write to: nullptr in normal
-// builds (and if the lookup fails).
-mt::BoundsRecord* bounds_record() {
+}  // namespace
+
+mt::BoundsRecord* mt::host::bounds_record() {
 #if MT_BOUNDS_CHECK
   int d = -1;
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) {
@@ -347,6 +330,8 @@ mt::BoundsRecord* bounds_record() {
   return nullptr;
 #endif
 }
+
+namespace {
 
 // The automatic 16-bit plan takes CTA pairs (256 x 256 tiles) when 256-wide
 // tiles are chosen and there are at least as many pair tiles as resident
@@ -863,7 +848,9 @@ mt_status set_smem_attr(int dev, const Launch& L) {
   return MT_OK;
 }
 
-mt_status pool_for(int dev, cudaMemPool_t* pool) {
+}  // namespace
+
+mt_status mt::host::pool_for(int dev, cudaMemPool_t* pool) {
   std::lock_guard<std::mutex> lock(g_mutex);
   if (!g_pools[dev]) {
     cudaMemPoolProps props;
@@ -886,6 +873,8 @@ mt_status pool_for(int dev, cudaMemPool_t* pool) {
   *pool = g_pools[dev];
   return MT_OK;
 }
+
+namespace {
 
 // [device][configuration]: shared-memory attribute of the 3xTF32 kernel applied.
 std::atomic<uint8_t> g_tf32x3_ready[kMaxDevices][16];

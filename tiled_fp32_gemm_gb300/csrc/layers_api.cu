@@ -1,0 +1,91 @@
+// C entry points of the feed-forward operators (include/mt_layers.h):
+// argument checks, launch choices, scratch.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "host.h"
+#include "layers.h"
+#include "mt_layers.h"
+
+namespace {
+
+using namespace mt::host;
+
+static_assert(MT_DTYPE_F16 == mt::DT_F16 && MT_DTYPE_BF16 == mt::DT_BF16 &&
+                  MT_DTYPE_F32 == mt::DT_F32 && MT_DTYPE_E4M3 == mt::DT_E4M3,
+              "storage type codes");
+
+// A rows x cols view of `elem`-byte values with row pitch ld, for the checks.
+struct View {
+  const void* p;
+  int64_t rows, cols, ld;
+  int elem;
+
+  int64_t bytes() const { return extent_bytes(rows, cols, ld, elem); }
+  bool empty() const { return rows == 0 || cols == 0; }
+  // The pitch holds a row, the span fits 64-bit offsets, and the pointer is
+  // there and aligned to its element unless there is nothing to address.
+  bool valid() const {
+    if (ld < (cols > 1 ? cols : 1) || ld > INT64_MAX / 64) return false;
+    if (rows > 0 && ld > INT64_MAX / 64 / rows) return false;
+    if (empty()) return true;
+    return p && (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(elem - 1)) == 0;
+  }
+  bool same(const View& o) const { return p == o.p && ld == o.ld && elem == o.elem; }
+  bool hits(const View& o) const { return overlaps(p, bytes(), o.p, o.bytes()); }
+};
+
+bool half_type(int t) { return t == MT_DTYPE_F16 || t == MT_DTYPE_BF16; }
+
+}  // namespace
+
+extern "C" {
+
+mt_status mt_rms_norm(const mt_rms_norm_args* g, cudaStream_t stream) {
+  if (!g || g->rows < 0 || g->d < 0 || g->d > INT32_MAX || g->rows > INT32_MAX)
+    return MT_ERR_INVALID_ARG;
+  if (!half_type(g->dtype) && g->dtype != MT_DTYPE_F32) return MT_ERR_INVALID_ARG;
+  if (g->out_dtype != g->dtype && g->out_dtype != MT_DTYPE_E4M3) return MT_ERR_INVALID_ARG;
+  if (g->weight && g->weight_dtype != g->dtype && g->weight_dtype != MT_DTYPE_F32)
+    return MT_ERR_INVALID_ARG;
+  if (!(g->eps >= 0.0f) || std::isinf(g->eps)) return MT_ERR_INVALID_ARG;
+  const bool e4m3 = g->out_dtype == MT_DTYPE_E4M3;
+  const int e = mt::dtype_bytes(g->dtype);
+  const int64_t rows = g->rows, d = g->d;
+  const View x{g->x, rows, d, g->ldx, e};
+  const View res{g->residual, g->residual ? rows : 0, d, g->residual ? g->ldr : INT32_MAX, e};
+  const View w{g->weight, g->weight ? 1 : 0, d, INT32_MAX, mt::dtype_bytes(g->weight_dtype)};
+  const View h{g->h, g->h ? rows : 0, d, g->h ? g->ldh : INT32_MAX, e};
+  const View y{g->y, rows, d, g->ldy, mt::dtype_bytes(g->out_dtype)};
+  const View scale{g->scale, e4m3 ? rows : 0, 1, 1, 4};
+  const View rstd{g->rstd, g->rstd ? rows : 0, 1, 1, 4};
+  for (const View* v : {&x, &res, &w, &h, &y, &scale, &rstd})
+    if (!v->valid()) return MT_ERR_INVALID_ARG;
+  if (!e4m3 && g->scale) return MT_ERR_INVALID_ARG;
+  if ((h.hits(x) && !h.same(x)) || (h.hits(res) && !h.same(res)) || (y.hits(x) && !y.same(x)) ||
+      y.hits(res) || y.hits(h) || w.hits(h) || w.hits(y))
+    return MT_ERR_ALIAS;
+  for (const View* s : {&scale, &rstd})
+    for (const View* v : {&x, &res, &w, &h, &y})
+      if (s->hits(*v)) return MT_ERR_ALIAS;
+  if (scale.hits(rstd)) return MT_ERR_ALIAS;
+  if (rows == 0) return MT_OK;
+  int dev = 0;
+  DeviceInfo info;
+  const mt_status st = current_device(&dev, &info);
+  if (st != MT_OK) return st;
+  const mt::RmsNormArgs a{rows, static_cast<int>(d), g->x, g->ldx, g->residual, g->ldr,
+                          g->weight, g->h, g->ldh, g->y, g->ldy, g->scale, g->rstd, g->eps,
+                          g->dtype, e4m3 ? 1 : 0, g->weight_dtype == MT_DTYPE_F32 ? 1 : 0,
+                          bounds_record()};
+  if (mt::launch_rms_norm(a, info.sms, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return MT_ERR_LAUNCH;
+  }
+  return MT_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,167 @@
+"""Binding of the feed-forward operators (include/mt_layers.h).
+
+``rms_norm`` on torch CUDA tensors, and the C entry points under their own
+names taking a filled argument structure.  Marshalling only, as in the
+package's ``__init__``, which re-exports everything here.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+_I64, _I32, _P, _F = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
+
+MT_DTYPE_F32 = 3
+MT_DTYPE_E4M3 = 4
+MT_E4M3_MAX = 448.0
+MT_SCALE_MIN = 2.0 ** -126
+
+
+class mt_rms_norm_args(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("d", _I64), ("x", _P), ("ldx", _I64), ("residual", _P),
+                ("ldr", _I64), ("weight", _P), ("h", _P), ("ldh", _I64), ("y", _P),
+                ("ldy", _I64), ("scale", _P), ("rstd", _P), ("eps", _F), ("dtype", _I32),
+                ("out_dtype", _I32), ("weight_dtype", _I32)]
+
+
+# name -> (restype, argtypes): every function include/mt_layers.h declares.
+# The argument structure is passed as its bytes or by reference.
+SIGNATURES = {
+    "mt_rms_norm": (ctypes.c_int, [_P, _P]),
+}
+
+
+def _packer(cls):
+    """struct.Struct.pack with the layout of a ctypes structure: one call
+    fills every field (None is not taken: NULL is 0)."""
+    code = {_I64: "q", _I32: "i", _P: "Q", _F: "f"}
+    s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_))
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_rms_norm = _packer(mt_rms_norm_args)
+
+
+# --- the C entry points, same names -----------------------------------------
+def mt_rms_norm(args: mt_rms_norm_args, stream: int = 0) -> int:
+    from . import lib
+    return lib().mt_rms_norm(ctypes.byref(args), stream)
+
+
+# --- torch convenience (marshalling only) ------------------------------------
+_codes = {}
+
+
+def _dtype_codes():
+    if not _codes:
+        import torch
+        _codes.update({torch.float16: 1, torch.bfloat16: 2, torch.float32: MT_DTYPE_F32,
+                       torch.float8_e4m3fn: MT_DTYPE_E4M3})
+    return _codes
+
+
+def _matrix(t, name, rows, cols, dtype, device):
+    """(pointer, row pitch) of a rows x cols CUDA matrix with unit column
+    stride; any pitch that holds a row serves a single row."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows <= 1 or ld < 1:
+        if rows > 1:
+            raise ValueError(f"{name}'s rows overlap")
+        ld = max(cols, 1)
+    return t.data_ptr(), ld
+
+
+def _vector(t, name, n, dtypes, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a {' or '.join(map(str, dtypes))} CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+    return t.data_ptr()
+
+
+def _first(t, name, dtypes):
+    """Checks of the operand whose device and type the others follow."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+
+
+def _call(fn, packed, device, stream):
+    """Runs one packed C call on the operands' device and stream."""
+    import torch
+    from . import MT_OK, MtError, lib
+    s = stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
+    f = getattr(lib(), fn)
+    if device.index == torch.cuda.current_device():
+        st = f(packed, s)
+    else:
+        with torch.cuda.device(device):
+            st = f(packed, s)
+    if st != MT_OK:
+        raise MtError(st, fn)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, out=None, h_out=None,
+             stream=None):
+    """Root-mean-square norm of h = x + residual over the last dimension,
+    times ``weight``, through mt_rms_norm.
+
+    x, residual: 2-D CUDA tensors of one dtype (float16, bfloat16 or
+    float32), rows may be strided; weight: a vector in that dtype or float32
+    (None: ones).  Returns ``(y, h, rstd)``; with ``out_dtype=
+    torch.float8_e4m3fn`` ``(q, scale, h, rstd)``: 8-bit rows with one
+    float32 scale each, y = q * scale.  h is x + residual in x's dtype (x
+    itself when there is no residual), rstd the float32 reciprocal norms
+    that ``rms_norm_backward`` takes.  ``out`` and ``h_out`` receive y (or q)
+    and h when given; h_out may be residual or x."""
+    import torch
+    codes = _dtype_codes()
+    _first(x, "x", (torch.float16, torch.bfloat16, torch.float32))
+    rows, d = x.shape
+    dt, dev = x.dtype, x.device
+    e4m3 = out_dtype == torch.float8_e4m3fn
+    if out_dtype is None:
+        out_dtype = dt
+    elif not e4m3 and out_dtype != dt:
+        raise TypeError("out_dtype must be x's dtype or torch.float8_e4m3fn")
+    xp, ldx = _matrix(x, "x", rows, d, dt, dev)
+    rp = ldr = hp = ldh = wp = sp = wcode = 0
+    if weight is not None:
+        wp = _vector(weight, "weight", d, (dt, torch.float32), dev)
+        wcode = codes[weight.dtype]
+    h = x
+    if residual is not None:
+        rp, ldr = _matrix(residual, "residual", rows, d, dt, dev)
+        h = torch.empty((rows, d), dtype=dt, device=dev) if h_out is None else h_out
+        hp, ldh = _matrix(h, "h_out", rows, d, dt, dev)
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual")
+    y = torch.empty((rows, d), dtype=out_dtype, device=dev) if out is None else out
+    yp, ldy = _matrix(y, "out", rows, d, out_dtype, dev)
+    # One allocation: the reciprocal norms, then the scales.
+    stats = torch.empty((2 if e4m3 else 1, rows), dtype=torch.float32, device=dev)
+    rstd = stats[0]
+    if e4m3:
+        scale = stats[1]
+        sp = scale.data_ptr()
+    _call("mt_rms_norm",
+          _pack_rms_norm(rows, d, xp, ldx, rp, ldr, wp, hp, ldh, yp, ldy, sp, rstd.data_ptr(),
+                         eps, codes[dt], codes[out_dtype], wcode), dev, stream)
+    return (y, scale, h, rstd) if e4m3 else (y, h, rstd)
