@@ -79,6 +79,42 @@ typedef struct {
  */
 MT_API mt_status mt_rms_norm(const mt_rms_norm_args *args, cudaStream_t stream);
 
+/*
+ * The gradient of mt_rms_norm: with xhat = h * rstd and g = dy * weight,
+ *
+ *     dx[i][k]   = rstd[i] * (g[i][k] - xhat[i][k] * mean_k(g[i] * xhat[i])) + dh[i][k]
+ *     dweight[k] = sum_i dy[i][k] * xhat[i][k]
+ *
+ * dy is the gradient of y (of the 8-bit y as if it were not rounded), dh the
+ * gradient that reaches h directly (the residual stream; NULL: none).  dx is
+ * the gradient of x and of the residual alike.  h and rstd are the forward
+ * call's (h: x itself where there was no residual).  dweight: d floats, each
+ * a sum over the rows in a fixed order (the same call gives the same bits);
+ * NULL: not computed.
+ */
+typedef struct {
+    int64_t rows, d;
+    const void *dy;
+    int64_t lddy;
+    const void *h;
+    int64_t ldh;
+    const void *weight;   /* NULL: ones */
+    const float *rstd;
+    const void *dh;
+    int64_t lddh;
+    void *dx;
+    int64_t lddx;
+    float *dweight;
+    int32_t dtype;        /* dy, h, dh, dx: MT_DTYPE_F16, _BF16 or _F32 */
+    int32_t weight_dtype; /* dtype or MT_DTYPE_F32 */
+} mt_rms_norm_backward_args;
+
+/* dx may be dy or dh itself (same pointer and pitch); any other overlap of an
+ * output is MT_ERR_ALIAS.  rows == 0 writes zeros to dweight.  Other errors
+ * as mt_rms_norm, and MT_ERR_CUDA when scratch cannot be allocated. */
+MT_API mt_status mt_rms_norm_backward(const mt_rms_norm_backward_args *args,
+                                      cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

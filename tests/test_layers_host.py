@@ -21,6 +21,9 @@ def built_library():
     return mt.lib()
 
 
+CLASSES = (mt.mt_rms_norm_args, mt.mt_rms_norm_backward_args)
+
+
 def norm_args(**change):
     a = mt.mt_rms_norm_args(rows=4, d=16, x=0x10000, ldx=16, residual=0x20000, ldr=16,
                             weight=0x30000, h=0x40000, ldh=16, y=0x50000, ldy=16, scale=None,
@@ -70,10 +73,43 @@ def test_norm_of_no_rows_is_nothing():
     assert mt.mt_rms_norm(norm_args(rows=0)) == mt.MT_OK
 
 
+def norm_grad_args(**change):
+    a = mt.mt_rms_norm_backward_args(rows=4, d=16, dy=0x10000, lddy=16, h=0x20000, ldh=16,
+                                     weight=0x30000, rstd=0x40000, dh=0x50000, lddh=16,
+                                     dx=0x60000, lddx=16, dweight=0x70000,
+                                     dtype=mt.MT_DTYPE_F16, weight_dtype=mt.MT_DTYPE_F16)
+    for k, v in change.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("change", [
+    dict(rows=-1), dict(d=1 << 31), dict(dy=None), dict(h=None), dict(rstd=None), dict(dx=None),
+    dict(lddy=15), dict(ldh=1), dict(lddh=0), dict(lddx=15), dict(dtype=mt.MT_DTYPE_E4M3),
+    dict(weight_dtype=mt.MT_DTYPE_BF16), dict(dweight=0x70002), dict(dx=0x60001)])
+def test_norm_backward_refuses_invalid_arguments(change):
+    assert mt.mt_rms_norm_backward(norm_grad_args(**change)) == mt.MT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [
+    dict(dx=0x10002), dict(dx=0x50000, lddx=32), dict(dx=0x20000), dict(dx=0x30000),
+    dict(dx=0x40000), dict(dweight=0x60000), dict(dweight=0x10004), dict(dweight=0x20000),
+    dict(dweight=0x30000), dict(dweight=0x40000), dict(dweight=0x50000)])
+def test_norm_backward_refuses_overlap(change):
+    assert mt.mt_rms_norm_backward(norm_grad_args(**change)) == mt.MT_ERR_ALIAS
+
+
+@pytest.mark.skipif(HAS_GPU, reason="made-up addresses")
+@pytest.mark.parametrize("change", [dict(), dict(dx=0x10000), dict(dx=0x50000), dict(dh=None),
+                                    dict(weight=None, dweight=None), dict(rows=0)])
+def test_norm_backward_without_a_device(change):
+    assert mt.mt_rms_norm_backward(norm_grad_args(**change)) == mt.MT_ERR_NO_DEVICE
+
+
 def test_packed_arguments_match_the_structure():
     """The binding's one-call packing lays the fields out as the structure."""
     from tiled_fp32_gemm_gb300 import layers
-    for cls in (mt.mt_rms_norm_args,):
+    for cls in CLASSES:
         values = [i + 1 for i in range(len(cls._fields_))]
         a = cls.from_buffer_copy(layers._packer(cls)(*values))
         for (name, _), v in zip(cls._fields_, values):
@@ -90,9 +126,8 @@ def test_arguments_have_the_c_layout(tmp_path):
         pytest.skip("no C compiler")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     cuda = os.path.join(os.path.dirname(os.path.dirname(mt_build.nvcc())), "include")
-    classes = (mt.mt_rms_norm_args,)
     lines, want = [], []
-    for cls in classes:
+    for cls in CLASSES:
         n = cls.__name__
         lines.append(f'printf("%zu\\n", sizeof({n}));')
         want.append(ctypes.sizeof(cls))

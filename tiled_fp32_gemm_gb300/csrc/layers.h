@@ -39,4 +39,89 @@ struct RmsNormArgs {
 
 cudaError_t launch_rms_norm(const RmsNormArgs& a, int sms, cudaStream_t stream);
 
+// rms_norm_grad.cu.  See mt_rms_norm_backward_args for the operator.
+struct RmsNormGradArgs {
+  int64_t rows;
+  int d;
+  const void* dy;
+  int64_t lddy;
+  const void* h;
+  int64_t ldh;
+  const void* weight;
+  const float* rstd;
+  const void* dh;
+  int64_t lddh;
+  void* dx;
+  int64_t lddx;
+  float* dweight;
+  int dtype;
+  int weight_f32;
+  BoundsRecord* bounds;
+};
+
+// Scratch bytes of a call, and the call (workspace of that many bytes).
+int64_t rms_norm_grad_workspace(const RmsNormGradArgs& a, int sms);
+cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, void* workspace, int sms,
+                                 cudaStream_t stream);
+
+// Adds `count` rows of `cols` floats (packed, in row order) to out[cols].
+cudaError_t launch_add_rows(const float* rows, int count, int cols, float* out,
+                            cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// The fused product of the linear layer and of its gradient:
+//
+//   z[t][c] = row_scale[t] * col_scale[c] * sum_k X[t][k] * W[k][c] + bias[c]
+//   Y[t][c] = act(z[t][c]) + residual[t][c],  Z[t][c] = z[t][c] (optional)
+//
+// X: T x K, stored K-contiguous, or T-contiguous (K x T) when x_mn.  W: K x C,
+// stored K-contiguous (C x K), or C-contiguous (K x C) when w_mn.  On the
+// tensor cores the columns of Y are the MMA's 128 lanes and its rows the
+// accumulator's columns, so a warp holds 32 consecutive columns of a row of Y
+// and its loads and stores are coalesced whatever the row pitch.
+enum Activation { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+struct LinearArgs {
+  int64_t T, C, K;
+  const void* X;
+  int64_t ldx;
+  const void* W;
+  int64_t ldw;
+  int x_mn, w_mn;
+  void* Y;
+  int64_t ldy;
+  void* Z;
+  int64_t ldz;
+  const void* residual;
+  int64_t ldr;
+  const float* bias;
+  const float* row_scale;
+  const float* col_scale;
+  int dtype;      // X and W: DT_F16, DT_BF16 or DT_E4M3 (then both K-contiguous)
+  int out_dtype;  // Y, Z, residual: DT_F16, DT_BF16 or DT_F32
+  int act;
+  BoundsRecord* bounds;
+};
+
+// What a product launches.  pair = 0: CTA tiles of 128 columns x bt rows of Y
+// (linear_split.cu), each computed by a cluster of `split` CTAs that take a
+// slice of K each and add their sums through distributed shared memory.
+struct LinearPlan {
+  int pair;
+  int bt;
+  int split;
+  int stages;
+  int64_t smem_bytes;
+  int64_t grid;
+  int64_t copy_x_bytes, copy_w_bytes;  // padded copies of operands TMA cannot read
+  int64_t workspace_bytes;
+};
+
+LinearPlan plan_linear(const LinearArgs& a, int sms, int pair_clusters);
+// Shared-memory limits of the kernels, once per device.
+cudaError_t linear_prepare();
+cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
+                          cudaStream_t stream, int fault_inject = 0);
+cudaError_t linear_read_and_clear_status(unsigned int* status);
+
 }  // namespace mt

@@ -38,6 +38,31 @@ struct View {
   bool hits(const View& o) const { return overlaps(p, bytes(), o.p, o.bytes()); }
 };
 
+// Scratch from the device's pool for one call; freed on the call's stream.
+struct Scratch {
+  void* p = nullptr;
+  cudaStream_t stream;
+
+  explicit Scratch(cudaStream_t s) : stream(s) {}
+  Scratch(const Scratch&) = delete;
+  Scratch& operator=(const Scratch&) = delete;
+  ~Scratch() {
+    if (p) cudaFreeAsync(p, stream);
+  }
+  mt_status get(int dev, int64_t bytes) {
+    if (bytes <= 0) return MT_OK;
+    cudaMemPool_t pool = nullptr;
+    const mt_status st = pool_for(dev, &pool);
+    if (st != MT_OK) return st;
+    if (cudaMallocFromPoolAsync(&p, static_cast<size_t>(bytes), pool, stream) != cudaSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+      return MT_ERR_CUDA;
+    }
+    return MT_OK;
+  }
+};
+
 bool half_type(int t) { return t == MT_DTYPE_F16 || t == MT_DTYPE_BF16; }
 
 }  // namespace
@@ -82,6 +107,44 @@ mt_status mt_rms_norm(const mt_rms_norm_args* g, cudaStream_t stream) {
                           g->dtype, e4m3 ? 1 : 0, g->weight_dtype == MT_DTYPE_F32 ? 1 : 0,
                           bounds_record()};
   if (mt::launch_rms_norm(a, info.sms, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return MT_ERR_LAUNCH;
+  }
+  return MT_OK;
+}
+
+mt_status mt_rms_norm_backward(const mt_rms_norm_backward_args* g, cudaStream_t stream) {
+  if (!g || g->rows < 0 || g->d < 0 || g->d > INT32_MAX || g->rows > INT32_MAX)
+    return MT_ERR_INVALID_ARG;
+  if (!half_type(g->dtype) && g->dtype != MT_DTYPE_F32) return MT_ERR_INVALID_ARG;
+  if (g->weight && g->weight_dtype != g->dtype && g->weight_dtype != MT_DTYPE_F32)
+    return MT_ERR_INVALID_ARG;
+  const int e = mt::dtype_bytes(g->dtype);
+  const int64_t rows = g->rows, d = g->d;
+  const View dy{g->dy, rows, d, g->lddy, e}, h{g->h, rows, d, g->ldh, e};
+  const View w{g->weight, g->weight ? 1 : 0, d, INT32_MAX, mt::dtype_bytes(g->weight_dtype)};
+  const View rstd{g->rstd, rows, 1, 1, 4};
+  const View dh{g->dh, g->dh ? rows : 0, d, g->dh ? g->lddh : INT32_MAX, e};
+  const View dx{g->dx, rows, d, g->lddx, e};
+  const View dw{g->dweight, g->dweight ? 1 : 0, d, INT32_MAX, 4};
+  for (const View* v : {&dy, &h, &w, &rstd, &dh, &dx, &dw})
+    if (!v->valid()) return MT_ERR_INVALID_ARG;
+  if ((dx.hits(dy) && !dx.same(dy)) || (dx.hits(dh) && !dx.same(dh))) return MT_ERR_ALIAS;
+  for (const View* v : {&h, &w, &rstd})
+    if (v->hits(dx) || v->hits(dw)) return MT_ERR_ALIAS;
+  if (dw.hits(dx) || dw.hits(dy) || dw.hits(dh)) return MT_ERR_ALIAS;
+  if (d == 0 || (rows == 0 && !g->dweight)) return MT_OK;
+  int dev = 0;
+  DeviceInfo info;
+  mt_status st = current_device(&dev, &info);
+  if (st != MT_OK) return st;
+  const mt::RmsNormGradArgs a{rows, static_cast<int>(d), g->dy, g->lddy, g->h, g->ldh, g->weight,
+                              g->rstd, g->dh, g->lddh, g->dx, g->lddx, g->dweight, g->dtype,
+                              g->weight_dtype == MT_DTYPE_F32 ? 1 : 0, bounds_record()};
+  Scratch ws(stream);
+  st = ws.get(dev, mt::rms_norm_grad_workspace(a, info.sms));
+  if (st != MT_OK) return st;
+  if (mt::launch_rms_norm_grad(a, ws.p, info.sms, stream) != cudaSuccess) {
     cudaGetLastError();
     return MT_ERR_LAUNCH;
   }

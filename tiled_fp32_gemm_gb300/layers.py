@@ -1,6 +1,6 @@
 """Binding of the feed-forward operators (include/mt_layers.h).
 
-``rms_norm`` on torch CUDA tensors, and the C entry points under their own
+``rms_norm`` and ``rms_norm_backward`` on torch CUDA tensors, and the C entry points under their own
 names taking a filled argument structure.  Marshalling only, as in the
 package's ``__init__``, which re-exports everything here.
 """
@@ -24,10 +24,18 @@ class mt_rms_norm_args(ctypes.Structure):
                 ("out_dtype", _I32), ("weight_dtype", _I32)]
 
 
+class mt_rms_norm_backward_args(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("d", _I64), ("dy", _P), ("lddy", _I64), ("h", _P),
+                ("ldh", _I64), ("weight", _P), ("rstd", _P), ("dh", _P), ("lddh", _I64),
+                ("dx", _P), ("lddx", _I64), ("dweight", _P), ("dtype", _I32),
+                ("weight_dtype", _I32)]
+
+
 # name -> (restype, argtypes): every function include/mt_layers.h declares.
 # The argument structure is passed as its bytes or by reference.
 SIGNATURES = {
     "mt_rms_norm": (ctypes.c_int, [_P, _P]),
+    "mt_rms_norm_backward": (ctypes.c_int, [_P, _P]),
 }
 
 
@@ -41,12 +49,18 @@ def _packer(cls):
 
 
 _pack_rms_norm = _packer(mt_rms_norm_args)
+_pack_rms_norm_backward = _packer(mt_rms_norm_backward_args)
 
 
 # --- the C entry points, same names -----------------------------------------
 def mt_rms_norm(args: mt_rms_norm_args, stream: int = 0) -> int:
     from . import lib
     return lib().mt_rms_norm(ctypes.byref(args), stream)
+
+
+def mt_rms_norm_backward(args: mt_rms_norm_backward_args, stream: int = 0) -> int:
+    from . import lib
+    return lib().mt_rms_norm_backward(ctypes.byref(args), stream)
 
 
 # --- torch convenience (marshalling only) ------------------------------------
@@ -165,3 +179,38 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, out=None, h_out
           _pack_rms_norm(rows, d, xp, ldx, rp, ldr, wp, hp, ldh, yp, ldy, sp, rstd.data_ptr(),
                          eps, codes[dt], codes[out_dtype], wcode), dev, stream)
     return (y, scale, h, rstd) if e4m3 else (y, h, rstd)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dh=None, need_weight=True, out=None, stream=None):
+    """``(dx, dweight)``: the gradient of ``rms_norm`` through
+    mt_rms_norm_backward.
+
+    dy: gradient of y; h and rstd: the forward call's; dh: the gradient that
+    reaches h directly (the residual stream), added to dx.  dx, in dy's
+    dtype, is the gradient of x and of the residual alike; dweight is
+    float32 (None when ``need_weight`` is false).  ``out`` receives dx when
+    given and may be dy or dh."""
+    import torch
+    codes = _dtype_codes()
+    _first(dy, "dy", (torch.float16, torch.bfloat16, torch.float32))
+    rows, d = dy.shape
+    dt, dev = dy.dtype, dy.device
+    dyp, lddy = _matrix(dy, "dy", rows, d, dt, dev)
+    hp, ldh = _matrix(h, "h", rows, d, dt, dev)
+    rp = _vector(rstd, "rstd", rows, (torch.float32,), dev)
+    wp = wcode = dhp = lddh = dwp = 0
+    if weight is not None:
+        wp = _vector(weight, "weight", d, (dt, torch.float32), dev)
+        wcode = codes[weight.dtype]
+    if dh is not None:
+        dhp, lddh = _matrix(dh, "dh", rows, d, dt, dev)
+    dx = torch.empty((rows, d), dtype=dt, device=dev) if out is None else out
+    dxp, lddx = _matrix(dx, "out", rows, d, dt, dev)
+    dweight = None
+    if need_weight:
+        dweight = torch.empty(d, dtype=torch.float32, device=dev)
+        dwp = dweight.data_ptr()
+    _call("mt_rms_norm_backward",
+          _pack_rms_norm_backward(rows, d, dyp, lddy, hp, ldh, wp, rp, dhp, lddh, dxp, lddx, dwp,
+                                  codes[dt], wcode), dev, stream)
+    return dx, dweight
