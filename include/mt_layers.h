@@ -115,6 +115,81 @@ typedef struct {
 MT_API mt_status mt_rms_norm_backward(const mt_rms_norm_backward_args *args,
                                       cudaStream_t stream);
 
+/* Activations of mt_linear, in fp32: identity, max(z, 0) (a NaN stays one),
+ * z * Phi(z) with the normal distribution's Phi (by erf), its tanh form
+ * z / 2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))), z / (1 + exp(-z)). */
+typedef enum {
+    MT_ACT_NONE = 0,
+    MT_ACT_RELU = 1,
+    MT_ACT_GELU = 2,
+    MT_ACT_GELU_TANH = 3,
+    MT_ACT_SILU = 4
+} mt_activation;
+
+/*
+ * The product with bias, activation and residual in its epilogue:
+ *
+ *     z[i][j] = (scale_a[i] * scale_b[j] *) sum_k A[i][k] * B[k][j]  + bias[j]
+ *     Y[i][j] = act(z[i][j]) + residual[i][j]
+ *
+ * A is M x K, B is K x N (B[k*ldb + j]) or, with trans_b, stored N x K
+ * (B[j*ldb + k]); bias, residual and Z may be NULL.  Z receives z (the
+ * pre-activation, which the gradient of an activation needs).  A and B hold
+ * 16-bit values (both the same type, no scales), or e4m3 values with fp32
+ * scales for every row of A and every column of B (trans_b only: both
+ * operands K-contiguous, as mt_rms_norm writes its 8-bit rows).  Products
+ * and sums are fp32 on the tensor cores; Y, Z and residual have out_dtype.
+ */
+typedef struct {
+    int64_t M, N, K;
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb;
+    void *Y;
+    int64_t ldy;
+    void *Z;
+    int64_t ldz;
+    const void *residual;
+    int64_t ldr;
+    const float *bias;     /* N floats */
+    const float *scale_a;  /* M floats; e4m3 only */
+    const float *scale_b;  /* N floats; e4m3 only */
+    int32_t trans_b;       /* 0 or 1 */
+    int32_t dtype;         /* A, B: MT_DTYPE_F16, _BF16 or _E4M3 */
+    int32_t out_dtype;     /* Y, Z, residual: dtype or MT_DTYPE_F32; for e4m3
+                              inputs MT_DTYPE_F16, _BF16 or _F32 */
+    int32_t activation;    /* mt_activation */
+    int32_t fault_inject;  /* test hook, 0 = off: 1 = the copy threads issue
+                              nothing, so the waits on their data run out, Y is
+                              left unwritten and mt_check_device_status returns
+                              MT_ERR_TIMEOUT */
+    int32_t reserved;      /* 0 */
+} mt_linear_args;
+
+/*
+ * M or N == 0 does nothing; K == 0 gives act(bias) + residual.  residual may
+ * be Y itself (same pointer and pitch); any other overlap of Y or Z with an
+ * operand or with each other is MT_ERR_ALIAS.  TMA reads A and B in place
+ * when their base is 16-byte aligned and their row pitch a multiple of 16
+ * bytes; otherwise the call first copies them into padded scratch.  Nothing
+ * depends on the alignment of the other operands.  Errors as mt_rms_norm,
+ * MT_ERR_UNSUPPORTED for more than 2^31 - 1 tiles, and MT_ERR_CUDA when the
+ * driver's tensor-map encoder cannot be found or scratch cannot be
+ * allocated.
+ */
+MT_API mt_status mt_linear(const mt_linear_args *args, cudaStream_t stream);
+
+/*
+ * The launch mt_linear would make for these arguments on a GPU with `sms`
+ * SMs, without launching anything (pointers are inspected for alignment
+ * only and may be NULL).  bm: rows of Y per tile, bn: columns; split_k:
+ * CTAs that share a tile's K; vec_ab: 1 when A and B are read in place;
+ * workspace_bytes: the scratch for their copies.  Fields that describe other
+ * kernels are 0.
+ */
+MT_API mt_status mt_linear_plan(const mt_linear_args *args, int sms, mt_plan *out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,7 +21,7 @@ def built_library():
     return mt.lib()
 
 
-CLASSES = (mt.mt_rms_norm_args, mt.mt_rms_norm_backward_args)
+CLASSES = (mt.mt_rms_norm_args, mt.mt_rms_norm_backward_args, mt.mt_linear_args)
 
 
 def norm_args(**change):
@@ -104,6 +104,94 @@ def test_norm_backward_refuses_overlap(change):
                                     dict(weight=None, dweight=None), dict(rows=0)])
 def test_norm_backward_without_a_device(change):
     assert mt.mt_rms_norm_backward(norm_grad_args(**change)) == mt.MT_ERR_NO_DEVICE
+
+
+def linear_args(**change):
+    a = mt.mt_linear_args(M=4, N=16, K=32, A=0x10000, lda=32, B=0x20000, ldb=16, Y=0x30000,
+                          ldy=16, Z=0x40000, ldz=16, residual=0x50000, ldr=16, bias=0x60000,
+                          dtype=mt.MT_DTYPE_BF16, out_dtype=mt.MT_DTYPE_BF16,
+                          activation=mt.MT_ACT_SILU)
+    for k, v in change.items():
+        setattr(a, k, v)
+    return a
+
+
+E4M3 = dict(dtype=mt.MT_DTYPE_E4M3, trans_b=1, ldb=32, scale_a=0x70000, scale_b=0x80000)
+
+
+@pytest.mark.parametrize("change", [
+    dict(M=-1), dict(N=-1), dict(K=-1), dict(M=1 << 31), dict(A=None), dict(B=None),
+    dict(Y=None), dict(lda=31), dict(ldb=15), dict(trans_b=1), dict(trans_b=2), dict(ldy=15),
+    dict(ldz=15), dict(ldr=15), dict(dtype=mt.MT_DTYPE_F32), dict(dtype=0),
+    dict(out_dtype=mt.MT_DTYPE_F16), dict(out_dtype=mt.MT_DTYPE_E4M3), dict(activation=5),
+    dict(activation=-1), dict(bias=0x60002), dict(A=0x10001), dict(Y=0x30001),
+    dict(scale_a=0x70000), dict(reserved=1), dict(fault_inject=2),
+    {**E4M3, "trans_b": 0}, {**E4M3, "scale_a": None}, {**E4M3, "scale_b": None},
+    {**E4M3, "scale_b": 0x80002}, {**E4M3, "out_dtype": mt.MT_DTYPE_E4M3}])
+def test_linear_refuses_invalid_arguments(change):
+    assert mt.mt_linear(linear_args(**change)) == mt.MT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [
+    dict(Y=0x10000), dict(Y=0x20010), dict(Y=0x50002), dict(Y=0x50000, ldy=32), dict(Y=0x40000),
+    dict(Y=0x60000), dict(Z=0x50000), dict(Z=0x10000), dict(Z=0x20000), dict(Z=0x60000),
+    {**E4M3, "Y": 0x70000}, {**E4M3, "Z": 0x80000}])
+def test_linear_refuses_overlap(change):
+    assert mt.mt_linear(linear_args(**change)) == mt.MT_ERR_ALIAS
+
+
+@pytest.mark.skipif(HAS_GPU, reason="made-up addresses")
+@pytest.mark.parametrize("change", [dict(), dict(Y=0x50000), dict(Z=None, residual=None, bias=None),
+                                    dict(K=0, A=None, B=None), dict(trans_b=1, ldb=32),
+                                    dict(out_dtype=mt.MT_DTYPE_F32), E4M3,
+                                    {**E4M3, "A": 0x10001, "lda": 33}])
+def test_linear_without_a_device(change):
+    assert mt.mt_linear(linear_args(**change)) == mt.MT_ERR_NO_DEVICE
+
+
+@pytest.mark.parametrize("change", [dict(M=0), dict(N=0)])
+def test_linear_of_nothing(change):
+    assert mt.mt_linear(linear_args(**change)) == mt.MT_OK
+
+
+def linear_plan(M, N, K, sms=152, **change):
+    trans = change.get("trans_b", 0)
+    a = linear_args(M=M, N=N, K=K, lda=max(K, 1), ldb=max(K if trans else N, 1), ldy=N, ldz=N,
+                    ldr=N)
+    for k, v in change.items():
+        setattr(a, k, v)
+    st, p = mt.mt_linear_plan(a, sms)
+    assert st == mt.MT_OK
+    return p.as_dict()
+
+
+def test_linear_plans_cover_the_product():
+    """Whatever the sizes: the tiles cover Y, slices of K are no more than
+    its K tiles and no more than a cluster holds, shared memory fits."""
+    for M in (1, 15, 16, 17, 33, 64, 65, 128, 129, 500, 4096, 8192):
+        for N in (1, 127, 128, 129, 4096, 11000):
+            for K in (0, 1, 64, 65, 1000, 8192):
+                for change in (dict(), dict(trans_b=1), E4M3):
+                    p = linear_plan(M, N, K, **{**change, "ldb": max(N, K, 1)})
+                    tiles = -(-M // p["bm"]) * -(-N // p["bn"])
+                    if p["bn"] == 128:
+                        assert p["grid"] == tiles * p["split_k"]
+                    assert 1 <= p["split_k"] <= max(1, min(8, -(-K // p["bk"])))
+                    assert p["smem_bytes"] <= 227 * 1024
+
+
+def test_linear_plan_reports_copies():
+    """Rows TMA cannot read in place are copied into rows of whole 128-byte
+    lines: 16-byte bases and pitches are read in place."""
+    assert linear_plan(64, 64, 64)["workspace_bytes"] == 0
+    p = linear_plan(64, 64, 65, lda=65)      # A's rows are 130 bytes
+    assert p["vec_ab"] == 0 and p["workspace_bytes"] == 64 * 256
+    p = linear_plan(64, 64, 64, A=0x10002)
+    assert p["vec_ab"] == 0 and p["workspace_bytes"] == 64 * 128
+    p = linear_plan(64, 65, 64)              # B's rows are 130 bytes
+    assert p["workspace_bytes"] == 64 * 256
+    p = linear_plan(64, 64, 72, **{**E4M3, "lda": 72, "ldb": 72})
+    assert p["workspace_bytes"] == 2 * 64 * 128
 
 
 def test_packed_arguments_match_the_structure():

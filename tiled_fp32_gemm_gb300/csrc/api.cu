@@ -14,6 +14,7 @@
 #include "device_util.cuh"
 #include "host.h"
 #include "kernels.h"
+#include "layers.h"
 #include "mt_sgemm.h"
 #include "smem_layout.cuh"
 
@@ -1523,13 +1524,14 @@ mt_status mt_check_device_status(cudaStream_t stream) {
     cudaGetLastError();
     return MT_ERR_CUDA;
   }
-  unsigned int flags = 0, flags16 = 0;
+  unsigned int flags = 0, flags16 = 0, flags_linear = 0;
   if (mt::tf32x3_read_and_clear_status(&flags) != cudaSuccess ||
-      mt::f16tc_read_and_clear_status(&flags16) != cudaSuccess) {
+      mt::f16tc_read_and_clear_status(&flags16) != cudaSuccess ||
+      mt::linear_read_and_clear_status(&flags_linear) != cudaSuccess) {
     cudaGetLastError();
     return MT_ERR_CUDA;
   }
-  flags |= flags16;
+  flags |= flags16 | flags_linear;
   return flags ? MT_ERR_TIMEOUT : MT_OK;
 }
 

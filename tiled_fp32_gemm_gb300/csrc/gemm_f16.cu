@@ -46,6 +46,7 @@
 #include <cuda_runtime.h>
 
 #include "device_util.cuh"
+#include "gemm_f16.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
 
@@ -53,19 +54,6 @@ namespace mt {
 namespace f16tc {
 
 using namespace tc;
-
-constexpr int BM = 128;
-constexpr int BK = 64;            // 16-bit values of K per stage: one 128-byte row
-constexpr int ROW_BYTES = BK * 2;
-constexpr int ATOM_BYTES = 8 * ROW_BYTES;
-constexpr int MN_BOX = 64;        // M/N values per box of an MN-major operand
-constexpr int MN_BOX_BYTES = BK * MN_BOX * 2;
-constexpr uint64_t SWIZZLE_128B = 2;  // descriptor layout code
-constexpr int THREADS = 192;
-constexpr int EPILOGUE_THREADS = 128;
-constexpr int SMEM_STAGE_BUDGET = 200 * 1024;
-
-__device__ unsigned int g_status;  // bit 0: a bounded wait expired
 
 template <int BN_>
 struct Geometry {
@@ -81,28 +69,6 @@ struct Geometry {
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 /*alignment*/ + 256 +
                                    EPI_STAGE_BYTES;
 };
-
-// Loads the `rows`-row tile of one operand for K tile k0 into `dst`.
-template <int ROWS, bool MN>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int r0,
-                                             int k0, uint32_t bar) {
-  if constexpr (!MN) {
-    tma_load_2d(dst, map, k0, r0, bar);  // box: 64 k x ROWS rows
-  } else {
-#pragma unroll
-    for (int c = 0; c < ROWS / MN_BOX; ++c)  // boxes: 64 m/n x 64 k
-      tma_load_2d(dst + c * MN_BOX_BYTES, map, r0 + c * MN_BOX, k0, bar);
-  }
-}
-
-// Descriptor of k-step j (16 values of K) of an operand tile at `base`.
-template <bool MN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int j) {
-  if constexpr (!MN)
-    return smem_desc(base + j * 32, 16, ATOM_BYTES, SWIZZLE_128B);  // 16 values = 32 bytes
-  else
-    return smem_desc(base + j * 16 * ROW_BYTES, MN_BOX_BYTES, ATOM_BYTES, SWIZZLE_128B);
-}
 
 template <int BN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -251,206 +217,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// ---------------------------------------------------------------------------
-// CTA-pair kernel: a cluster of two CTAs on two SMs computes 256 x 256 tiles
-// with tcgen05.mma.cta_group::2.  CTA r (0 or 1) of the pair holds rows
-// m0 + 128 r .. +127 of A's tile and columns n0 + 128 r .. +127 of B's, so
-// each SM stages 32 KB per 64-deep K tile for a 128 x 256 share of the
-// product (a single-CTA 128 x 256 tile stages 48 KB for the same share).
-//   both CTAs, warp 0: TMA loads of the CTA's halves into its own ring; the
-//     bytes of both complete on the even CTA's full[s] (cta_group::2 copies),
-//     and only the even CTA arms it (expect_tx of both halves);
-//   even CTA, warp 1: per K tile 4 pair MMAs 256 x 256 x 16, then a commit
-//     multicast to empty[s] of both CTAs, and after a unit's last K tile to
-//     acc_full[b] of both;
-//   both CTAs, warps 2-5: drain their own TMEM half (128 rows x 256) to C,
-//     then one arrival per warp on the even CTA's acc_empty[b].
-// ACC_BUFS accumulators of 256 columns each (1 or 2) sit in TMEM.
-constexpr int PAIR_TILE = 256;
-constexpr int PAIR_HALF = 128;
-
-template <int ACC_BUFS_>
-struct PairGeometry {
-  static constexpr int ACC_BUFS = ACC_BUFS_;
-  static constexpr int A_BYTES = PAIR_HALF * ROW_BYTES;  // this CTA's half of A
-  static constexpr int B_BYTES = PAIR_HALF * ROW_BYTES;  // this CTA's half of B
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES_FIT = SMEM_STAGE_BUDGET / STAGE_BYTES;
-  static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
-  static constexpr uint32_t TMEM_COLS = ACC_BUFS * PAIR_TILE;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 /*alignment*/ + 256 +
-                                   EPI_STAGE_BYTES;
+// The pair kernel's drain of a tile of C: alpha, beta, bias and mask, or a
+// K slice's partial tile.
+struct CUpdate {
+  Epilogue ep;
+  __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int lane,
+                                             const Sched& sched, float* square,
+                                             int rank) const {
+    store_accumulator<PAIR_HALF, PAIR_TILE, PAIR_TILE>(t_row, w, q, lane, ep, sched.partial,
+                                                       square, rank * PAIR_HALF);
+  }
 };
-
-template <bool A_MN, bool B_MN, int ACC_BUFS>
-__global__ void __launch_bounds__(THREADS, 1)
-    f16tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                      const __grid_constant__ CUtensorMap tmap_b, uint32_t idesc, Epilogue ep,
-                      int Kt, int tiles_m, int tiles_n, int group_m, Sched sched,
-                      int fault_inject) {
-  using G = PairGeometry<ACC_BUFS>;
-  constexpr int STAGES = G::STAGES;
-  constexpr int STAGE_BYTES = G::STAGE_BYTES;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
-  // bars: [0, S) full (used on the even CTA), [S, 2S) empty, then
-  // acc_full[ACC_BUFS], acc_empty[ACC_BUFS] (used on the even CTA), drain.
-  constexpr int FULL = 0, EMPTY = STAGES, ACC_FULL = 2 * STAGES,
-                ACC_EMPTY = 2 * STAGES + ACC_BUFS, DRAIN = 2 * STAGES + 2 * ACC_BUFS,
-                NBARS = DRAIN + 1;
-  static_assert(NBARS * 8 + 8 <= 256, "barriers, TMEM slot and abort flag fit 256 bytes");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const WaitCtx wc{abort_flag, &g_status};
-  auto bar = [&](int i) { return smem_u32(bars + i); };
-
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank();  // 0: even (MMA issuer), 1: odd
-  const bool leader = rank == 0;
-  const int cluster = static_cast<int>(cluster_id_x());
-  const int clusters = static_cast<int>(cluster_count_x());
-  const int num_tiles = tiles_m * tiles_n;
-  const int num_units = units_of(cluster, clusters, sched, num_tiles, Kt);  // this cluster's units
-
-  if (threadIdx.x == 0) {
-    prefetch_tmap(&tmap_a);
-    prefetch_tmap(&tmap_b);
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(bar(FULL + s), 1);   // the even CTA's arrival + both CTAs' bytes
-      mbar_init(bar(EMPTY + s), 1);  // pair MMA commit
-    }
-    for (int b = 0; b < ACC_BUFS; ++b) {
-      mbar_init(bar(ACC_FULL + b), 1);   // pair MMA commit
-      mbar_init(bar(ACC_EMPTY + b), 8);  // one arrival per epilogue warp of both CTAs
-    }
-    mbar_init(bar(DRAIN), 1);
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), G::TMEM_COLS);
-  tc_fence_before();
-  cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  if (warp == 0) {
-    if (lane == 0) {
-      // Producer (both CTAs): this CTA's halves into its own stages.
-      bool stop = fault_inject != 0;
-      uint32_t g = 0;
-      for (int u = 0; u < num_units && !stop; ++u) {
-        const Unit w = unit_at(u, cluster, clusters, sched, tiles_m, tiles_n, group_m, Kt);
-        const int r0a = w.tm * PAIR_TILE + static_cast<int>(rank) * PAIR_HALF;
-        const int r0b = w.tn * PAIR_TILE + static_cast<int>(rank) * PAIR_HALF;
-        for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
-          const uint32_t s = g % STAGES, round = g / STAGES;
-          if (g >= STAGES && !wait_phase(bar(EMPTY + s), (round + 1) & 1u, wc)) {
-            stop = true;
-            break;
-          }
-          const uint32_t full_even = map_to_cta(bar(FULL + s), 0);
-          if (leader) mbar_arrive_expect_tx(bar(FULL + s), 2 * STAGE_BYTES);
-          const uint32_t st = smem_u32(smem + s * STAGE_BYTES);
-          const int k0 = kt * BK;
-          if constexpr (!A_MN) {
-            tma_load_2d_pair(st, &tmap_a, k0, r0a, full_even);
-          } else {
-            tma_load_2d_pair(st, &tmap_a, r0a, k0, full_even);
-            tma_load_2d_pair(st + MN_BOX_BYTES, &tmap_a, r0a + MN_BOX, k0, full_even);
-          }
-          const uint32_t sb = st + G::A_BYTES;
-          if constexpr (!B_MN) {
-            tma_load_2d_pair(sb, &tmap_b, k0, r0b, full_even);
-          } else {
-            tma_load_2d_pair(sb, &tmap_b, r0b, k0, full_even);
-            tma_load_2d_pair(sb + MN_BOX_BYTES, &tmap_b, r0b + MN_BOX, k0, full_even);
-          }
-        }
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // Pair MMA issuer (even CTA).
-      uint32_t g = 0;
-      bool stop = false;
-      int it = 0;
-      for (int u = 0; u < num_units && !stop; ++u, ++it) {
-        const Unit w = unit_at(u, cluster, clusters, sched, tiles_m, tiles_n, group_m, Kt);
-        const int b = it % ACC_BUFS, use = it / ACC_BUFS;
-        // Both CTAs' epilogues must have drained this accumulator.
-        if (use >= 1 && !wait_phase(bar(ACC_EMPTY + b), (use + 1) & 1u, wc)) break;
-        tc_fence_after();
-        const uint32_t acc_tmem = tmem + static_cast<uint32_t>(b * PAIR_TILE);
-        uint32_t acc = 0;
-        for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
-          const uint32_t s = g % STAGES, round = g / STAGES;
-          if (!wait_phase(bar(FULL + s), round & 1u, wc)) {
-            stop = true;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a_base = smem_u32(smem + s * STAGE_BYTES);
-          const uint32_t b_base = a_base + G::A_BYTES;
-#pragma unroll
-          for (int j = 0; j < BK / 16; ++j) {
-            mma_f16_pair(acc_tmem, operand_desc<A_MN>(a_base, j), operand_desc<B_MN>(b_base, j),
-                         idesc, acc);
-            acc = 1;
-          }
-          mma_commit_pair(bar(EMPTY + s), 0x3);
-        }
-        if (!stop) mma_commit_pair(bar(ACC_FULL + b), 0x3);
-      }
-      // Every pair MMA issued has retired once DRAIN completes.
-      mma_commit_pair(bar(DRAIN), 0x1);
-      wait_phase(bar(DRAIN), 0, wc, false);
-    }
-  } else {
-    // Epilogue warps of both CTAs: warp w may access TMEM lanes 32*(w%4)..+31.
-    const int q = warp & 3;
-    // This warp's staging square, past the barriers.
-    float* const epi_square =
-        reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES + 256) + q * EPI_WARP_FLOATS;
-    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t acc_empty_even = map_to_cta(bar(ACC_EMPTY), 0);
-    int it = 0;
-    for (int u = 0; u < num_units; ++u, ++it) {
-      const int b = it % ACC_BUFS, use = it / ACC_BUFS;
-      const bool ready = wait_phase(bar(ACC_FULL + b), use & 1u, wc, true,
-                                    TIMEOUT_NS + 20000ull * static_cast<uint64_t>(Kt));
-      if (!__all_sync(0xffffffffu, ready)) break;
-      tc_fence_after();
-      __syncwarp();
-      const Unit w = unit_at(u, cluster, clusters, sched, tiles_m, tiles_n, group_m, Kt);
-      store_accumulator<PAIR_HALF, PAIR_TILE, PAIR_TILE>(
-          tmem + lane_base + static_cast<uint32_t>(b * PAIR_TILE), w, q, lane, ep,
-          sched.partial, epi_square, static_cast<int>(rank) * PAIR_HALF);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_empty_even + 8u * static_cast<uint32_t>(b));
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (*abort_flag) {
-    // Copies this CTA issued complete on the even CTA's barriers, which it
-    // cannot wait on: give any still in flight time to land (bounded).
-    const uint64_t t0 = globaltimer();
-    while (globaltimer() - t0 < 200000ull) {
-    }
-  }
-  // The even CTA's MMAs (which read the odd CTA's shared memory) have
-  // retired and every cross-CTA arrival is done before either CTA leaves.
-  cluster_sync();
-  if (warp == 1) {
-    __syncwarp();
-    tc_fence_after();
-    tmem_dealloc_pair(tmem, G::TMEM_COLS);
-  }
-}
 
 // dst[r * ldd + c] = src[r * lds + c] for c < cols, 0 for cols <= c < ldd
 // (16-bit values; ldd % 8 == 0 and dst 16-byte aligned, one 16-byte store
@@ -618,7 +395,7 @@ struct CfgPair {
 
   template <bool A_MN, bool B_MN>
   static constexpr auto kernel() {
-    return f16tc::f16tc_pair_kernel<A_MN, B_MN, kPairAccBufs>;
+    return f16tc::pair_kernel<f16tc::Half, A_MN, B_MN, kPairAccBufs, f16tc::CUpdate>;
   }
 
   static const void* kernel_ptr(bool a_mn, bool b_mn) {
@@ -689,8 +466,8 @@ struct CfgPair {
       sched.partial = reinterpret_cast<float*>(ws + L.partial_offset);
     const int units = a.full_tiles + (tiles - a.full_tiles) * a.split;
     const int clusters = persistent_grid(a, units, max_clusters);
-    const tc::Epilogue ep =
-        tc::make_epilogue(a, vec_c, tiles, PAIR_TILE, PAIR_TILE, staged_epilogue(a, vec_c));
+    const f16tc::CUpdate drain{
+        tc::make_epilogue(a, vec_c, tiles, PAIR_TILE, PAIR_TILE, staged_epilogue(a, vec_c))};
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -699,13 +476,14 @@ struct CfgPair {
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     cfg.blockDim = dim3(f16tc::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = tc::epilogue_smem(G::SMEM_BYTES, ep);
+    cfg.dynamicSmemBytes = tc::epilogue_smem(G::SMEM_BYTES, drain.ep);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int group_m = a.group_m;
-    void* args[] = {&map_a, &map_b, const_cast<uint32_t*>(&idesc), const_cast<tc::Epilogue*>(&ep),
-                    const_cast<int*>(&kt), const_cast<int*>(&mt), const_cast<int*>(&nt),
+    void* args[] = {&map_a, &map_b, const_cast<uint32_t*>(&idesc),
+                    const_cast<f16tc::CUpdate*>(&drain), const_cast<int*>(&kt),
+                    const_cast<int*>(&mt), const_cast<int*>(&nt),
                     &group_m, &sched, const_cast<int*>(&fault_inject)};
     e = cudaLaunchKernelExC(&cfg, kernel_ptr(a_mn, b_mn), args);
     if (e != cudaSuccess) return e;

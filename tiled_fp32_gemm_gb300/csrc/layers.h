@@ -103,21 +103,17 @@ struct LinearArgs {
   BoundsRecord* bounds;
 };
 
-// What a product launches.  pair = 0: CTA tiles of 128 columns x bt rows of Y
-// (linear_split.cu), each computed by a cluster of `split` CTAs that take a
-// slice of K each and add their sums through distributed shared memory.
+// What a product launches (linear_split.cu): CTA tiles of bc = 128 columns x
+// bt rows of Y, each computed by a cluster of `split` CTAs that take a slice
+// of K each and add their sums through distributed shared memory.
 struct LinearPlan {
-  int pair;
-  int bt;
-  int split;
-  int stages;
-  int64_t smem_bytes;
-  int64_t grid;
+  int bt, bc, split, stages, threads;
+  int64_t smem_bytes, grid;
   int64_t copy_x_bytes, copy_w_bytes;  // padded copies of operands TMA cannot read
   int64_t workspace_bytes;
 };
 
-LinearPlan plan_linear(const LinearArgs& a, int sms, int pair_clusters);
+LinearPlan plan_linear(const LinearArgs& a, int sms);
 // Shared-memory limits of the kernels, once per device.
 cudaError_t linear_prepare();
 cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,

@@ -1,8 +1,11 @@
 // C entry points of the feed-forward operators (include/mt_layers.h):
 // argument checks, launch choices, scratch.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
+#include <mutex>
 
 #include <cuda_runtime.h>
 
@@ -17,6 +20,13 @@ using namespace mt::host;
 static_assert(MT_DTYPE_F16 == mt::DT_F16 && MT_DTYPE_BF16 == mt::DT_BF16 &&
                   MT_DTYPE_F32 == mt::DT_F32 && MT_DTYPE_E4M3 == mt::DT_E4M3,
               "storage type codes");
+static_assert(MT_ACT_RELU == mt::ACT_RELU && MT_ACT_GELU == mt::ACT_GELU &&
+                  MT_ACT_GELU_TANH == mt::ACT_GELU_TANH && MT_ACT_SILU == mt::ACT_SILU,
+              "activation codes");
+
+// Largest row, column or contraction count of a product: tile coordinates
+// past the edge stay inside 32 bits.
+constexpr int64_t kMaxSize = INT32_MAX - 255;
 
 // A rows x cols view of `elem`-byte values with row pitch ld, for the checks.
 struct View {
@@ -64,6 +74,58 @@ struct Scratch {
 };
 
 bool half_type(int t) { return t == MT_DTYPE_F16 || t == MT_DTYPE_BF16; }
+
+// The product an mt_linear call makes.
+mt::LinearArgs product_of(const mt_linear_args& g) {
+  mt::LinearArgs a{};
+  a.T = g.M;
+  a.C = g.N;
+  a.K = g.K;
+  a.X = g.A;
+  a.ldx = g.lda;
+  a.W = g.B;
+  a.ldw = g.ldb;
+  a.w_mn = g.trans_b ? 0 : 1;
+  a.Y = g.Y;
+  a.ldy = g.ldy;
+  a.Z = g.Z;
+  a.ldz = g.ldz;
+  a.residual = g.residual;
+  a.ldr = g.ldr;
+  a.bias = g.bias;
+  a.row_scale = g.scale_a;
+  a.col_scale = g.scale_b;
+  a.dtype = g.dtype;
+  a.out_dtype = g.out_dtype;
+  a.act = g.activation;
+  a.bounds = bounds_record();
+  return a;
+}
+
+bool linear_types_ok(const mt_linear_args& g) {
+  const bool e4m3 = g.dtype == MT_DTYPE_E4M3;
+  if (!half_type(g.dtype) && !e4m3) return false;
+  if (g.out_dtype != MT_DTYPE_F32 && (e4m3 ? !half_type(g.out_dtype) : g.out_dtype != g.dtype))
+    return false;
+  if (g.trans_b < 0 || g.trans_b > 1 || (e4m3 && !g.trans_b)) return false;
+  return g.activation >= MT_ACT_NONE && g.activation <= MT_ACT_SILU;
+}
+
+// The product kernels' shared-memory limits, set once per device.
+std::mutex g_linear_mutex;
+std::atomic<uint8_t> g_linear_ready[kMaxDevices];
+
+mt_status prepare_linear(int dev) {
+  if (!mt::tensor_map_encoder_available()) return MT_ERR_CUDA;
+  if (g_linear_ready[dev].load(std::memory_order_acquire)) return MT_OK;
+  std::lock_guard<std::mutex> lock(g_linear_mutex);
+  if (mt::linear_prepare() != cudaSuccess) {
+    cudaGetLastError();
+    return MT_ERR_LAUNCH;
+  }
+  g_linear_ready[dev].store(1, std::memory_order_release);
+  return MT_OK;
+}
 
 }  // namespace
 
@@ -148,6 +210,68 @@ mt_status mt_rms_norm_backward(const mt_rms_norm_backward_args* g, cudaStream_t 
     cudaGetLastError();
     return MT_ERR_LAUNCH;
   }
+  return MT_OK;
+}
+
+mt_status mt_linear(const mt_linear_args* g, cudaStream_t stream) {
+  if (!g || g->M < 0 || g->N < 0 || g->K < 0 || g->M > kMaxSize || g->N > kMaxSize ||
+      g->K > kMaxSize || g->reserved || g->fault_inject < 0 || g->fault_inject > 1 ||
+      !linear_types_ok(*g))
+    return MT_ERR_INVALID_ARG;
+  const bool e4m3 = g->dtype == MT_DTYPE_E4M3;
+  const int e = mt::dtype_bytes(g->dtype), eo = mt::dtype_bytes(g->out_dtype);
+  const int64_t M = g->M, N = g->N, K = g->K;
+  if (!e4m3 && (g->scale_a || g->scale_b)) return MT_ERR_INVALID_ARG;
+  const View A{g->A, M, K, g->lda, e};
+  const View B = g->trans_b ? View{g->B, N, K, g->ldb, e} : View{g->B, K, N, g->ldb, e};
+  const View Y{g->Y, M, N, g->ldy, eo};
+  const View Z{g->Z, g->Z ? M : 0, N, g->Z ? g->ldz : INT32_MAX, eo};
+  const View res{g->residual, g->residual ? M : 0, N, g->residual ? g->ldr : INT32_MAX, eo};
+  const View bias{g->bias, g->bias ? 1 : 0, N, INT32_MAX, 4};
+  const View sa{g->scale_a, e4m3 ? 1 : 0, M, INT32_MAX, 4};
+  const View sb{g->scale_b, e4m3 ? 1 : 0, N, INT32_MAX, 4};
+  for (const View* v : {&A, &B, &Y, &Z, &res, &bias, &sa, &sb})
+    if (!v->valid()) return MT_ERR_INVALID_ARG;
+  for (const View* v : {&A, &B, &bias, &sa, &sb})
+    if (Y.hits(*v) || Z.hits(*v)) return MT_ERR_ALIAS;
+  if ((Y.hits(res) && !Y.same(res)) || Z.hits(res) || Z.hits(Y)) return MT_ERR_ALIAS;
+  if (M == 0 || N == 0) return MT_OK;
+  int dev = 0;
+  DeviceInfo info;
+  mt_status st = current_device(&dev, &info);
+  if (st == MT_OK) st = prepare_linear(dev);
+  if (st != MT_OK) return st;
+  const mt::LinearArgs a = product_of(*g);
+  const mt::LinearPlan p = mt::plan_linear(a, info.sms);
+  if (p.grid > INT32_MAX) return MT_ERR_UNSUPPORTED;
+  Scratch ws(stream);
+  st = ws.get(dev, p.workspace_bytes);
+  if (st != MT_OK) return st;
+  if (mt::launch_linear(a, p, ws.p, stream, g->fault_inject) != cudaSuccess) {
+    cudaGetLastError();
+    return MT_ERR_LAUNCH;
+  }
+  return MT_OK;
+}
+
+mt_status mt_linear_plan(const mt_linear_args* g, int sms, mt_plan* out) {
+  if (!g || !out || sms < 1 || g->M < 1 || g->N < 1 || g->K < 0 || g->M > kMaxSize ||
+      g->N > kMaxSize || g->K > kMaxSize || !linear_types_ok(*g))
+    return MT_ERR_INVALID_ARG;
+  const mt::LinearPlan p = mt::plan_linear(product_of(*g), sms);
+  if (p.grid > INT32_MAX) return MT_ERR_UNSUPPORTED;
+  std::memset(out, 0, sizeof(*out));
+  out->variant = MT_VARIANT_TC16;
+  out->bm = p.bt;
+  out->bn = p.bc;
+  out->bk = 128 / mt::dtype_bytes(g->dtype);
+  out->stages = p.stages;
+  out->threads = p.threads;
+  out->vec_ab = p.workspace_bytes == 0;
+  out->split_k = p.split;
+  out->grid = p.grid;
+  out->smem_bytes = p.smem_bytes;
+  out->workspace_bytes = p.workspace_bytes;
   return MT_OK;
 }
 

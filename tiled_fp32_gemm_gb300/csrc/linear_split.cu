@@ -1,0 +1,442 @@
+// The fused linear layer on one CTA tile per cluster: 128 columns x BT rows
+// of Y, K cut into one slice per CTA of the cluster.
+//
+// The weight's columns are the MMA's M side (128 lanes of tensor memory), the
+// tokens its N side, so a few tokens cost a narrow MMA and the weight, which
+// is all there is to read then, streams through a ring of BT-dependent depth
+// with two CTAs on an SM.  Per CTA (192 threads):
+//   warp 0, one thread: TMA loads of the slice's K tiles (128 bytes of K);
+//   warp 1, one thread: 4 tcgen05.mma 128 x BT per K tile, commit -> empty;
+//   warps 2-5: the sums, from tensor memory.  With one CTA they are finished
+//     and stored from registers.  With more, every CTA leaves its sums in its
+//     shared memory (the ring, idle by then), and after a cluster barrier CTA
+//     r adds rows r * q .. of all of them, in slice order, so the result does
+//     not depend on timing.
+// Every wait is bounded, as in the other tcgen05 kernels; a CTA that gave up
+// leaves its flag where its cluster sees it, and none of them stores.
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "gemm_f16.cuh"
+#include "layers.h"
+#include "linear.cuh"
+
+namespace mt {
+namespace linear {
+
+using namespace f16tc;
+
+constexpr int BC = 128;  // columns of Y per tile
+constexpr int MAX_SPLIT = 8;
+
+template <int BT_>
+struct SplitGeometry {
+  static constexpr int BT = BT_;
+  static constexpr int W_BYTES = BC * ROW_BYTES;
+  static constexpr int X_BYTES = BT * ROW_BYTES;
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+  // Two CTAs share an SM's 227 KB.
+  static constexpr int STAGES = 108 * 1024 / STAGE_BYTES;
+  static constexpr uint32_t TMEM_COLS = BT < 32 ? 32 : BT;
+  static constexpr int SUM_BYTES = BT * BC * 4;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 /*alignment*/ + 256;
+  static_assert(SUM_BYTES <= STAGES * STAGE_BYTES, "the sums fit the ring");
+  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs on an SM");
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// FINISH_ROWS columns of this thread's TMEM lane; zeros for an empty slice of
+// K, whose tensor memory holds nothing.  (Warp w may access TMEM lanes
+// 32*(w%4) .. +31.)
+__device__ __forceinline__ void load_sums(uint32_t addr, bool any, Rows& v) {
+  if (any) {
+    tmem_ld16(addr, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < FINISH_ROWS; ++i) v[i] = 0.0f;
+  }
+}
+
+template <class E, int BT, bool W_MN, bool X_MN>
+__global__ void __launch_bounds__(THREADS, 2)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w,
+                        const __grid_constant__ CUtensorMap tmap_x, uint32_t idesc,
+                        const LinearEpilogue ep, int Kt, int tiles_t, int split, int fault_inject) {
+  static_assert(E::BYTES == 2 || (!W_MN && !X_MN), "8-bit operands are K-major");
+  using G = SplitGeometry<BT>;
+  constexpr int STAGES = G::STAGES;
+  constexpr int BK_ELEMS = ROW_BYTES / E::BYTES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * G::STAGE_BYTES);
+  constexpr int FULL = 0, EMPTY = STAGES, ACC_FULL = 2 * STAGES, NBARS = 2 * STAGES + 1;
+  static_assert(NBARS * 8 + 8 <= 256, "barriers, TMEM slot and abort flag fit 256 bytes");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const WaitCtx wc{abort_flag, &g_status};
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / split;
+  // Tiles of one weight panel follow each other, so the panel is read from
+  // memory once and found in L2 by the rest.
+  const int c0 = tile / tiles_t * BC, t0 = tile % tiles_t * BT;
+  const int kt0 = static_cast<int>(static_cast<int64_t>(Kt) * rank / split);
+  const int kt1 = static_cast<int>(static_cast<int64_t>(Kt) * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    if (Kt > 0) {  // without a product the maps hold nothing
+      prefetch_tmap(&tmap_w);
+      prefetch_tmap(&tmap_x);
+    }
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar(FULL + s), 1);   // producer arrival + tx bytes
+      mbar_init(bar(EMPTY + s), 1);  // MMA commit
+    }
+    mbar_init(bar(ACC_FULL), 1);  // MMA commit
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), G::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  float* const sums = reinterpret_cast<float*>(smem);  // [row][column], over the ring
+  int issued = 0;  // producer: K tiles issued
+  bool ready = true;
+  if (warp == 0) {
+    if (lane == 0 && !fault_inject) {
+      for (int kt = kt0; kt < kt1; ++kt, ++issued) {
+        const int s = issued % STAGES, round = issued / STAGES;
+        if (issued >= STAGES && !wait_phase(bar(EMPTY + s), (round + 1) & 1u, wc)) break;
+        const uint32_t st = smem_u32(smem + s * G::STAGE_BYTES);
+        mbar_arrive_expect_tx(bar(FULL + s), G::STAGE_BYTES);
+        load_operand<BC, W_MN>(st, &tmap_w, c0, kt * BK_ELEMS, bar(FULL + s));
+        load_operand<BT, X_MN>(st + G::W_BYTES, &tmap_x, t0, kt * BK_ELEMS, bar(FULL + s));
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool stop = false;
+      for (int g = 0; g < kt1 - kt0; ++g) {
+        const int s = g % STAGES, round = g / STAGES;
+        if (!wait_phase(bar(FULL + s), round & 1u, wc)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t w_base = smem_u32(smem + s * G::STAGE_BYTES);
+        const uint32_t x_base = w_base + G::W_BYTES;
+#pragma unroll
+        for (int j = 0; j < ROW_BYTES / 32; ++j)
+          E::mma(tmem, operand_desc<W_MN>(w_base, j), operand_desc<X_MN>(x_base, j), idesc,
+                 g > 0 || j > 0);
+        mma_commit(bar(EMPTY + s));
+      }
+      // Every MMA issued has retired once ACC_FULL completes, also after a
+      // wait that ran out.
+      mma_commit(bar(ACC_FULL));
+      if (stop) wait_phase(bar(ACC_FULL), 0, wc, false);
+    }
+  } else {
+    const int q = warp & 3;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int rows = min(BT, ep.T - t0);  // >= 1
+    ready = wait_phase(bar(ACC_FULL), 0, wc, true,
+                       TIMEOUT_NS + 20000ull * static_cast<uint64_t>(kt1 - kt0));
+    ready = __all_sync(0xffffffffu, ready && !*abort_flag);
+    tc_fence_after();
+    __syncwarp();
+    if (ready && split > 1) {
+#pragma unroll 1
+      for (int t = 0; t < rows; t += FINISH_ROWS) {
+        Rows v;
+        load_sums(t_row + t, kt1 > kt0, v);
+#pragma unroll
+        for (int i = 0; i < FINISH_ROWS; ++i)
+          if (t + i < rows) sums[(t + i) * BC + q * 32 + lane] = v[i];
+      }
+    }
+  }
+
+  if (split > 1) {
+    __syncwarp();
+    cluster_sync();  // every CTA's sums (or its abort flag) are in place
+    if (warp >= 2)
+      for (int s = 0; s < split; ++s)
+        ready = ready && !ld_cluster_s32(map_to_cta(smem_u32(const_cast<int*>(abort_flag)), s));
+  }
+  if (warp >= 2 && ready) {
+    const int q = warp & 3, c = q * 32 + lane;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int rows = min(BT, ep.T - t0), per = (rows + split - 1) / split;
+    const int first = rank * per, last = min(rows, first + per);
+#pragma unroll 1
+    for (int t = first; t < last; t += FINISH_ROWS) {
+      Rows v;
+      if (split == 1) {
+        load_sums(t_row + t, kt1 > kt0, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < FINISH_ROWS; ++i) v[i] = 0.0f;
+#pragma unroll 1
+        for (int s = 0; s < split; ++s) {
+          const uint32_t from = map_to_cta(smem_u32(sums + t * BC + c), s);
+#pragma unroll
+          for (int i = 0; i < FINISH_ROWS; ++i)
+            if (t + i < last) v[i] += ld_cluster_f32(from + i * BC * 4);
+        }
+      }
+      finish(ep, c0 + c, t0 + t, t0 + last, v);
+    }
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while its sums are being read
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0 && lane == 0 && *abort_flag) {
+    // Let the copies the producer issued land before the CTA exits.
+    for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+      wait_phase(bar(FULL + i % STAGES), (i / STAGES) & 1u, wc, false);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, G::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Padded copies of operands TMA cannot read in place (row pitch not a
+// multiple of 16 bytes, or base not 16-byte aligned): dst rows of `pitch`
+// bytes (a multiple of 16), the bytes past `bytes` zero.  E: element bytes,
+// which the source is aligned to.
+template <class T>
+__global__ void __launch_bounds__(256) copy_rows_kernel(const T* src, int64_t lds, uint8_t* dst,
+                                                        int64_t pitch, int64_t rows,
+                                                        int64_t cols) {
+  constexpr int N = 16 / sizeof(T);
+  const int64_t per_row = pitch / 16, total = rows * per_row;
+  for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < total;
+       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = e / per_row, c0 = (e % per_row) * N;
+    union {
+      T v[N];
+      uint4 u;
+    } o;
+    const T* s = src + r * lds;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o.v[i] = c0 + i < cols ? s[c0 + i] : T(0);
+    *reinterpret_cast<uint4*>(dst + r * pitch + (e % per_row) * 16) = o.u;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+namespace {
+
+bool tma_readable(const void* p, int64_t ld, int elem) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * elem % 16 == 0 &&
+         ld * elem < (int64_t(1) << 39);
+}
+
+// The stored matrix of an operand: rows and columns in memory.
+struct Stored {
+  const void* p;
+  int64_t rows, cols, ld;
+};
+Stored stored_x(const LinearArgs& a) {
+  return a.x_mn ? Stored{a.X, a.K, a.T, a.ldx} : Stored{a.X, a.T, a.K, a.ldx};
+}
+Stored stored_w(const LinearArgs& a) {
+  return a.w_mn ? Stored{a.W, a.K, a.C, a.ldw} : Stored{a.W, a.C, a.K, a.ldw};
+}
+
+int64_t copy_pitch_bytes(int64_t cols, int elem) { return (cols * elem + 127) / 128 * 128; }
+
+int64_t copy_bytes(const Stored& m, int elem) {
+  if (tma_readable(m.p, m.ld, elem)) return 0;
+  return (m.rows * copy_pitch_bytes(m.cols, elem) + 255) / 256 * 256;
+}
+
+cudaError_t copy_operand(Stored* m, int elem, void* dst, cudaStream_t stream) {
+  const int64_t pitch = copy_pitch_bytes(m->cols, elem);
+  const int64_t work = m->rows * (pitch / 16);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(1216, (work + 255) / 256));
+  if (elem == 1)
+    copy_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint8_t*>(m->p), m->ld,
+                                               static_cast<uint8_t*>(dst), pitch, m->rows,
+                                               m->cols);
+  else
+    copy_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(m->p), m->ld,
+                                               static_cast<uint8_t*>(dst), pitch, m->rows,
+                                               m->cols);
+  m->p = dst;
+  m->ld = pitch / elem;
+  return cudaGetLastError();
+}
+
+bool encode(CUtensorMap* map, int dtype, const Stored& m, bool mn, int rows) {
+  const CUtensorMapDataType t = dtype == DT_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                : dtype == DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int elem = dtype_bytes(dtype);
+  return mn ? encode_tensor_map_2d(map, t, elem, m.p, m.rows, m.cols, m.ld, MN_BOX, BK,
+                                   CU_TENSOR_MAP_SWIZZLE_128B)
+            : encode_tensor_map_2d(map, t, elem, m.p, m.rows, m.cols, m.ld, ROW_BYTES / elem,
+                                   rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+struct SplitEntry {
+  const void* kernel;
+  int smem, stages;
+};
+
+template <class E, int BT, bool W_MN, bool X_MN>
+SplitEntry entry() {
+  return SplitEntry{reinterpret_cast<const void*>(linear_split_kernel<E, BT, W_MN, X_MN>),
+                    SplitGeometry<BT>::SMEM_BYTES, SplitGeometry<BT>::STAGES};
+}
+
+// The built kernels: x_mn needs 64-row boxes and comes with w_mn only (the
+// weight gradient).
+bool split_entry(int dtype, int bt, bool w_mn, bool x_mn, SplitEntry* e) {
+  if (dtype == DT_E4M3) {
+    if (w_mn || x_mn) return false;
+    switch (bt) {
+      case 16: *e = entry<E4m3, 16, false, false>(); return true;
+      case 32: *e = entry<E4m3, 32, false, false>(); return true;
+      case 64: *e = entry<E4m3, 64, false, false>(); return true;
+      case 128: *e = entry<E4m3, 128, false, false>(); return true;
+    }
+    return false;
+  }
+  if (x_mn) {
+    if (!w_mn) return false;
+    switch (bt) {
+      case 64: *e = entry<Half, 64, true, true>(); return true;
+      case 128: *e = entry<Half, 128, true, true>(); return true;
+    }
+    return false;
+  }
+  switch (bt) {
+    case 16: *e = w_mn ? entry<Half, 16, true, false>() : entry<Half, 16, false, false>(); return true;
+    case 32: *e = w_mn ? entry<Half, 32, true, false>() : entry<Half, 32, false, false>(); return true;
+    case 64: *e = w_mn ? entry<Half, 64, true, false>() : entry<Half, 64, false, false>(); return true;
+    case 128: *e = w_mn ? entry<Half, 128, true, false>() : entry<Half, 128, false, false>(); return true;
+  }
+  return false;
+}
+
+}  // namespace
+}  // namespace linear
+
+using namespace linear;
+
+LinearPlan plan_linear(const LinearArgs& a, int sms) {
+  LinearPlan p{};
+  const int elem = dtype_bytes(a.dtype);
+  p.bt = a.T <= 16 && !a.x_mn ? 16 : a.T <= 32 && !a.x_mn ? 32 : a.T <= 64 ? 64 : 128;
+  SplitEntry e{};
+  split_entry(a.dtype, p.bt, a.w_mn, a.x_mn, &e);
+  const int64_t tiles = ((a.C + BC - 1) / BC) * ((a.T + p.bt - 1) / p.bt);
+  const int64_t ktiles = (a.K * elem + ROW_BYTES - 1) / ROW_BYTES;
+  // Slices of K: as many CTAs as two per SM hold, each at least four K tiles.
+  const int64_t split = std::min<int64_t>({MAX_SPLIT, 2 * sms / tiles, ktiles / 4});
+  p.split = static_cast<int>(std::max<int64_t>(1, split));
+  p.bc = BC;
+  p.threads = THREADS;
+  p.stages = e.stages;
+  p.smem_bytes = e.smem;
+  p.grid = tiles * p.split;
+  p.copy_x_bytes = a.K > 0 ? copy_bytes(stored_x(a), elem) : 0;
+  p.copy_w_bytes = a.K > 0 ? copy_bytes(stored_w(a), elem) : 0;
+  p.workspace_bytes = p.copy_x_bytes + p.copy_w_bytes;
+  return p;
+}
+
+cudaError_t linear_prepare() {
+  for (int dtype : {DT_F16, DT_E4M3})
+    for (int bt : {16, 32, 64, 128})
+      for (int mn = 0; mn < 4; ++mn) {
+        SplitEntry e{};
+        if (!split_entry(dtype, bt, mn & 1, mn >> 1, &e)) continue;
+        const cudaError_t r =
+            cudaFuncSetAttribute(e.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, e.smem);
+        if (r != cudaSuccess) return r;
+      }
+  return cudaSuccess;
+}
+
+cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
+                          cudaStream_t stream, int fault_inject) {
+  const int elem = dtype_bytes(a.dtype);
+  Stored x = stored_x(a), w = stored_w(a);
+  char* ws = static_cast<char*>(workspace);
+  if (p.copy_x_bytes) {
+    const cudaError_t r = copy_operand(&x, elem, ws, stream);
+    if (r != cudaSuccess) return r;
+  }
+  if (p.copy_w_bytes) {
+    const cudaError_t r = copy_operand(&w, elem, ws + p.copy_x_bytes, stream);
+    if (r != cudaSuccess) return r;
+  }
+  SplitEntry e{};
+  if (!split_entry(a.dtype, p.bt, a.w_mn, a.x_mn, &e)) return cudaErrorInvalidValue;
+  CUtensorMap map_w{}, map_x{};
+  // Without a product (K = 0) the maps are not read.
+  if (a.K > 0 && (!encode(&map_w, a.dtype, w, a.w_mn, BC) ||
+                  !encode(&map_x, a.dtype, x, a.x_mn, p.bt)))
+    return cudaErrorInvalidValue;
+  const uint32_t fmt = a.dtype == DT_BF16 ? 1u : 0u;  // f16 0, bf16 1; e4m3 0
+  uint32_t idesc = tc::instr_desc(BC, p.bt, fmt, fmt, a.w_mn ? 1u : 0u, a.x_mn ? 1u : 0u);
+  LinearEpilogue ep{a.Y, a.ldy, a.Z, a.ldz, a.residual, a.ldr, a.bias, a.row_scale, a.col_scale,
+                    static_cast<int>(a.T), static_cast<int>(a.C), a.out_dtype, a.act, a.bounds};
+  int kt = static_cast<int>((a.K * elem + ROW_BYTES - 1) / ROW_BYTES);
+  int tiles_t = static_cast<int>((a.T + p.bt - 1) / p.bt), split = p.split;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&map_w, &map_x, &idesc, &ep, &kt, &tiles_t, &split, &fault_inject};
+  return cudaLaunchKernelExC(&cfg, e.kernel, args);
+}
+
+cudaError_t linear_read_and_clear_status(unsigned int* status) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, f16tc::g_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(f16tc::g_status, &zero, sizeof(unsigned int));
+}
+
+}  // namespace mt

@@ -1,6 +1,6 @@
 """Binding of the feed-forward operators (include/mt_layers.h).
 
-``rms_norm`` and ``rms_norm_backward`` on torch CUDA tensors, and the C entry points under their own
+``rms_norm``, ``rms_norm_backward`` and ``linear`` on torch CUDA tensors, and the C entry points under their own
 names taking a filled argument structure.  Marshalling only, as in the
 package's ``__init__``, which re-exports everything here.
 """
@@ -15,6 +15,10 @@ MT_DTYPE_F32 = 3
 MT_DTYPE_E4M3 = 4
 MT_E4M3_MAX = 448.0
 MT_SCALE_MIN = 2.0 ** -126
+
+MT_ACT_NONE, MT_ACT_RELU, MT_ACT_GELU, MT_ACT_GELU_TANH, MT_ACT_SILU = range(5)
+ACTIVATIONS = {None: MT_ACT_NONE, "none": MT_ACT_NONE, "relu": MT_ACT_RELU, "gelu": MT_ACT_GELU,
+               "gelu_tanh": MT_ACT_GELU_TANH, "silu": MT_ACT_SILU}
 
 
 class mt_rms_norm_args(ctypes.Structure):
@@ -31,11 +35,21 @@ class mt_rms_norm_backward_args(ctypes.Structure):
                 ("weight_dtype", _I32)]
 
 
+class mt_linear_args(ctypes.Structure):
+    _fields_ = [("M", _I64), ("N", _I64), ("K", _I64), ("A", _P), ("lda", _I64), ("B", _P),
+                ("ldb", _I64), ("Y", _P), ("ldy", _I64), ("Z", _P), ("ldz", _I64),
+                ("residual", _P), ("ldr", _I64), ("bias", _P), ("scale_a", _P),
+                ("scale_b", _P), ("trans_b", _I32), ("dtype", _I32), ("out_dtype", _I32),
+                ("activation", _I32), ("fault_inject", _I32), ("reserved", _I32)]
+
+
 # name -> (restype, argtypes): every function include/mt_layers.h declares.
 # The argument structure is passed as its bytes or by reference.
 SIGNATURES = {
     "mt_rms_norm": (ctypes.c_int, [_P, _P]),
     "mt_rms_norm_backward": (ctypes.c_int, [_P, _P]),
+    "mt_linear": (ctypes.c_int, [_P, _P]),
+    "mt_linear_plan": (ctypes.c_int, [_P, ctypes.c_int, _P]),
 }
 
 
@@ -50,6 +64,7 @@ def _packer(cls):
 
 _pack_rms_norm = _packer(mt_rms_norm_args)
 _pack_rms_norm_backward = _packer(mt_rms_norm_backward_args)
+_pack_linear = _packer(mt_linear_args)
 
 
 # --- the C entry points, same names -----------------------------------------
@@ -61,6 +76,18 @@ def mt_rms_norm(args: mt_rms_norm_args, stream: int = 0) -> int:
 def mt_rms_norm_backward(args: mt_rms_norm_backward_args, stream: int = 0) -> int:
     from . import lib
     return lib().mt_rms_norm_backward(ctypes.byref(args), stream)
+
+
+def mt_linear(args: mt_linear_args, stream: int = 0) -> int:
+    from . import lib
+    return lib().mt_linear(ctypes.byref(args), stream)
+
+
+def mt_linear_plan(args: mt_linear_args, sms: int):
+    from . import lib, mt_plan
+    out = mt_plan()
+    st = lib().mt_linear_plan(ctypes.byref(args), sms, ctypes.byref(out))
+    return st, out
 
 
 # --- torch convenience (marshalling only) ------------------------------------
@@ -214,3 +241,66 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, need_weight=True, out=None, 
           _pack_rms_norm_backward(rows, d, dyp, lddy, hp, ldh, wp, rp, dhp, lddh, dxp, lddx, dwp,
                                   codes[dt], wcode), dev, stream)
     return dx, dweight
+
+
+def _activation(name):
+    try:
+        return ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)} "
+                         "or None") from None
+
+
+def linear(a, b, bias=None, activation=None, residual=None, trans_b=False, scale_a=None,
+           scale_b=None, out_dtype=None, out=None, preact=False, stream=None):
+    """act(a @ op(b) + bias) + residual in one pass, through mt_linear.
+
+    a: M x K, b: K x N (or N x K with ``trans_b``), 2-D CUDA tensors of one
+    16-bit dtype, rows may be strided; bias: N float32 values; residual:
+    M x N in the output's dtype; activation: None, "relu", "gelu",
+    "gelu_tanh" or "silu".  With float8_e4m3fn a and b (``trans_b`` only) the
+    product is scaled by ``scale_a`` (M float32 values, one per row of a)
+    and ``scale_b`` (N, one per column of the output).  ``out_dtype``: a's
+    dtype (bfloat16 for 8-bit inputs) unless given; float32 is always
+    allowed.  Returns the output (``out`` when given, which may be the
+    residual), or ``(output, z)`` with the pre-activation z in the output's
+    dtype when ``preact`` is set."""
+    import torch
+    codes = _dtype_codes()
+    _first(a, "a", (torch.float16, torch.bfloat16, torch.float8_e4m3fn))
+    M, K = a.shape
+    dt, dev = a.dtype, a.device
+    if not isinstance(b, torch.Tensor) or b.dim() != 2:
+        raise ValueError("b must be a 2-D CUDA tensor")
+    N = b.shape[0] if trans_b else b.shape[1]
+    ap, lda = _matrix(a, "a", M, K, dt, dev)
+    bp, ldb = _matrix(b, "b", *((N, K) if trans_b else (K, N)), dt, dev)
+    bias_p = rp = ldr = zp = ldz = sap = sbp = 0
+    if dt == torch.float8_e4m3fn:
+        if not trans_b:
+            raise ValueError("8-bit inputs need b stored N x K (trans_b)")
+        sap = _vector(scale_a, "scale_a", M, (torch.float32,), dev)
+        sbp = _vector(scale_b, "scale_b", N, (torch.float32,), dev)
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in (torch.float16, torch.bfloat16, torch.float32):
+            raise TypeError("out_dtype must be float16, bfloat16 or float32")
+    else:
+        if scale_a is not None or scale_b is not None:
+            raise ValueError("scales go with float8_e4m3fn inputs")
+        out_dtype = out_dtype or dt
+        if out_dtype not in (dt, torch.float32):
+            raise TypeError("out_dtype must be a's dtype or float32")
+    if bias is not None:
+        bias_p = _vector(bias, "bias", N, (torch.float32,), dev)
+    if residual is not None:
+        rp, ldr = _matrix(residual, "residual", M, N, out_dtype, dev)
+    y = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+    yp, ldy = _matrix(y, "out", M, N, out_dtype, dev)
+    if preact:
+        z = torch.empty((M, N), dtype=out_dtype, device=dev)
+        zp, ldz = z.data_ptr(), max(N, 1)
+    _call("mt_linear",
+          _pack_linear(M, N, K, ap, lda, bp, ldb, yp, ldy, zp, ldz, rp, ldr, bias_p, sap, sbp,
+                       int(trans_b), codes[dt], codes[out_dtype], _activation(activation), 0, 0),
+          dev, stream)
+    return (y, z) if preact else y
