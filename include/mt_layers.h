@@ -190,6 +190,46 @@ MT_API mt_status mt_linear(const mt_linear_args *args, cudaStream_t stream);
  */
 MT_API mt_status mt_linear_plan(const mt_linear_args *args, int sms, mt_plan *out);
 
+/*
+ * The gradient of mt_linear with 16-bit inputs: with dz = dY * act'(Z), in
+ * fp32 and rounded to dtype for the two products,
+ *
+ *     dA       = dz * B^T                    M x K, dtype
+ *     dB       = A^T * dz, stored as B is    K x N (N x K with trans_b), db_dtype
+ *     dbias[j] = sum_i dz[i][j]              N floats, of the unrounded dz, in
+ *                                            a fixed order (same bits each time)
+ *
+ * The residual's gradient is dY itself.  Z is the forward call's
+ * pre-activation (not read for MT_ACT_NONE).  dA, dB and dbias may each be
+ * NULL: not computed; B is read for dA only, A for dB only.
+ */
+typedef struct {
+    int64_t M, N, K;
+    const void *dY;
+    int64_t lddy;
+    const void *Z;
+    int64_t ldz;
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb;
+    void *dA;
+    int64_t ldda;
+    void *dB;
+    int64_t lddb;
+    float *dbias;
+    int32_t trans_b;    /* 0 or 1 */
+    int32_t dtype;      /* dY, Z, A, B, dA: MT_DTYPE_F16 or MT_DTYPE_BF16 */
+    int32_t db_dtype;   /* dB: dtype or MT_DTYPE_F32 */
+    int32_t activation; /* mt_activation */
+} mt_linear_backward_args;
+
+/* An empty sum gives zeros (M == 0: dB and dbias; N == 0: dA).  Outputs
+ * overlap nothing (MT_ERR_ALIAS).  Scratch: dz, unless the activation is the
+ * identity and TMA reads dY in place, column sums for dbias, and copies of
+ * operands TMA cannot read in place.  Other errors as mt_linear. */
+MT_API mt_status mt_linear_backward(const mt_linear_backward_args *args, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

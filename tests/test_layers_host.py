@@ -21,7 +21,8 @@ def built_library():
     return mt.lib()
 
 
-CLASSES = (mt.mt_rms_norm_args, mt.mt_rms_norm_backward_args, mt.mt_linear_args)
+CLASSES = (mt.mt_rms_norm_args, mt.mt_rms_norm_backward_args, mt.mt_linear_args,
+           mt.mt_linear_backward_args)
 
 
 def norm_args(**change):
@@ -192,6 +193,48 @@ def test_linear_plan_reports_copies():
     assert p["workspace_bytes"] == 64 * 256
     p = linear_plan(64, 64, 72, **{**E4M3, "lda": 72, "ldb": 72})
     assert p["workspace_bytes"] == 2 * 64 * 128
+
+
+def linear_grad_args(**change):
+    a = mt.mt_linear_backward_args(M=4, N=16, K=32, dY=0x10000, lddy=16, Z=0x20000, ldz=16,
+                                   A=0x30000, lda=32, B=0x40000, ldb=16, dA=0x50000, ldda=32,
+                                   dB=0x60000, lddb=16, dbias=0x70000, dtype=mt.MT_DTYPE_F16,
+                                   db_dtype=mt.MT_DTYPE_F16, activation=mt.MT_ACT_GELU)
+    for k, v in change.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("change", [
+    dict(M=-1), dict(N=1 << 31), dict(K=-1), dict(dY=None), dict(Z=None), dict(A=None),
+    dict(B=None), dict(lddy=15), dict(ldz=15), dict(lda=31), dict(ldb=15), dict(ldda=31),
+    dict(lddb=15), dict(trans_b=1), dict(trans_b=-1), dict(dtype=mt.MT_DTYPE_E4M3),
+    dict(dtype=mt.MT_DTYPE_F32), dict(db_dtype=mt.MT_DTYPE_BF16), dict(activation=7),
+    dict(dbias=0x70001), dict(dB=0x60002, db_dtype=mt.MT_DTYPE_F32)])
+def test_linear_backward_refuses_invalid_arguments(change):
+    assert mt.mt_linear_backward(linear_grad_args(**change)) == mt.MT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [
+    dict(dA=0x10000), dict(dA=0x20000), dict(dA=0x30000), dict(dA=0x40000), dict(dA=0x60000),
+    dict(dA=0x70000), dict(dB=0x10000), dict(dB=0x20000), dict(dB=0x30000), dict(dB=0x40000),
+    dict(dB=0x70000), dict(dbias=0x10000), dict(dbias=0x20004)])
+def test_linear_backward_refuses_overlap(change):
+    assert mt.mt_linear_backward(linear_grad_args(**change)) == mt.MT_ERR_ALIAS
+
+
+@pytest.mark.skipif(HAS_GPU, reason="made-up addresses")
+@pytest.mark.parametrize("change", [
+    dict(), dict(activation=0, Z=None), dict(dA=None, B=None), dict(dB=None, A=None),
+    dict(dbias=None), dict(M=0), dict(trans_b=1, ldb=32, lddb=32),
+    dict(db_dtype=mt.MT_DTYPE_F32)])
+def test_linear_backward_without_a_device(change):
+    assert mt.mt_linear_backward(linear_grad_args(**change)) == mt.MT_ERR_NO_DEVICE
+
+
+def test_linear_backward_of_nothing():
+    assert mt.mt_linear_backward(linear_grad_args(dA=None, dB=None, dbias=None)) == mt.MT_OK
+    assert mt.mt_linear_backward(linear_grad_args(K=0, dbias=None)) == mt.MT_OK
 
 
 def test_packed_arguments_match_the_structure():

@@ -19,7 +19,7 @@ by ``tiled_fp32_gemm_gb300.build``).  This module only marshals arguments:
   (torch supplies device memory and the current stream; nothing else);
   ``gemm`` for the general form and ``gemm_mixed`` for 16-bit inputs;
 * the feed-forward operators of ``layers`` (include/mt_layers.h):
-  ``rms_norm``, ``rms_norm_backward`` and ``linear``.
+  ``rms_norm``, ``linear`` and their gradients.
 
 There is no CPU fallback: if the library is missing, every call raises.
 """
@@ -141,7 +141,8 @@ SIGNATURES = {
 
 from .layers import (ACTIVATIONS, MT_ACT_GELU, MT_ACT_GELU_TANH,  # noqa: E402,F401
                      MT_ACT_NONE, MT_ACT_RELU, MT_ACT_SILU, MT_DTYPE_E4M3, MT_DTYPE_F32,
-                     MT_E4M3_MAX, MT_SCALE_MIN, linear, mt_linear, mt_linear_args,
+                     MT_E4M3_MAX, MT_SCALE_MIN, linear, linear_backward, mt_linear, mt_linear_args,
+                     mt_linear_backward, mt_linear_backward_args,
                      mt_linear_plan, mt_rms_norm, mt_rms_norm_args, mt_rms_norm_backward,
                      mt_rms_norm_backward_args, rms_norm, rms_norm_backward)
 from .layers import SIGNATURES as _LAYER_SIGNATURES  # noqa: E402

@@ -120,4 +120,27 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* worksp
                           cudaStream_t stream, int fault_inject = 0);
 cudaError_t linear_read_and_clear_status(unsigned int* status);
 
+// Whether TMA reads a matrix of `elem`-byte values in place: 16-byte aligned
+// base, row pitch a multiple of 16 bytes.
+bool tma_readable(const void* p, int64_t ld, int elem);
+
+// linear_grad.cu: dz = dY * act'(Z) rounded to `dtype` (dZ null: not
+// written), and the column sums of the unrounded dz (dbias null: not
+// computed), through `partial` (linear_dz_workspace bytes).
+struct LinearDzArgs {
+  int64_t M;
+  int N;
+  const void* dY;
+  int64_t lddy;
+  const void* Z;
+  int64_t ldz;
+  void* dZ;
+  int64_t lddz;
+  float* dbias;
+  int dtype, act;
+  BoundsRecord* bounds;
+};
+int64_t linear_dz_workspace(const LinearDzArgs& a, int sms);
+cudaError_t launch_linear_dz(const LinearDzArgs& a, void* partial, int sms, cudaStream_t stream);
+
 }  // namespace mt

@@ -275,4 +275,107 @@ mt_status mt_linear_plan(const mt_linear_args* g, int sms, mt_plan* out) {
   return MT_OK;
 }
 
+mt_status mt_linear_backward(const mt_linear_backward_args* g, cudaStream_t stream) {
+  if (!g || g->M < 0 || g->N < 0 || g->K < 0 || g->M > kMaxSize || g->N > kMaxSize ||
+      g->K > kMaxSize || g->trans_b < 0 || g->trans_b > 1 || !half_type(g->dtype) ||
+      (g->db_dtype != g->dtype && g->db_dtype != MT_DTYPE_F32) ||
+      g->activation < MT_ACT_NONE || g->activation > MT_ACT_SILU)
+    return MT_ERR_INVALID_ARG;
+  const int64_t M = g->M, N = g->N, K = g->K;
+  const bool act = g->activation != MT_ACT_NONE;
+  // A B stored K x N, or N x K; rows == 0 for what is not there or not read.
+  auto like_b = [&](const void* p, int64_t ld, int elem, bool used) {
+    return g->trans_b ? View{p, used ? N : 0, K, used ? ld : INT32_MAX, elem}
+                      : View{p, used ? K : 0, N, used ? ld : INT32_MAX, elem};
+  };
+  const View dY{g->dY, M, N, g->lddy, 2};
+  const View Z{g->Z, act ? M : 0, N, act ? g->ldz : INT32_MAX, 2};
+  const View A{g->A, g->dB ? M : 0, K, g->dB ? g->lda : INT32_MAX, 2};
+  const View B = like_b(g->B, g->ldb, 2, g->dA != nullptr);
+  const View dA{g->dA, g->dA ? M : 0, K, g->dA ? g->ldda : INT32_MAX, 2};
+  const View dB = like_b(g->dB, g->lddb, mt::dtype_bytes(g->db_dtype), g->dB != nullptr);
+  const View db{g->dbias, g->dbias ? 1 : 0, N, INT32_MAX, 4};
+  for (const View* v : {&dY, &Z, &A, &B, &dA, &dB, &db})
+    if (!v->valid()) return MT_ERR_INVALID_ARG;
+  for (const View* out : {&dA, &dB, &db})
+    for (const View* in : {&dY, &Z, &A, &B})
+      if (out->hits(*in)) return MT_ERR_ALIAS;
+  if (dA.hits(dB) || dA.hits(db) || dB.hits(db)) return MT_ERR_ALIAS;
+  const bool want_a = g->dA && M > 0 && K > 0, want_b = g->dB && N > 0 && K > 0;
+  const bool want_bias = g->dbias && N > 0;
+  if (!want_a && !want_b && !want_bias) return MT_OK;
+  int dev = 0;
+  DeviceInfo info;
+  mt_status st = current_device(&dev, &info);
+  if (st == MT_OK) st = prepare_linear(dev);
+  if (st != MT_OK) return st;
+
+  // dz, in rows of whole 128-byte lines, unless dY serves as it is.
+  const bool products = (want_a || want_b) && M > 0 && N > 0;
+  const bool make_dz = products && (act || !mt::tma_readable(g->dY, g->lddy, 2));
+  const int64_t lddz = ceil_div(N, 64) * 64;
+  const int64_t dz_bytes = make_dz ? ceil_div(M * lddz * 2, 256) * 256 : 0;
+  mt::LinearDzArgs dz{M, static_cast<int>(N), g->dY, g->lddy, g->Z, g->ldz, nullptr, lddz,
+                      want_bias ? g->dbias : nullptr, g->dtype, g->activation, bounds_record()};
+  const int64_t sum_bytes = ceil_div(mt::linear_dz_workspace(dz, info.sms), 256) * 256;
+
+  mt::LinearArgs pa{}, pb{};
+  pa.dtype = pb.dtype = g->dtype;
+  pa.out_dtype = g->dtype;
+  pb.out_dtype = g->db_dtype;
+  pa.act = pb.act = mt::ACT_NONE;
+  pa.bounds = pb.bounds = bounds_record();
+  // dA = dz * B^T: rows of dz against B's columns k, contracted over n.
+  pa.T = M;
+  pa.C = K;
+  pa.K = N;
+  pa.W = g->B;
+  pa.ldw = g->ldb;
+  pa.w_mn = g->trans_b;
+  pa.Y = g->dA;
+  pa.ldy = g->ldda;
+  // dB as B is stored, contracted over rows: A^T * dz, or dz^T * A.
+  pb.T = g->trans_b ? N : K;
+  pb.C = g->trans_b ? K : N;
+  pb.K = M;
+  pb.x_mn = pb.w_mn = 1;
+  pb.Y = g->dB;
+  pb.ldy = g->lddb;
+
+  // The scratch of the products follows; the plans look at the operands'
+  // alignment, which scratch addresses (256-byte aligned) do not change.
+  auto bind = [&](const void* dzp, int64_t ld) {
+    pa.X = dzp;
+    pa.ldx = ld;
+    pb.X = g->trans_b ? dzp : g->A;
+    pb.ldx = g->trans_b ? ld : g->lda;
+    pb.W = g->trans_b ? g->A : dzp;
+    pb.ldw = g->trans_b ? g->lda : ld;
+  };
+  bind(make_dz ? nullptr : g->dY, make_dz ? lddz : g->lddy);
+  mt::LinearPlan plan_a{}, plan_b{};
+  if (want_a) plan_a = mt::plan_linear(pa, info.sms);
+  if (want_b) plan_b = mt::plan_linear(pb, info.sms);
+  if (plan_a.grid > INT32_MAX || plan_b.grid > INT32_MAX) return MT_ERR_UNSUPPORTED;
+  Scratch ws(stream);
+  st = ws.get(dev, dz_bytes + sum_bytes + plan_a.workspace_bytes + plan_b.workspace_bytes);
+  if (st != MT_OK) return st;
+  char* base = static_cast<char*>(ws.p);
+  if (make_dz) {
+    dz.dZ = base;
+    bind(base, lddz);
+  }
+  cudaError_t e = cudaSuccess;
+  if (make_dz || want_bias) e = mt::launch_linear_dz(dz, base + dz_bytes, info.sms, stream);
+  char* wa = base + dz_bytes + sum_bytes;
+  if (e == cudaSuccess && want_a) e = mt::launch_linear(pa, plan_a, wa, stream);
+  if (e == cudaSuccess && want_b)
+    e = mt::launch_linear(pb, plan_b, wa + plan_a.workspace_bytes, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return MT_ERR_LAUNCH;
+  }
+  return MT_OK;
+}
+
 }  // extern "C"

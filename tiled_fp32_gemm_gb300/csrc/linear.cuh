@@ -33,6 +33,29 @@ __device__ __forceinline__ float activate(float z) {
   }
 }
 
+// Their derivatives.  Past the clamps the logistic forms' derivatives are 0
+// or 1 to fp32; the clamps keep 0 * infinity out of them (a NaN passes).
+template <int ACT>
+__device__ __forceinline__ float activate_grad(float z) {
+  if constexpr (ACT == ACT_RELU) {
+    return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
+  } else if constexpr (ACT == ACT_GELU) {
+    // Phi(z) + z * phi(z)
+    return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z),
+                0.5f * (1.0f + erff(z * 0.70710678118654752f)));
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    const float x = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;
+    const float p = logistic(1.5957691216057308f * fmaf(0.044715f * x * x, x, x));
+    return fmaf(p * (1.0f - p) * x, 1.5957691216057308f * fmaf(0.134145f * x, x, 1.0f), p);
+  } else if constexpr (ACT == ACT_SILU) {
+    const float x = z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z;
+    const float p = logistic(x);
+    return p * fmaf(x, 1.0f - p, 1.0f);
+  } else {
+    return 1.0f;
+  }
+}
+
 struct LinearEpilogue {
   void* Y;
   int64_t ldy;

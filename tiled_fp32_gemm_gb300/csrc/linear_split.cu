@@ -257,11 +257,6 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const T* src, int64_t ld
 
 namespace {
 
-bool tma_readable(const void* p, int64_t ld, int elem) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * elem % 16 == 0 &&
-         ld * elem < (int64_t(1) << 39);
-}
-
 // The stored matrix of an operand: rows and columns in memory.
 struct Stored {
   const void* p;
@@ -354,6 +349,11 @@ bool split_entry(int dtype, int bt, bool w_mn, bool x_mn, SplitEntry* e) {
 }  // namespace linear
 
 using namespace linear;
+
+bool tma_readable(const void* p, int64_t ld, int elem) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * elem % 16 == 0 &&
+         ld * elem < (int64_t(1) << 39);
+}
 
 LinearPlan plan_linear(const LinearArgs& a, int sms) {
   LinearPlan p{};

@@ -1,6 +1,6 @@
 """Binding of the feed-forward operators (include/mt_layers.h).
 
-``rms_norm``, ``rms_norm_backward`` and ``linear`` on torch CUDA tensors, and the C entry points under their own
+``rms_norm``, ``linear`` and their gradients on torch CUDA tensors, and the C entry points under their own
 names taking a filled argument structure.  Marshalling only, as in the
 package's ``__init__``, which re-exports everything here.
 """
@@ -43,12 +43,20 @@ class mt_linear_args(ctypes.Structure):
                 ("activation", _I32), ("fault_inject", _I32), ("reserved", _I32)]
 
 
+class mt_linear_backward_args(ctypes.Structure):
+    _fields_ = [("M", _I64), ("N", _I64), ("K", _I64), ("dY", _P), ("lddy", _I64), ("Z", _P),
+                ("ldz", _I64), ("A", _P), ("lda", _I64), ("B", _P), ("ldb", _I64), ("dA", _P),
+                ("ldda", _I64), ("dB", _P), ("lddb", _I64), ("dbias", _P), ("trans_b", _I32),
+                ("dtype", _I32), ("db_dtype", _I32), ("activation", _I32)]
+
+
 # name -> (restype, argtypes): every function include/mt_layers.h declares.
 # The argument structure is passed as its bytes or by reference.
 SIGNATURES = {
     "mt_rms_norm": (ctypes.c_int, [_P, _P]),
     "mt_rms_norm_backward": (ctypes.c_int, [_P, _P]),
     "mt_linear": (ctypes.c_int, [_P, _P]),
+    "mt_linear_backward": (ctypes.c_int, [_P, _P]),
     "mt_linear_plan": (ctypes.c_int, [_P, ctypes.c_int, _P]),
 }
 
@@ -65,6 +73,7 @@ def _packer(cls):
 _pack_rms_norm = _packer(mt_rms_norm_args)
 _pack_rms_norm_backward = _packer(mt_rms_norm_backward_args)
 _pack_linear = _packer(mt_linear_args)
+_pack_linear_backward = _packer(mt_linear_backward_args)
 
 
 # --- the C entry points, same names -----------------------------------------
@@ -88,6 +97,11 @@ def mt_linear_plan(args: mt_linear_args, sms: int):
     out = mt_plan()
     st = lib().mt_linear_plan(ctypes.byref(args), sms, ctypes.byref(out))
     return st, out
+
+
+def mt_linear_backward(args: mt_linear_backward_args, stream: int = 0) -> int:
+    from . import lib
+    return lib().mt_linear_backward(ctypes.byref(args), stream)
 
 
 # --- torch convenience (marshalling only) ------------------------------------
@@ -304,3 +318,49 @@ def linear(a, b, bias=None, activation=None, residual=None, trans_b=False, scale
                        int(trans_b), codes[dt], codes[out_dtype], _activation(activation), 0, 0),
           dev, stream)
     return (y, z) if preact else y
+
+
+def linear_backward(dy, a, b, z=None, activation=None, trans_b=False, need_a=True, need_b=True,
+                    need_bias=True, db_dtype=None, stream=None):
+    """``(da, db, dbias)``: the gradient of ``linear`` with 16-bit inputs,
+    through mt_linear_backward (None for what is not needed; the residual's
+    gradient is dy itself).
+
+    dy: M x N gradient of the output, in a's dtype; z: the forward call's
+    pre-activation (needed unless ``activation`` is None); a, b, ``trans_b``
+    as there.  da has a's dtype, db is stored as b in ``db_dtype`` (a's, or
+    float32), dbias is float32."""
+    import torch
+    codes = _dtype_codes()
+    _first(dy, "dy", (torch.float16, torch.bfloat16))
+    M, N = dy.shape
+    dt, dev = dy.dtype, dy.device
+    act = _activation(activation)
+    if not isinstance(a, torch.Tensor) or a.dim() != 2:
+        raise ValueError("a must be a 2-D CUDA tensor")
+    K = a.shape[1]
+    db_dtype = db_dtype or dt
+    if db_dtype not in (dt, torch.float32):
+        raise TypeError("db_dtype must be a's dtype or float32")
+    dyp, lddy = _matrix(dy, "dy", M, N, dt, dev)
+    ap, lda = _matrix(a, "a", M, K, dt, dev)
+    shape = (N, K) if trans_b else (K, N)
+    bp, ldb = _matrix(b, "b", *shape, dt, dev)
+    zp = ldz = dap = dbp = dbiasp = 0
+    if act != MT_ACT_NONE:
+        zp, ldz = _matrix(z, "z", M, N, dt, dev)
+    da = db = dbias = None
+    if need_a:
+        da = torch.empty((M, K), dtype=dt, device=dev)
+        dap = da.data_ptr()
+    if need_b:
+        db = torch.empty(shape, dtype=db_dtype, device=dev)
+        dbp = db.data_ptr()
+    if need_bias:
+        dbias = torch.empty(N, dtype=torch.float32, device=dev)
+        dbiasp = dbias.data_ptr()
+    _call("mt_linear_backward",
+          _pack_linear_backward(M, N, K, dyp, lddy, zp, ldz, ap, lda, bp, ldb, dap, max(K, 1),
+                                dbp, max(shape[1], 1), dbiasp, int(trans_b), codes[dt],
+                                codes[db_dtype], act), dev, stream)
+    return da, db, dbias
