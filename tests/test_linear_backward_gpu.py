@@ -100,6 +100,20 @@ def test_matches_the_formula(dt, trans, M, N, K, pad, act):
     check(dy, a, b, z, act, trans, db_dtype=torch.float32 if M % 2 else None)
 
 
+@pytest.mark.parametrize("dt", sorted(DTYPES))
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("M,N,K", [(2400, 2305, 2561), (2305, 2305, 2305)])
+def test_tiles_that_fill_the_gpu(dt, trans, act, M, N, K):
+    g = torch.Generator().manual_seed(M + trans)
+    t = DTYPES[dt]
+    dy, a = stored(g, M, N, N + 7, t), stored(g, M, K, K + 7, t)
+    z = stored(g, M, N, N, t, 2.0) if act != "none" else None
+    shape = (N, K) if trans else (K, N)
+    check(dy, a, stored(g, *shape, shape[1], t, K ** -0.5), z, act, trans,
+          db_dtype=torch.float32 if M % 2 else None)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dt", sorted(DTYPES))
 def test_derivatives_over_their_range(act, dt):

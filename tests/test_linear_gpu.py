@@ -128,7 +128,29 @@ def test_8_bit(M, N, K, pad, out):
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16", "e4m3"])
-@pytest.mark.parametrize("M,N,K", [(3, 200, 4100), (130, 300, 1000), (600, 520, 256)])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("M,N,K,pad", [(2500, 2305, 640, 0), (2305, 2561, 77, 5),
+                                       (1, 40000, 64, 0), (20000, 256, 128, 8)])
+@pytest.mark.parametrize("out", [None, torch.float32])
+def test_tiles_that_fill_the_gpu(dt, trans, M, N, K, pad, out):
+    """Enough 256 x 256 tiles for the CTA-pair kernel, with ragged edges."""
+    if dt == "e4m3" and not trans:
+        return
+    g = torch.Generator().manual_seed(M + N)
+    t = E4M3 if dt == "e4m3" else DTYPES[dt]
+    a = stored(g, M, K, K + pad, t)
+    b = stored(g, *((N, K) if trans else (K, N)), (K if trans else N) + pad, t, K ** -0.5)
+    res = stored(g, M, N, N + pad, out or (torch.bfloat16 if dt == "e4m3" else t))
+    sa = sb = None
+    if dt == "e4m3":
+        sa, sb = torch.rand(M, generator=g).cuda() + 0.5, torch.rand(N, generator=g).cuda() + 0.5
+    check(a, b, torch.randn(N, generator=g).cuda(), "gelu", res, trans, sa, sb, out,
+          preact=K % 2 == 0)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("M,N,K", [(3, 200, 4100), (130, 300, 1000), (600, 520, 256),
+                                   (2304, 2304, 300)])
 def test_integers_are_exact(dt, M, N, K):
     g = np.random.default_rng(M)
     t = E4M3 if dt == "e4m3" else DTYPES[dt]

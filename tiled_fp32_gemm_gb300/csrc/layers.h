@@ -103,10 +103,12 @@ struct LinearArgs {
   BoundsRecord* bounds;
 };
 
-// What a product launches (linear_split.cu): CTA tiles of bc = 128 columns x
-// bt rows of Y, each computed by a cluster of `split` CTAs that take a slice
-// of K each and add their sums through distributed shared memory.
+// What a product launches.  pair: CTA pairs on tiles of 256 columns x 256
+// rows of Y (linear_pair.cu); else CTA tiles of bc = 128 columns x bt rows,
+// each computed by a cluster of `split` CTAs that take a slice of K each and
+// add their sums through distributed shared memory (linear_split.cu).
 struct LinearPlan {
+  int pair;
   int bt, bc, split, stages, threads;
   int64_t smem_bytes, grid;
   int64_t copy_x_bytes, copy_w_bytes;  // padded copies of operands TMA cannot read

@@ -1,0 +1,208 @@
+// Host side of the fused linear layer: padded copies of operands TMA cannot
+// read in place, the choice of kernel and its launch.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "layers.h"
+#include "linear.cuh"
+#include "tcgen05.cuh"
+
+namespace mt {
+namespace {
+
+using namespace linear;
+
+constexpr int kRowBytes = 128;  // K of one staged tile row, in bytes
+constexpr int kThreads = 192;
+constexpr int kMaxSplit = 8;    // CTAs of a cluster (portable size)
+constexpr int kPair = 256;      // columns and rows of Y per CTA pair
+
+// Padded copies of operands TMA cannot read in place (row pitch not a
+// multiple of 16 bytes, or base not 16-byte aligned): dst rows of `pitch`
+// bytes (a multiple of 16), the bytes past `bytes` zero.  E: element bytes,
+// which the source is aligned to.
+template <class T>
+__global__ void __launch_bounds__(256) copy_rows_kernel(const T* src, int64_t lds, uint8_t* dst,
+                                                        int64_t pitch, int64_t rows,
+                                                        int64_t cols) {
+  constexpr int N = 16 / sizeof(T);
+  const int64_t per_row = pitch / 16, total = rows * per_row;
+  for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < total;
+       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = e / per_row, c0 = (e % per_row) * N;
+    union {
+      T v[N];
+      uint4 u;
+    } o;
+    const T* s = src + r * lds;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o.v[i] = c0 + i < cols ? s[c0 + i] : T(0);
+    *reinterpret_cast<uint4*>(dst + r * pitch + (e % per_row) * 16) = o.u;
+  }
+}
+
+
+// The stored matrix of an operand: rows and columns in memory.
+struct Stored {
+  const void* p;
+  int64_t rows, cols, ld;
+};
+Stored stored_x(const LinearArgs& a) {
+  return a.x_mn ? Stored{a.X, a.K, a.T, a.ldx} : Stored{a.X, a.T, a.K, a.ldx};
+}
+Stored stored_w(const LinearArgs& a) {
+  return a.w_mn ? Stored{a.W, a.K, a.C, a.ldw} : Stored{a.W, a.C, a.K, a.ldw};
+}
+
+int64_t copy_pitch_bytes(int64_t cols, int elem) { return (cols * elem + 127) / 128 * 128; }
+
+int64_t copy_bytes(const Stored& m, int elem) {
+  if (tma_readable(m.p, m.ld, elem)) return 0;
+  return (m.rows * copy_pitch_bytes(m.cols, elem) + 255) / 256 * 256;
+}
+
+cudaError_t copy_operand(Stored* m, int elem, void* dst, cudaStream_t stream) {
+  const int64_t pitch = copy_pitch_bytes(m->cols, elem);
+  const int64_t work = m->rows * (pitch / 16);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(1216, (work + 255) / 256));
+  if (elem == 1)
+    copy_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint8_t*>(m->p), m->ld,
+                                               static_cast<uint8_t*>(dst), pitch, m->rows,
+                                               m->cols);
+  else
+    copy_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(m->p), m->ld,
+                                               static_cast<uint8_t*>(dst), pitch, m->rows,
+                                               m->cols);
+  m->p = dst;
+  m->ld = pitch / elem;
+  return cudaGetLastError();
+}
+
+bool encode(CUtensorMap* map, int dtype, const Stored& m, bool mn, int rows) {
+  const CUtensorMapDataType t = dtype == DT_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                : dtype == DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int elem = dtype_bytes(dtype);
+  return mn ? encode_tensor_map_2d(map, t, elem, m.p, m.rows, m.cols, m.ld, 64, 64,
+                                   CU_TENSOR_MAP_SWIZZLE_128B)
+            : encode_tensor_map_2d(map, t, elem, m.p, m.rows, m.cols, m.ld, 128 / elem,
+                                   rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+bool tma_readable(const void* p, int64_t ld, int elem) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * elem % 16 == 0 &&
+         ld * elem < (int64_t(1) << 39);
+}
+
+LinearPlan plan_linear(const LinearArgs& a, int sms) {
+  LinearPlan p{};
+  const int elem = dtype_bytes(a.dtype);
+  const int64_t ktiles = ceil_div(a.K * elem, kRowBytes);
+  p.threads = kThreads;
+  const int64_t pairs = ceil_div(a.C, kPair) * ceil_div(a.T, kPair);
+  // CTA pairs when their tiles come close to filling the GPU.
+  p.pair = a.K > 0 && pairs >= sms / 2;
+  if (p.pair) {
+    const LinearKernel k = linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn);
+    p.bt = p.bc = kPair;
+    p.split = 1;
+    p.stages = k.stages;
+    p.smem_bytes = k.smem;
+    p.grid = 2 * std::min<int64_t>(pairs, sms / 2);
+  } else {
+    p.bt = a.T <= 16 && !a.x_mn ? 16 : a.T <= 32 && !a.x_mn ? 32 : a.T <= 64 ? 64 : 128;
+    p.bc = LINEAR_BC;
+    const LinearKernel k = linear_split_kernel_for(a.dtype, p.bt, a.w_mn, a.x_mn);
+    const int64_t tiles = ceil_div(a.C, p.bc) * ceil_div(a.T, p.bt);
+    // Slices of K: as many CTAs as two per SM hold, each at least four K tiles.
+    const int64_t split = std::min<int64_t>({kMaxSplit, 2 * sms / tiles, ktiles / 4});
+    p.split = static_cast<int>(std::max<int64_t>(1, split));
+    p.stages = k.stages;
+    p.smem_bytes = k.smem;
+    p.grid = tiles * p.split;
+  }
+  p.copy_x_bytes = a.K > 0 ? copy_bytes(stored_x(a), elem) : 0;
+  p.copy_w_bytes = a.K > 0 ? copy_bytes(stored_w(a), elem) : 0;
+  p.workspace_bytes = p.copy_x_bytes + p.copy_w_bytes;
+  return p;
+}
+
+cudaError_t linear_prepare() {
+  for (int dtype : {DT_F16, DT_E4M3})
+    for (int bt : {16, 32, 64, 128, kPair})
+      for (int mn = 0; mn < 4; ++mn) {
+        const LinearKernel k = bt == kPair
+                                   ? linear_pair_kernel_for(dtype, mn & 1, mn >> 1)
+                                   : linear_split_kernel_for(dtype, bt, mn & 1, mn >> 1);
+        if (!k.kernel) continue;
+        const cudaError_t r =
+            cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        if (r != cudaSuccess) return r;
+      }
+  return cudaSuccess;
+}
+
+cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
+                          cudaStream_t stream, int fault_inject) {
+  const int elem = dtype_bytes(a.dtype);
+  Stored x = stored_x(a), w = stored_w(a);
+  char* ws = static_cast<char*>(workspace);
+  if (p.copy_x_bytes) {
+    const cudaError_t r = copy_operand(&x, elem, ws, stream);
+    if (r != cudaSuccess) return r;
+  }
+  if (p.copy_w_bytes) {
+    const cudaError_t r = copy_operand(&w, elem, ws + p.copy_x_bytes, stream);
+    if (r != cudaSuccess) return r;
+  }
+  const LinearKernel k = p.pair ? linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn)
+                                : linear_split_kernel_for(a.dtype, p.bt, a.w_mn, a.x_mn);
+  if (!k.kernel) return cudaErrorInvalidValue;
+  CUtensorMap map_w{}, map_x{};
+  // A pair's CTAs load half a tile of each operand; without a product (K = 0)
+  // the maps are not read.
+  const int box_w = p.pair ? kPair / 2 : p.bc, box_x = p.pair ? kPair / 2 : p.bt;
+  if (a.K > 0 && (!encode(&map_w, a.dtype, w, a.w_mn, box_w) ||
+                  !encode(&map_x, a.dtype, x, a.x_mn, box_x)))
+    return cudaErrorInvalidValue;
+  const uint32_t fmt = a.dtype == DT_BF16 ? 1u : 0u;  // f16 0, bf16 1; e4m3 0
+  uint32_t idesc = tc::instr_desc(p.bc, p.bt, fmt, fmt, a.w_mn ? 1u : 0u, a.x_mn ? 1u : 0u);
+  LinearEpilogue ep{a.Y, a.ldy, a.Z, a.ldz, a.residual, a.ldr, a.bias, a.row_scale, a.col_scale,
+                    static_cast<int>(a.T), static_cast<int>(a.C), a.out_dtype, a.act, a.bounds};
+  int kt = static_cast<int>(ceil_div(a.K * elem, kRowBytes));
+  if (p.pair)
+    return launch_linear_pair(k, map_w, map_x, idesc, ep, kt, static_cast<int>(p.grid / 2),
+                              fault_inject, stream);
+  int tiles_t = static_cast<int>(ceil_div(a.T, p.bt)), split = p.split;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&map_w, &map_x, &idesc, &ep, &kt, &tiles_t, &split, &fault_inject};
+  return cudaLaunchKernelExC(&cfg, k.kernel, args);
+}
+
+cudaError_t linear_read_and_clear_status(unsigned int* status) {
+  unsigned int split = 0, pair = 0;
+  cudaError_t e = linear_split_read_and_clear_status(&split);
+  if (e == cudaSuccess) e = linear_pair_read_and_clear_status(&pair);
+  *status = split | pair;
+  return e;
+}
+
+}  // namespace mt

@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include <cuda.h>
+
 #include "device_util.cuh"
 #include "layers.h"
 #include "row_util.cuh"
@@ -144,5 +146,24 @@ __device__ __forceinline__ void finish(const LinearEpilogue& e, int c, int t0, i
   store_rows(e, e.Y, e.ldy, c, t0, rows, v);
 }
 
+// A built kernel (kernel null: no such form), its dynamic shared memory and
+// pipeline stages.
+struct LinearKernel {
+  const void* kernel = nullptr;
+  int smem = 0, stages = 0;
+};
+
+constexpr int LINEAR_BC = 128;  // columns of Y per tile of the split kernels
+
 }  // namespace linear
+
+linear::LinearKernel linear_split_kernel_for(int dtype, int bt, bool w_mn, bool x_mn);
+cudaError_t linear_split_read_and_clear_status(unsigned int* status);
+linear::LinearKernel linear_pair_kernel_for(int dtype, bool w_mn, bool x_mn);
+cudaError_t launch_linear_pair(const linear::LinearKernel& k, const CUtensorMap& map_w,
+                               const CUtensorMap& map_x, uint32_t idesc,
+                               const linear::LinearEpilogue& ep, int kt, int clusters,
+                               int fault_inject, cudaStream_t stream);
+cudaError_t linear_pair_read_and_clear_status(unsigned int* status);
+
 }  // namespace mt

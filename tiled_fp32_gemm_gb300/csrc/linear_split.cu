@@ -14,9 +14,7 @@
 //     not depend on timing.
 // Every wait is bounded, as in the other tcgen05 kernels; a CTA that gave up
 // leaves its flag where its cluster sees it, and none of them stores.
-#include <algorithm>
 #include <cstdint>
-#include <mutex>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -30,8 +28,7 @@ namespace linear {
 
 using namespace f16tc;
 
-constexpr int BC = 128;  // columns of Y per tile
-constexpr int MAX_SPLIT = 8;
+constexpr int BC = LINEAR_BC;  // columns of Y per tile
 
 template <int BT_>
 struct SplitGeometry {
@@ -227,212 +224,47 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 }
 
-// ---------------------------------------------------------------------------
-// Padded copies of operands TMA cannot read in place (row pitch not a
-// multiple of 16 bytes, or base not 16-byte aligned): dst rows of `pitch`
-// bytes (a multiple of 16), the bytes past `bytes` zero.  E: element bytes,
-// which the source is aligned to.
-template <class T>
-__global__ void __launch_bounds__(256) copy_rows_kernel(const T* src, int64_t lds, uint8_t* dst,
-                                                        int64_t pitch, int64_t rows,
-                                                        int64_t cols) {
-  constexpr int N = 16 / sizeof(T);
-  const int64_t per_row = pitch / 16, total = rows * per_row;
-  for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < total;
-       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = e / per_row, c0 = (e % per_row) * N;
-    union {
-      T v[N];
-      uint4 u;
-    } o;
-    const T* s = src + r * lds;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = c0 + i < cols ? s[c0 + i] : T(0);
-    *reinterpret_cast<uint4*>(dst + r * pitch + (e % per_row) * 16) = o.u;
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Host side.
-
-namespace {
-
-// The stored matrix of an operand: rows and columns in memory.
-struct Stored {
-  const void* p;
-  int64_t rows, cols, ld;
-};
-Stored stored_x(const LinearArgs& a) {
-  return a.x_mn ? Stored{a.X, a.K, a.T, a.ldx} : Stored{a.X, a.T, a.K, a.ldx};
-}
-Stored stored_w(const LinearArgs& a) {
-  return a.w_mn ? Stored{a.W, a.K, a.C, a.ldw} : Stored{a.W, a.C, a.K, a.ldw};
-}
-
-int64_t copy_pitch_bytes(int64_t cols, int elem) { return (cols * elem + 127) / 128 * 128; }
-
-int64_t copy_bytes(const Stored& m, int elem) {
-  if (tma_readable(m.p, m.ld, elem)) return 0;
-  return (m.rows * copy_pitch_bytes(m.cols, elem) + 255) / 256 * 256;
-}
-
-cudaError_t copy_operand(Stored* m, int elem, void* dst, cudaStream_t stream) {
-  const int64_t pitch = copy_pitch_bytes(m->cols, elem);
-  const int64_t work = m->rows * (pitch / 16);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(1216, (work + 255) / 256));
-  if (elem == 1)
-    copy_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint8_t*>(m->p), m->ld,
-                                               static_cast<uint8_t*>(dst), pitch, m->rows,
-                                               m->cols);
-  else
-    copy_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(m->p), m->ld,
-                                               static_cast<uint8_t*>(dst), pitch, m->rows,
-                                               m->cols);
-  m->p = dst;
-  m->ld = pitch / elem;
-  return cudaGetLastError();
-}
-
-bool encode(CUtensorMap* map, int dtype, const Stored& m, bool mn, int rows) {
-  const CUtensorMapDataType t = dtype == DT_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                : dtype == DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const int elem = dtype_bytes(dtype);
-  return mn ? encode_tensor_map_2d(map, t, elem, m.p, m.rows, m.cols, m.ld, MN_BOX, BK,
-                                   CU_TENSOR_MAP_SWIZZLE_128B)
-            : encode_tensor_map_2d(map, t, elem, m.p, m.rows, m.cols, m.ld, ROW_BYTES / elem,
-                                   rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-struct SplitEntry {
-  const void* kernel;
-  int smem, stages;
-};
-
 template <class E, int BT, bool W_MN, bool X_MN>
-SplitEntry entry() {
-  return SplitEntry{reinterpret_cast<const void*>(linear_split_kernel<E, BT, W_MN, X_MN>),
-                    SplitGeometry<BT>::SMEM_BYTES, SplitGeometry<BT>::STAGES};
+LinearKernel entry() {
+  return LinearKernel{reinterpret_cast<const void*>(linear_split_kernel<E, BT, W_MN, X_MN>),
+                      SplitGeometry<BT>::SMEM_BYTES, SplitGeometry<BT>::STAGES};
 }
 
-// The built kernels: x_mn needs 64-row boxes and comes with w_mn only (the
-// weight gradient).
-bool split_entry(int dtype, int bt, bool w_mn, bool x_mn, SplitEntry* e) {
-  if (dtype == DT_E4M3) {
-    if (w_mn || x_mn) return false;
-    switch (bt) {
-      case 16: *e = entry<E4m3, 16, false, false>(); return true;
-      case 32: *e = entry<E4m3, 32, false, false>(); return true;
-      case 64: *e = entry<E4m3, 64, false, false>(); return true;
-      case 128: *e = entry<E4m3, 128, false, false>(); return true;
-    }
-    return false;
-  }
-  if (x_mn) {
-    if (!w_mn) return false;
-    switch (bt) {
-      case 64: *e = entry<Half, 64, true, true>(); return true;
-      case 128: *e = entry<Half, 128, true, true>(); return true;
-    }
-    return false;
-  }
+template <bool W_MN>
+LinearKernel entry_16(int bt) {
   switch (bt) {
-    case 16: *e = w_mn ? entry<Half, 16, true, false>() : entry<Half, 16, false, false>(); return true;
-    case 32: *e = w_mn ? entry<Half, 32, true, false>() : entry<Half, 32, false, false>(); return true;
-    case 64: *e = w_mn ? entry<Half, 64, true, false>() : entry<Half, 64, false, false>(); return true;
-    case 128: *e = w_mn ? entry<Half, 128, true, false>() : entry<Half, 128, false, false>(); return true;
+    case 16: return entry<Half, 16, W_MN, false>();
+    case 32: return entry<Half, 32, W_MN, false>();
+    case 64: return entry<Half, 64, W_MN, false>();
+    case 128: return entry<Half, 128, W_MN, false>();
   }
-  return false;
+  return LinearKernel{};
 }
 
-}  // namespace
 }  // namespace linear
 
 using namespace linear;
 
-bool tma_readable(const void* p, int64_t ld, int elem) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * elem % 16 == 0 &&
-         ld * elem < (int64_t(1) << 39);
-}
-
-LinearPlan plan_linear(const LinearArgs& a, int sms) {
-  LinearPlan p{};
-  const int elem = dtype_bytes(a.dtype);
-  p.bt = a.T <= 16 && !a.x_mn ? 16 : a.T <= 32 && !a.x_mn ? 32 : a.T <= 64 ? 64 : 128;
-  SplitEntry e{};
-  split_entry(a.dtype, p.bt, a.w_mn, a.x_mn, &e);
-  const int64_t tiles = ((a.C + BC - 1) / BC) * ((a.T + p.bt - 1) / p.bt);
-  const int64_t ktiles = (a.K * elem + ROW_BYTES - 1) / ROW_BYTES;
-  // Slices of K: as many CTAs as two per SM hold, each at least four K tiles.
-  const int64_t split = std::min<int64_t>({MAX_SPLIT, 2 * sms / tiles, ktiles / 4});
-  p.split = static_cast<int>(std::max<int64_t>(1, split));
-  p.bc = BC;
-  p.threads = THREADS;
-  p.stages = e.stages;
-  p.smem_bytes = e.smem;
-  p.grid = tiles * p.split;
-  p.copy_x_bytes = a.K > 0 ? copy_bytes(stored_x(a), elem) : 0;
-  p.copy_w_bytes = a.K > 0 ? copy_bytes(stored_w(a), elem) : 0;
-  p.workspace_bytes = p.copy_x_bytes + p.copy_w_bytes;
-  return p;
-}
-
-cudaError_t linear_prepare() {
-  for (int dtype : {DT_F16, DT_E4M3})
-    for (int bt : {16, 32, 64, 128})
-      for (int mn = 0; mn < 4; ++mn) {
-        SplitEntry e{};
-        if (!split_entry(dtype, bt, mn & 1, mn >> 1, &e)) continue;
-        const cudaError_t r =
-            cudaFuncSetAttribute(e.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, e.smem);
-        if (r != cudaSuccess) return r;
-      }
-  return cudaSuccess;
-}
-
-cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
-                          cudaStream_t stream, int fault_inject) {
-  const int elem = dtype_bytes(a.dtype);
-  Stored x = stored_x(a), w = stored_w(a);
-  char* ws = static_cast<char*>(workspace);
-  if (p.copy_x_bytes) {
-    const cudaError_t r = copy_operand(&x, elem, ws, stream);
-    if (r != cudaSuccess) return r;
+LinearKernel linear_split_kernel_for(int dtype, int bt, bool w_mn, bool x_mn) {
+  if (dtype == DT_E4M3) {
+    if (w_mn || x_mn) return LinearKernel{};
+    switch (bt) {
+      case 16: return entry<E4m3, 16, false, false>();
+      case 32: return entry<E4m3, 32, false, false>();
+      case 64: return entry<E4m3, 64, false, false>();
+      case 128: return entry<E4m3, 128, false, false>();
+    }
+    return LinearKernel{};
   }
-  if (p.copy_w_bytes) {
-    const cudaError_t r = copy_operand(&w, elem, ws + p.copy_x_bytes, stream);
-    if (r != cudaSuccess) return r;
-  }
-  SplitEntry e{};
-  if (!split_entry(a.dtype, p.bt, a.w_mn, a.x_mn, &e)) return cudaErrorInvalidValue;
-  CUtensorMap map_w{}, map_x{};
-  // Without a product (K = 0) the maps are not read.
-  if (a.K > 0 && (!encode(&map_w, a.dtype, w, a.w_mn, BC) ||
-                  !encode(&map_x, a.dtype, x, a.x_mn, p.bt)))
-    return cudaErrorInvalidValue;
-  const uint32_t fmt = a.dtype == DT_BF16 ? 1u : 0u;  // f16 0, bf16 1; e4m3 0
-  uint32_t idesc = tc::instr_desc(BC, p.bt, fmt, fmt, a.w_mn ? 1u : 0u, a.x_mn ? 1u : 0u);
-  LinearEpilogue ep{a.Y, a.ldy, a.Z, a.ldz, a.residual, a.ldr, a.bias, a.row_scale, a.col_scale,
-                    static_cast<int>(a.T), static_cast<int>(a.C), a.out_dtype, a.act, a.bounds};
-  int kt = static_cast<int>((a.K * elem + ROW_BYTES - 1) / ROW_BYTES);
-  int tiles_t = static_cast<int>((a.T + p.bt - 1) / p.bt), split = p.split;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.grid), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void* args[] = {&map_w, &map_x, &idesc, &ep, &kt, &tiles_t, &split, &fault_inject};
-  return cudaLaunchKernelExC(&cfg, e.kernel, args);
+  if (!x_mn) return w_mn ? entry_16<true>(bt) : entry_16<false>(bt);
+  // Transposed X comes with transposed W only (the weight gradient), and its
+  // boxes are 64 rows.
+  if (!w_mn) return LinearKernel{};
+  if (bt == 64) return entry<Half, 64, true, true>();
+  return bt == 128 ? entry<Half, 128, true, true>() : LinearKernel{};
 }
 
-cudaError_t linear_read_and_clear_status(unsigned int* status) {
+cudaError_t linear_split_read_and_clear_status(unsigned int* status) {
   cudaError_t e = cudaMemcpyFromSymbol(status, f16tc::g_status, sizeof(unsigned int));
   if (e != cudaSuccess) return e;
   const unsigned int zero = 0;
