@@ -474,7 +474,8 @@ typedef enum {
     MT_SITE_SLICE_SUM = 9,  /* shared read or write of a K group's sum */
     MT_SITE_PREP_SRC = 10,  /* global read of an operand by the copy kernel */
     MT_SITE_PREP_DST = 11,  /* global write of an operand copy */
-    MT_SITE_P18 = 12        /* any access of the one-warp kernel */
+    MT_SITE_P18 = 12,       /* any access of the one-warp kernel */
+    MT_SITE_ROWS = 13       /* any access of the row-wise kernels of mt_layers.h */
 } mt_bounds_site;
 
 /*

@@ -58,6 +58,7 @@ MT_DTYPE_BF16 = 2
 MT_SITE_A_LOAD, MT_SITE_B_LOAD, MT_SITE_A_SMEM, MT_SITE_B_SMEM = 1, 2, 3, 4
 MT_SITE_FRAG, MT_SITE_C_STORE, MT_SITE_PARTIAL, MT_SITE_BIAS = 5, 6, 7, 8
 MT_SITE_SLICE_SUM, MT_SITE_PREP_SRC, MT_SITE_PREP_DST, MT_SITE_P18 = 9, 10, 11, 12
+MT_SITE_ROWS = 13
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libmtsgemm.so")
 CHECKED_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "checked",

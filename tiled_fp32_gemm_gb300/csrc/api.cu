@@ -1484,7 +1484,8 @@ static_assert(MT_SITE_A_LOAD == mt::SITE_A_LOAD && MT_SITE_B_LOAD == mt::SITE_B_
                   MT_SITE_PARTIAL == mt::SITE_PARTIAL && MT_SITE_BIAS == mt::SITE_BIAS &&
                   MT_SITE_SLICE_SUM == mt::SITE_SLICE_SUM &&
                   MT_SITE_PREP_SRC == mt::SITE_PREP_SRC &&
-                  MT_SITE_PREP_DST == mt::SITE_PREP_DST && MT_SITE_P18 == mt::SITE_P18,
+                  MT_SITE_PREP_DST == mt::SITE_PREP_DST && MT_SITE_P18 == mt::SITE_P18 &&
+                  MT_SITE_ROWS == mt::SITE_ROWS,
               "site numbers of the header and the kernels");
 
 mt_status mt_bounds_status(int64_t* count, int* site, int64_t* offset, int64_t* extent) {

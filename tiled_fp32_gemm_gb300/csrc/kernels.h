@@ -33,7 +33,8 @@ enum BoundsSite {
   SITE_SLICE_SUM = 9,   // shared read or write of a K group's sum
   SITE_PREP_SRC = 10,   // global read of an operand by the copy kernel
   SITE_PREP_DST = 11,   // global write of an operand copy
-  SITE_P18 = 12         // any access of the one-warp kernel
+  SITE_P18 = 12,        // any access of the one-warp kernel
+  SITE_ROWS = 13        // any access of a row-wise kernel (norm, gradient of an activation)
 };
 
 // One compiled FFMA tile configuration and its kernel instantiations.

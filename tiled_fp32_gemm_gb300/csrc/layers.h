@@ -37,7 +37,7 @@ struct RmsNormArgs {
   BoundsRecord* bounds;
 };
 
-cudaError_t launch_rms_norm(const RmsNormArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t stream);
 
 // rms_norm_grad.cu.  See mt_rms_norm_backward_args for the operator.
 struct RmsNormGradArgs {
@@ -66,7 +66,7 @@ cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, void* workspace, int 
 
 // Adds `count` rows of `cols` floats (packed, in row order) to out[cols].
 cudaError_t launch_add_rows(const float* rows, int count, int cols, float* out,
-                            cudaStream_t stream);
+                            BoundsRecord* bounds, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // The fused product of the linear layer and of its gradient:

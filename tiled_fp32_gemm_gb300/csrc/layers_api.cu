@@ -168,7 +168,7 @@ mt_status mt_rms_norm(const mt_rms_norm_args* g, cudaStream_t stream) {
                           g->weight, g->h, g->ldh, g->y, g->ldy, g->scale, g->rstd, g->eps,
                           g->dtype, e4m3 ? 1 : 0, g->weight_dtype == MT_DTYPE_F32 ? 1 : 0,
                           bounds_record()};
-  if (mt::launch_rms_norm(a, info.sms, stream) != cudaSuccess) {
+  if (mt::launch_rms_norm(a, stream) != cudaSuccess) {
     cudaGetLastError();
     return MT_ERR_LAUNCH;
   }

@@ -62,7 +62,7 @@ cudaError_t launch(const LinearDzArgs& a, float* partial, int sms, cudaStream_t 
       <<<dim3((a.N + 31) / 32, blocks), 32 * kWarps, 0, stream>>>(a, per, partial);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.dbias) return e;
-  return launch_add_rows(partial, blocks, a.N, a.dbias, stream);
+  return launch_add_rows(partial, blocks, a.N, a.dbias, a.bounds, stream);
 }
 
 template <class T>

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,6 +47,179 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
+
+// A strided matrix a row-wise kernel reads or writes.  Eight consecutive
+// values move as 16-byte accesses (8 bytes for e4m3): the caller has checked
+// the alignment of every such column of every row.  The checked build tests
+// each access.
+template <class T>
+struct Matrix {
+  T* p;
+  int64_t ld, extent;
+  BoundsRecord* rec;
+
+  __device__ __forceinline__ bool ok(int64_t at, int width) const {
+    return bounds_ok(rec, SITE_ROWS, at, width, extent);
+  }
+  __device__ __forceinline__ float load(int64_t row, int col) const {
+    const int64_t at = row * ld + col;
+    return ok(at, 1) ? to_f32(p[at]) : 0.0f;
+  }
+  __device__ __forceinline__ void store(int64_t row, int col, float v) const {
+    const int64_t at = row * ld + col;
+    if (ok(at, 1)) p[at] = from_f32<T>(v);
+  }
+};
+
+// Eight values of a storage type as they lie in memory.
+template <class T>
+struct Pack8;
+template <>
+struct Pack8<float> {
+  float4 lo, hi;
+  __device__ __forceinline__ void keep() {}
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    lo = make_float4(v[0], v[1], v[2], v[3]);
+    hi = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+template <>
+struct Pack8<__half> {
+  uint4 u;
+  __device__ __forceinline__ void keep() {
+    asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Pack8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void keep() {
+    asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// A thread's E values of a row that `threads` threads share: eight
+// consecutive ones per step (VEC) or one, threads side by side.
+template <int E, bool VEC>
+struct Slots {
+  static constexpr int STEP = VEC ? 8 : 1;
+  static constexpr int COUNT = E / STEP;
+  static __device__ __forceinline__ int col(int i, int tid, int threads) {
+    return (i * threads + tid) * STEP;
+  }
+};
+
+// What a thread holds of a row of a matrix, unconverted.
+template <class T, int E, bool VEC>
+struct Held {
+  using S = Slots<E, VEC>;
+  using Item = typename std::conditional<VEC, Pack8<T>, T>::type;
+  Item item[S::COUNT];
+
+  __device__ __forceinline__ void load(const Matrix<const T>& m, int64_t row, int d, int tid,
+                                       int threads) {
+#pragma unroll
+    for (int i = 0; i < S::COUNT; ++i) {
+      const int c = S::col(i, tid, threads);
+      const int64_t at = row * m.ld + c;
+      if (c < d && m.ok(at, S::STEP)) item[i] = *reinterpret_cast<const Item*>(m.p + at);
+      else item[i] = Item{};
+    }
+  }
+  // Between two uses: the packed form is what stays in registers (else the
+  // compiler keeps the first use's fp32 values for the second).
+  __device__ __forceinline__ void keep() {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < S::COUNT; ++i) item[i].keep();
+    }
+  }
+  // The values of step i, in order.
+  __device__ __forceinline__ void get(int i, float (&v)[S::STEP]) const {
+    if constexpr (VEC) item[i].get(v);
+    else v[0] = to_f32(item[i]);
+  }
+};
+
+template <class T, bool VEC>
+__device__ __forceinline__ void store_step(const Matrix<T>& m, int64_t row, int c,
+                                           const float (&v)[VEC ? 8 : 1]) {
+  const int64_t at = row * m.ld + c;
+  if (!m.ok(at, VEC ? 8 : 1)) return;
+  if constexpr (VEC) {
+    Pack8<T> o;
+    o.set(v);
+    *reinterpret_cast<Pack8<T>*>(m.p + at) = o;
+  } else {
+    m.p[at] = from_f32<T>(v[0]);
+  }
+}
+
+// Whether every eighth column of every row is aligned for Pack8.
+inline bool rows_aligned(const void* p, int64_t ld, int elem) {
+  const int unit = elem == 1 ? 8 : 16;
+  return reinterpret_cast<uintptr_t>(p) % unit == 0 && ld * elem % unit == 0;
+}
+
+// Calls f(threads per row, values per thread) with the smallest row layout
+// that holds d values, at most MOST values a thread where threads allow;
+// false when d is past the widest.
+template <int MOST, class F>
+bool row_layout(int d, F&& f) {
+  using std::integral_constant;
+  auto go = [&](auto threads, auto values) { f(threads, values); return true; };
+  if (d <= 256) return go(integral_constant<int, 32>{}, integral_constant<int, 8>{});
+  if (d <= 64 * MOST) return go(integral_constant<int, 64>{}, integral_constant<int, MOST>{});
+  if (d <= 128 * MOST) return go(integral_constant<int, 128>{}, integral_constant<int, MOST>{});
+  if (d <= 256 * MOST) return go(integral_constant<int, 256>{}, integral_constant<int, MOST>{});
+  if (d <= 512 * MOST) return go(integral_constant<int, 512>{}, integral_constant<int, MOST>{});
+  if (d <= 1024 * MOST) return go(integral_constant<int, 1024>{}, integral_constant<int, MOST>{});
+  if (d <= 16384) return go(integral_constant<int, 1024>{}, integral_constant<int, 16>{});
+  return false;
+}
+
+// Rows a CTA works on at a time: one, or one per warp when a warp holds a
+// row.
+constexpr int rows_per_cta(int threads) { return threads == 32 ? 4 : 1; }
 
 }  // namespace row
 }  // namespace mt
