@@ -105,72 +105,97 @@ def mt_linear_backward(args: mt_linear_backward_args, stream: int = 0) -> int:
 
 
 # --- torch convenience (marshalling only) ------------------------------------
+# What a call needs of torch and the library, looked up at the first call:
+# for a few tokens the host's time is what a call takes.
+_torch = None
 _codes = {}
+_FLOATS = _HALVES = _F32 = _F8 = None
+_empty = _raw_stream = _device_now = None
+_functions = {}
 
 
-def _dtype_codes():
-    if not _codes:
-        import torch
-        _codes.update({torch.float16: 1, torch.bfloat16: 2, torch.float32: MT_DTYPE_F32,
-                       torch.float8_e4m3fn: MT_DTYPE_E4M3})
-    return _codes
+def _setup():
+    global _torch, _FLOATS, _HALVES, _F32, _F8, _empty, _raw_stream, _device_now
+    import torch
+    from . import lib
+    handle = lib()
+    for name in SIGNATURES:
+        _functions[name] = getattr(handle, name)
+    _codes.update({torch.float16: 1, torch.bfloat16: 2, torch.float32: MT_DTYPE_F32,
+                   torch.float8_e4m3fn: MT_DTYPE_E4M3})
+    _HALVES = (torch.float16, torch.bfloat16)
+    _FLOATS = (*_HALVES, torch.float32)
+    _F32, _F8 = torch.float32, torch.float8_e4m3fn
+    _empty, _device_now = torch.empty, torch.cuda.current_device
+    # The current stream's handle without building a Stream object.
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+
+
+def _first(t, name, dtypes):
+    """(rows, columns, dtype, device) of the operand whose device and type the
+    others follow."""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return shape[0], shape[1], t.dtype, t.device
 
 
 def _matrix(t, name, rows, cols, dtype, device):
     """(pointer, row pitch) of a rows x cols CUDA matrix with unit column
     stride; any pitch that holds a row serves a single row."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+    if not isinstance(t, _torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a {dtype} CUDA tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {rows} x {cols}")
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    if rows <= 1 or ld < 1:
-        if rows > 1:
-            raise ValueError(f"{name}'s rows overlap")
-        ld = max(cols, 1)
+    if rows <= 1:
+        ld = cols or 1
+    elif ld < 1:
+        raise ValueError(f"{name}'s rows overlap")
     return t.data_ptr(), ld
 
 
 def _vector(t, name, n, dtypes, device):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+    if not isinstance(t, _torch.Tensor) or t.dtype not in dtypes or not t.is_cuda:
         raise TypeError(f"{name} must be a {' or '.join(map(str, dtypes))} CUDA tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n}")
     return t.data_ptr()
 
 
-def _first(t, name, dtypes):
-    """Checks of the operand whose device and type the others follow."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
+def _result(out, name, rows, cols, dtype, device):
+    """(tensor, pointer, row pitch): `out` checked, or a new matrix."""
+    if out is None:
+        out = _empty((rows, cols), dtype=dtype, device=device)
+        return out, out.data_ptr(), cols or 1
+    return (out, *_matrix(out, name, rows, cols, dtype, device))
 
 
-def _call(fn, packed, device, stream):
+def _call(name, packed, device, stream):
     """Runs one packed C call on the operands' device and stream."""
-    import torch
-    from . import MT_OK, MtError, lib
-    s = stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
-    f = getattr(lib(), fn)
-    if device.index == torch.cuda.current_device():
-        st = f(packed, s)
+    index = device.index
+    if stream is None:
+        stream = _raw_stream(index)
+    if index == _device_now():
+        st = _functions[name](packed, stream)
     else:
-        with torch.cuda.device(device):
-            st = f(packed, s)
-    if st != MT_OK:
-        raise MtError(st, fn)
+        with _torch.cuda.device(device):
+            st = _functions[name](packed, stream)
+    if st:
+        from . import MtError
+        raise MtError(st, name)
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, out=None, h_out=None,
@@ -186,40 +211,34 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, out=None, h_out
     itself when there is no residual), rstd the float32 reciprocal norms
     that ``rms_norm_backward`` takes.  ``out`` and ``h_out`` receive y (or q)
     and h when given; h_out may be residual or x."""
-    import torch
-    codes = _dtype_codes()
-    _first(x, "x", (torch.float16, torch.bfloat16, torch.float32))
-    rows, d = x.shape
-    dt, dev = x.dtype, x.device
-    e4m3 = out_dtype == torch.float8_e4m3fn
+    if _torch is None:
+        _setup()
+    rows, d, dt, dev = _first(x, "x", _FLOATS)
     if out_dtype is None:
         out_dtype = dt
-    elif not e4m3 and out_dtype != dt:
+    elif out_dtype != dt and out_dtype != _F8:
         raise TypeError("out_dtype must be x's dtype or torch.float8_e4m3fn")
     xp, ldx = _matrix(x, "x", rows, d, dt, dev)
     rp = ldr = hp = ldh = wp = sp = wcode = 0
     if weight is not None:
-        wp = _vector(weight, "weight", d, (dt, torch.float32), dev)
-        wcode = codes[weight.dtype]
+        wp = _vector(weight, "weight", d, (dt, _F32), dev)
+        wcode = _codes[weight.dtype]
     h = x
     if residual is not None:
         rp, ldr = _matrix(residual, "residual", rows, d, dt, dev)
-        h = torch.empty((rows, d), dtype=dt, device=dev) if h_out is None else h_out
-        hp, ldh = _matrix(h, "h_out", rows, d, dt, dev)
+        h, hp, ldh = _result(h_out, "h_out", rows, d, dt, dev)
     elif h_out is not None:
         raise ValueError("h_out needs a residual")
-    y = torch.empty((rows, d), dtype=out_dtype, device=dev) if out is None else out
-    yp, ldy = _matrix(y, "out", rows, d, out_dtype, dev)
-    # One allocation: the reciprocal norms, then the scales.
-    stats = torch.empty((2 if e4m3 else 1, rows), dtype=torch.float32, device=dev)
-    rstd = stats[0]
-    if e4m3:
-        scale = stats[1]
+    y, yp, ldy = _result(out, "out", rows, d, out_dtype, dev)
+    rstd = _empty(rows, dtype=_F32, device=dev)
+    scale = None
+    if out_dtype == _F8:
+        scale = _empty(rows, dtype=_F32, device=dev)
         sp = scale.data_ptr()
     _call("mt_rms_norm",
           _pack_rms_norm(rows, d, xp, ldx, rp, ldr, wp, hp, ldh, yp, ldy, sp, rstd.data_ptr(),
-                         eps, codes[dt], codes[out_dtype], wcode), dev, stream)
-    return (y, scale, h, rstd) if e4m3 else (y, h, rstd)
+                         eps, _codes[dt], _codes[out_dtype], wcode), dev, stream)
+    return (y, h, rstd) if scale is None else (y, scale, h, rstd)
 
 
 def rms_norm_backward(dy, h, weight, rstd, dh=None, need_weight=True, out=None, stream=None):
@@ -231,29 +250,26 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, need_weight=True, out=None, 
     dtype, is the gradient of x and of the residual alike; dweight is
     float32 (None when ``need_weight`` is false).  ``out`` receives dx when
     given and may be dy or dh."""
-    import torch
-    codes = _dtype_codes()
-    _first(dy, "dy", (torch.float16, torch.bfloat16, torch.float32))
-    rows, d = dy.shape
-    dt, dev = dy.dtype, dy.device
+    if _torch is None:
+        _setup()
+    rows, d, dt, dev = _first(dy, "dy", _FLOATS)
     dyp, lddy = _matrix(dy, "dy", rows, d, dt, dev)
     hp, ldh = _matrix(h, "h", rows, d, dt, dev)
-    rp = _vector(rstd, "rstd", rows, (torch.float32,), dev)
+    rp = _vector(rstd, "rstd", rows, (_F32,), dev)
     wp = wcode = dhp = lddh = dwp = 0
     if weight is not None:
-        wp = _vector(weight, "weight", d, (dt, torch.float32), dev)
-        wcode = codes[weight.dtype]
+        wp = _vector(weight, "weight", d, (dt, _F32), dev)
+        wcode = _codes[weight.dtype]
     if dh is not None:
         dhp, lddh = _matrix(dh, "dh", rows, d, dt, dev)
-    dx = torch.empty((rows, d), dtype=dt, device=dev) if out is None else out
-    dxp, lddx = _matrix(dx, "out", rows, d, dt, dev)
+    dx, dxp, lddx = _result(out, "out", rows, d, dt, dev)
     dweight = None
     if need_weight:
-        dweight = torch.empty(d, dtype=torch.float32, device=dev)
+        dweight = _empty(d, dtype=_F32, device=dev)
         dwp = dweight.data_ptr()
     _call("mt_rms_norm_backward",
           _pack_rms_norm_backward(rows, d, dyp, lddy, hp, ldh, wp, rp, dhp, lddh, dxp, lddx, dwp,
-                                  codes[dt], wcode), dev, stream)
+                                  _codes[dt], wcode), dev, stream)
     return dx, dweight
 
 
@@ -279,44 +295,46 @@ def linear(a, b, bias=None, activation=None, residual=None, trans_b=False, scale
     allowed.  Returns the output (``out`` when given, which may be the
     residual), or ``(output, z)`` with the pre-activation z in the output's
     dtype when ``preact`` is set."""
-    import torch
-    codes = _dtype_codes()
-    _first(a, "a", (torch.float16, torch.bfloat16, torch.float8_e4m3fn))
-    M, K = a.shape
-    dt, dev = a.dtype, a.device
-    if not isinstance(b, torch.Tensor) or b.dim() != 2:
+    if _torch is None:
+        _setup()
+    M, K, dt, dev = _first(a, "a", (*_HALVES, _F8))
+    if not isinstance(b, _torch.Tensor) or b.dim() != 2:
         raise ValueError("b must be a 2-D CUDA tensor")
-    N = b.shape[0] if trans_b else b.shape[1]
     ap, lda = _matrix(a, "a", M, K, dt, dev)
-    bp, ldb = _matrix(b, "b", *((N, K) if trans_b else (K, N)), dt, dev)
     bias_p = rp = ldr = zp = ldz = sap = sbp = 0
-    if dt == torch.float8_e4m3fn:
+    if trans_b:
+        N = b.shape[0]
+        bp, ldb = _matrix(b, "b", N, K, dt, dev)
+    else:
+        N = b.shape[1]
+        bp, ldb = _matrix(b, "b", K, N, dt, dev)
+    if dt == _F8:
         if not trans_b:
             raise ValueError("8-bit inputs need b stored N x K (trans_b)")
-        sap = _vector(scale_a, "scale_a", M, (torch.float32,), dev)
-        sbp = _vector(scale_b, "scale_b", N, (torch.float32,), dev)
-        out_dtype = out_dtype or torch.bfloat16
-        if out_dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        sap = _vector(scale_a, "scale_a", M, (_F32,), dev)
+        sbp = _vector(scale_b, "scale_b", N, (_F32,), dev)
+        out_dtype = out_dtype or _torch.bfloat16
+        if out_dtype not in _FLOATS:
             raise TypeError("out_dtype must be float16, bfloat16 or float32")
     else:
         if scale_a is not None or scale_b is not None:
             raise ValueError("scales go with float8_e4m3fn inputs")
-        out_dtype = out_dtype or dt
-        if out_dtype not in (dt, torch.float32):
+        if out_dtype is None:
+            out_dtype = dt
+        elif out_dtype != dt and out_dtype != _F32:
             raise TypeError("out_dtype must be a's dtype or float32")
     if bias is not None:
-        bias_p = _vector(bias, "bias", N, (torch.float32,), dev)
+        bias_p = _vector(bias, "bias", N, (_F32,), dev)
     if residual is not None:
         rp, ldr = _matrix(residual, "residual", M, N, out_dtype, dev)
-    y = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
-    yp, ldy = _matrix(y, "out", M, N, out_dtype, dev)
+    y, yp, ldy = _result(out, "out", M, N, out_dtype, dev)
+    z = None
     if preact:
-        z = torch.empty((M, N), dtype=out_dtype, device=dev)
-        zp, ldz = z.data_ptr(), max(N, 1)
+        z, zp, ldz = _result(None, "z", M, N, out_dtype, dev)
     _call("mt_linear",
           _pack_linear(M, N, K, ap, lda, bp, ldb, yp, ldy, zp, ldz, rp, ldr, bias_p, sap, sbp,
-                       int(trans_b), codes[dt], codes[out_dtype], _activation(activation), 0, 0),
-          dev, stream)
+                       1 if trans_b else 0, _codes[dt], _codes[out_dtype],
+                       _activation(activation), 0, 0), dev, stream)
     return (y, z) if preact else y
 
 
@@ -330,37 +348,34 @@ def linear_backward(dy, a, b, z=None, activation=None, trans_b=False, need_a=Tru
     pre-activation (needed unless ``activation`` is None); a, b, ``trans_b``
     as there.  da has a's dtype, db is stored as b in ``db_dtype`` (a's, or
     float32), dbias is float32."""
-    import torch
-    codes = _dtype_codes()
-    _first(dy, "dy", (torch.float16, torch.bfloat16))
-    M, N = dy.shape
-    dt, dev = dy.dtype, dy.device
+    if _torch is None:
+        _setup()
+    M, N, dt, dev = _first(dy, "dy", _HALVES)
     act = _activation(activation)
-    if not isinstance(a, torch.Tensor) or a.dim() != 2:
+    if not isinstance(a, _torch.Tensor) or a.dim() != 2:
         raise ValueError("a must be a 2-D CUDA tensor")
     K = a.shape[1]
-    db_dtype = db_dtype or dt
-    if db_dtype not in (dt, torch.float32):
+    if db_dtype is None:
+        db_dtype = dt
+    elif db_dtype != dt and db_dtype != _F32:
         raise TypeError("db_dtype must be a's dtype or float32")
     dyp, lddy = _matrix(dy, "dy", M, N, dt, dev)
     ap, lda = _matrix(a, "a", M, K, dt, dev)
-    shape = (N, K) if trans_b else (K, N)
-    bp, ldb = _matrix(b, "b", *shape, dt, dev)
-    zp = ldz = dap = dbp = dbiasp = 0
+    rows, cols = (N, K) if trans_b else (K, N)
+    bp, ldb = _matrix(b, "b", rows, cols, dt, dev)
+    zp = ldz = dap = ldda = dbp = lddb = dbiasp = 0
     if act != MT_ACT_NONE:
         zp, ldz = _matrix(z, "z", M, N, dt, dev)
     da = db = dbias = None
     if need_a:
-        da = torch.empty((M, K), dtype=dt, device=dev)
-        dap = da.data_ptr()
+        da, dap, ldda = _result(None, "da", M, K, dt, dev)
     if need_b:
-        db = torch.empty(shape, dtype=db_dtype, device=dev)
-        dbp = db.data_ptr()
+        db, dbp, lddb = _result(None, "db", rows, cols, db_dtype, dev)
     if need_bias:
-        dbias = torch.empty(N, dtype=torch.float32, device=dev)
+        dbias = _empty(N, dtype=_F32, device=dev)
         dbiasp = dbias.data_ptr()
     _call("mt_linear_backward",
-          _pack_linear_backward(M, N, K, dyp, lddy, zp, ldz, ap, lda, bp, ldb, dap, max(K, 1),
-                                dbp, max(shape[1], 1), dbiasp, int(trans_b), codes[dt],
-                                codes[db_dtype], act), dev, stream)
+          _pack_linear_backward(M, N, K, dyp, lddy, zp, ldz, ap, lda, bp, ldb, dap, ldda, dbp,
+                                lddb, dbiasp, 1 if trans_b else 0, _codes[dt],
+                                _codes[db_dtype], act), dev, stream)
     return da, db, dbias
