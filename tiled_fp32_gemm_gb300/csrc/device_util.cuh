@@ -38,6 +38,18 @@ __device__ __forceinline__ bool bounds_ok(BoundsRecord* rec, int site, int64_t o
 #endif
 }
 
+// Programmatic dependent launch (the kernels of mt_layers.h): a kernel lets
+// the next one in its stream be launched as soon as its own CTAs run, and
+// touches nothing in global memory before the kernel before it has completed
+// and its writes are visible.  Both are no-ops in a launch without the
+// attribute.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // The pair kernel's drain of a tile of C: alpha, beta, bias and mask, or a
 // K slice's partial tile.
 struct CUpdate {
+  static constexpr bool DEPENDENT_LAUNCH = false;
   Epilogue ep;
   __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int lane,
                                              const Sched& sched, float* square,

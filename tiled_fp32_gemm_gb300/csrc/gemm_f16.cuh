@@ -69,6 +69,17 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
+// Prefetches the same tile to L2.
+template <int ROWS, bool MN>
+__device__ __forceinline__ void prefetch_operand(const CUtensorMap* map, int r0, int k0) {
+  if constexpr (!MN) {
+    tma_prefetch_2d(map, k0, r0);
+  } else {
+#pragma unroll
+    for (int c = 0; c < ROWS / MN_BOX; ++c) tma_prefetch_2d(map, r0 + c * MN_BOX, k0);
+  }
+}
+
 // Descriptor of k-step j (32 bytes of K: 16 16-bit or 32 8-bit values) of an
 // operand tile at `base`.
 template <bool MN>
@@ -96,6 +107,8 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int j) {
 // E: the element type (Half or E4m3); drain(t_row, unit, q, lane, sched,
 // square, rank) takes the 32 x 256 accumulator of warp q's lanes at TMEM
 // address t_row (rows q * 32 .. of CTA `rank`'s half) to memory.
+// Drain::DEPENDENT_LAUNCH: the kernel is launched as a programmatic dependent
+// and lets its own dependents launch early.
 // ACC_BUFS accumulators of 256 columns each (1 or 2) sit in TMEM.
 constexpr int PAIR_TILE = 256;
 constexpr int PAIR_HALF = 128;
@@ -165,6 +178,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (Drain::DEPENDENT_LAUNCH) {
+    grid_launch_dependents();
+    grid_wait();
+  }
 
   if (warp == 0) {
     if (lane == 0) {

@@ -265,4 +265,11 @@ cudaError_t launch_f16tc(const GemmArgs& a, const F16Operands& f, void* workspac
                          int bm, int bn, int max_ctas, int fault_inject, cudaStream_t stream);
 cudaError_t f16tc_read_and_clear_status(unsigned int* status);
 
+// ---------------------------------------------------------------------------
+// Launches a kernel that calls grid_wait as a programmatic dependent of the
+// kernel before it on `stream` (see device_util.cuh), in clusters of
+// `cluster` CTAs.
+cudaError_t launch_dependent(const void* kernel, dim3 grid, int block, int64_t smem, int cluster,
+                             cudaStream_t stream, void** args);
+
 }  // namespace mt

@@ -15,6 +15,15 @@ enum DType { DT_F16 = 1, DT_BF16 = 2, DT_F32 = 3, DT_E4M3 = 4 };
 
 inline int dtype_bytes(int t) { return t == DT_F32 ? 4 : t == DT_E4M3 ? 1 : 2; }
 
+// launch_dependent with typed arguments, no cluster and no dynamic shared
+// memory.
+template <class... P>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int block, cudaStream_t stream,
+                             P... args) {
+  void* list[] = {&args...};
+  return launch_dependent(reinterpret_cast<const void*>(kernel), grid, block, 0, 1, stream, list);
+}
+
 // rms_norm.cu.  See mt_rms_norm_args for the operator.
 struct RmsNormArgs {
   int64_t rows;

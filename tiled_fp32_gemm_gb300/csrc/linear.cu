@@ -29,6 +29,8 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const T* src, int64_t ld
                                                         int64_t pitch, int64_t rows,
                                                         int64_t cols) {
   constexpr int N = 16 / sizeof(T);
+  grid_launch_dependents();
+  grid_wait();
   const int64_t per_row = pitch / 16, total = rows * per_row;
   for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < total;
        e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -68,17 +70,16 @@ cudaError_t copy_operand(Stored* m, int elem, void* dst, cudaStream_t stream) {
   const int64_t pitch = copy_pitch_bytes(m->cols, elem);
   const int64_t work = m->rows * (pitch / 16);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(1216, (work + 255) / 256));
-  if (elem == 1)
-    copy_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint8_t*>(m->p), m->ld,
-                                               static_cast<uint8_t*>(dst), pitch, m->rows,
-                                               m->cols);
-  else
-    copy_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(m->p), m->ld,
-                                               static_cast<uint8_t*>(dst), pitch, m->rows,
-                                               m->cols);
+  const cudaError_t e =
+      elem == 1 ? launch_dependent(copy_rows_kernel<uint8_t>, grid, 256, stream,
+                                   static_cast<const uint8_t*>(m->p), m->ld,
+                                   static_cast<uint8_t*>(dst), pitch, m->rows, m->cols)
+                : launch_dependent(copy_rows_kernel<uint16_t>, grid, 256, stream,
+                                   static_cast<const uint16_t*>(m->p), m->ld,
+                                   static_cast<uint8_t*>(dst), pitch, m->rows, m->cols);
   m->p = dst;
   m->ld = pitch / elem;
-  return cudaGetLastError();
+  return e;
 }
 
 bool encode(CUtensorMap* map, int dtype, const Stored& m, bool mn, int rows) {
@@ -107,8 +108,8 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
   const int64_t ktiles = ceil_div(a.K * elem, kRowBytes);
   p.threads = kThreads;
   const int64_t pairs = ceil_div(a.C, kPair) * ceil_div(a.T, kPair);
-  // CTA pairs when their tiles come close to filling the GPU.
-  p.pair = a.K > 0 && pairs >= sms / 2;
+  // CTA pairs when their tiles fill the GPU, and with tokens, not with padding.
+  p.pair = a.K > 0 && pairs >= sms / 2 && a.T > 128;
   if (p.pair) {
     const LinearKernel k = linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn);
     p.bt = p.bc = kPair;
@@ -142,8 +143,12 @@ cudaError_t linear_prepare() {
                                    ? linear_pair_kernel_for(dtype, mn & 1, mn >> 1)
                                    : linear_split_kernel_for(dtype, bt, mn & 1, mn >> 1);
         if (!k.kernel) continue;
-        const cudaError_t r =
+        cudaError_t r =
             cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        // Without this the SM is configured for one CTA's shared memory.
+        if (r == cudaSuccess)
+          r = cudaFuncSetAttribute(k.kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                   cudaSharedmemCarveoutMaxShared);
         if (r != cudaSuccess) return r;
       }
   return cudaSuccess;
@@ -181,20 +186,9 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* worksp
     return launch_linear_pair(k, map_w, map_x, idesc, ep, kt, static_cast<int>(p.grid / 2),
                               fault_inject, stream);
   int tiles_t = static_cast<int>(ceil_div(a.T, p.bt)), split = p.split;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.grid), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   void* args[] = {&map_w, &map_x, &idesc, &ep, &kt, &tiles_t, &split, &fault_inject};
-  return cudaLaunchKernelExC(&cfg, k.kernel, args);
+  return launch_dependent(k.kernel, dim3(static_cast<unsigned>(p.grid)), kThreads, p.smem_bytes,
+                          split, stream, args);
 }
 
 cudaError_t linear_read_and_clear_status(unsigned int* status) {

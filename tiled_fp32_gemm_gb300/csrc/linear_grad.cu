@@ -23,6 +23,8 @@ __global__ void __launch_bounds__(32 * kWarps) linear_dz_kernel(const LinearDzAr
                                                                 int64_t rows_per_block,
                                                                 float* partial) {
   __shared__ float sums[kWarps][32];
+  grid_launch_dependents();
+  grid_wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + lane;
   const int64_t first = blockIdx.y * rows_per_block;
@@ -58,9 +60,9 @@ template <class T, int ACT>
 cudaError_t launch(const LinearDzArgs& a, float* partial, int sms, cudaStream_t stream) {
   const int blocks = row_blocks(a, sms);
   const int64_t per = (a.M + blocks - 1) / blocks;
-  linear_dz_kernel<T, ACT>
-      <<<dim3((a.N + 31) / 32, blocks), 32 * kWarps, 0, stream>>>(a, per, partial);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(linear_dz_kernel<T, ACT>,
+                                         dim3((a.N + 31) / 32, blocks), 32 * kWarps, stream, a,
+                                         per, partial);
   if (e != cudaSuccess || !a.dbias) return e;
   return launch_add_rows(partial, blocks, a.N, a.dbias, a.bounds, stream);
 }

@@ -19,6 +19,7 @@ using namespace f16tc;
 // Takes warp q's 32 columns of Y, 256 rows, from tensor memory to Y while the
 // next tile's MMAs run on the other accumulator.
 struct PairDrain {
+  static constexpr bool DEPENDENT_LAUNCH = true;
   LinearEpilogue ep;
   __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int lane,
                                              const Sched&, float*, int rank) const {
@@ -63,22 +64,11 @@ cudaError_t launch_linear_pair(const LinearKernel& k, const CUtensorMap& map_w,
   int tiles_c = (ep.C + PAIR_TILE - 1) / PAIR_TILE, tiles_t = (ep.T + PAIR_TILE - 1) / PAIR_TILE;
   int group = 8;
   Sched sched{tiles_c * tiles_t, 1, kt, nullptr, 0, 0};
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(clusters), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   CUtensorMap w = map_w, x = map_x;
   void* args[] = {&w,       &x,       &idesc, &drain, &kt,
                   &tiles_c, &tiles_t, &group, &sched, &fault_inject};
-  return cudaLaunchKernelExC(&cfg, k.kernel, args);
+  return launch_dependent(k.kernel, dim3(2 * static_cast<unsigned>(clusters)), THREADS, k.smem, 2,
+                          stream, args);
 }
 
 cudaError_t linear_pair_read_and_clear_status(unsigned int* status) {

@@ -28,6 +28,7 @@ namespace linear {
 
 using namespace f16tc;
 
+constexpr int PREFETCH_STAGES = 1;  // rings of the weight's tiles prefetched to L2
 constexpr int BC = LINEAR_BC;  // columns of Y per tile
 
 template <int BT_>
@@ -115,6 +116,13 @@ __global__ void __launch_bounds__(THREADS, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_launch_dependents();
+  // While the kernel before this one ends, the first of the weight's tiles
+  // travel to L2 (a hint: nothing is read before grid_wait).
+  if (warp == 0 && lane == 0)
+    for (int kt = kt0; kt < min(kt1, kt0 + PREFETCH_STAGES * STAGES); ++kt)
+      prefetch_operand<BC, W_MN>(&tmap_w, c0, kt * BK_ELEMS);
+  grid_wait();
 
   float* const sums = reinterpret_cast<float*>(smem);  // [row][column], over the ring
   int issued = 0;  // producer: K tiles issued

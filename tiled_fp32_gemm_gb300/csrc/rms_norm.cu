@@ -71,6 +71,8 @@ template <class T, class W, bool E4M3, int THREADS, int E, bool VEC>
 __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS))
     rms_norm_kernel(const RmsNormArgs a, const Operands<T> o, const Matrix<const W> weight) {
   using S = Slots<E, VEC>;
+  grid_launch_dependents();
+  grid_wait();
   const int tid = threadIdx.x % THREADS;
   const int64_t row =
       static_cast<int64_t>(blockIdx.x) * rows_per_cta(THREADS) + threadIdx.x / THREADS;
@@ -140,6 +142,8 @@ template <class T, class W, bool E4M3>
 __global__ void __launch_bounds__(kWideThreads)
     rms_norm_wide_kernel(const RmsNormArgs a, const Operands<T> o,
                          const Matrix<const W> weight) {
+  grid_launch_dependents();
+  grid_wait();
   const int64_t row = blockIdx.x;
   auto load = [&](int c) {
     return o.x.load(row, c) + (a.residual ? o.residual.load(row, c) : 0.0f);
@@ -185,21 +189,19 @@ cudaError_t launch(const RmsNormArgs& a, cudaStream_t stream) {
                    rows_aligned(a.h, a.h ? a.ldh : 0, e) &&
                    rows_aligned(a.y, a.ldy, E4M3 ? 1 : e) &&
                    rows_aligned(a.weight, 0, sizeof(W));
+  cudaError_t err = cudaSuccess;
   const bool held = row_layout<16>(a.d, [&](auto threads, auto values) {
     constexpr int THREADS = decltype(threads)::value, E = decltype(values)::value;
     constexpr int ROWS = rows_per_cta(THREADS);
-    const unsigned grid = static_cast<unsigned>((n + ROWS - 1) / ROWS);
-    if (vec)
-      rms_norm_kernel<T, W, E4M3, THREADS, E, true>
-          <<<grid, THREADS * ROWS, 0, stream>>>(a, o, weight);
-    else
-      rms_norm_kernel<T, W, E4M3, THREADS, E, false>
-          <<<grid, THREADS * ROWS, 0, stream>>>(a, o, weight);
+    err = launch_dependent(vec ? rms_norm_kernel<T, W, E4M3, THREADS, E, true>
+                               : rms_norm_kernel<T, W, E4M3, THREADS, E, false>,
+                           static_cast<unsigned>((n + ROWS - 1) / ROWS), THREADS * ROWS, stream,
+                           a, o, weight);
   });
   if (!held)
-    rms_norm_wide_kernel<T, W, E4M3>
-        <<<static_cast<unsigned>(n), kWideThreads, 0, stream>>>(a, o, weight);
-  return cudaGetLastError();
+    err = launch_dependent(rms_norm_wide_kernel<T, W, E4M3>, static_cast<unsigned>(n),
+                           kWideThreads, stream, a, o, weight);
+  return err;
 }
 
 template <class T>

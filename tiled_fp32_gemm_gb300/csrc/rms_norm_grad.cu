@@ -60,6 +60,8 @@ __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS),
       r = o.rstd.load(row, 0);
     }
   };
+  grid_launch_dependents();
+  grid_wait();
   Held<W, E, VEC> w;
   if (a.weight) w.load(weight, 0, a.d, tid, THREADS);
   float dw[S::COUNT][S::STEP];
@@ -132,6 +134,8 @@ __global__ void __launch_bounds__(kWideThreads)
     rms_norm_grad_wide_kernel(const RmsNormGradArgs a, const Operands<T> o,
                               const Matrix<const W> weight) {
   __shared__ float part[kWideThreads / 32];
+  grid_launch_dependents();
+  grid_wait();
   const int64_t row = blockIdx.x;
   auto weight_at = [&](int c) { return a.weight ? weight.load(0, c) : 1.0f; };
   const float r = o.rstd.load(row, 0);
@@ -160,6 +164,8 @@ __global__ void __launch_bounds__(32 * kColumnWarps)
     rms_norm_grad_columns_kernel(const RmsNormGradArgs a, const Operands<T> o,
                                  int64_t rows_per_block) {
   __shared__ float sums[kColumnWarps][32];
+  grid_launch_dependents();
+  grid_wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + lane;
   const int64_t first = blockIdx.y * rows_per_block;
@@ -183,6 +189,8 @@ __global__ void __launch_bounds__(1024) add_rows_kernel(const Matrix<const float
                                                         int count, int cols,
                                                         const Matrix<float> out) {
   __shared__ float sums[32][33];
+  grid_launch_dependents();
+  grid_wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
@@ -246,27 +254,25 @@ cudaError_t launch(const RmsNormGradArgs& a, float* partial, int sms, cudaStream
   const Matrix<const W> weight{static_cast<const W*>(a.weight), 0, a.d, a.bounds};
   const bool vec = vectored<T, W>(a);
   const int sm = vec ? sm_threads<T, true>() : sm_threads<T, false>();
+  cudaError_t err = cudaSuccess;
   const bool held = row_layout<8>(a.d, [&](auto threads, auto values) {
     constexpr int THREADS = decltype(threads)::value, E = decltype(values)::value;
     const int ctas = held_ctas(a, THREADS, sm, sms), block = THREADS * rows_per_cta(THREADS);
     parts = ctas * rows_per_cta(THREADS);
-    if (vec)
-      rms_norm_grad_kernel<T, W, THREADS, E, true><<<ctas, block, 0, stream>>>(a, o, weight);
-    else
-      rms_norm_grad_kernel<T, W, THREADS, E, false><<<ctas, block, 0, stream>>>(a, o, weight);
+    err = launch_dependent(vec ? rms_norm_grad_kernel<T, W, THREADS, E, true>
+                               : rms_norm_grad_kernel<T, W, THREADS, E, false>,
+                           ctas, block, stream, a, o, weight);
   });
   if (!held) {
     // The column sums come first: dx may overwrite dy.
     if (a.dweight)
-      rms_norm_grad_columns_kernel<T>
-          <<<dim3((a.d + 31) / 32, parts), 32 * kColumnWarps, 0, stream>>>(
-              a, o, (n + parts - 1) / parts);
-    if (n > 0)
-      rms_norm_grad_wide_kernel<T, W>
-          <<<static_cast<unsigned>(n), kWideThreads, 0, stream>>>(a, o, weight);
+      err = launch_dependent(rms_norm_grad_columns_kernel<T>, dim3((a.d + 31) / 32, parts),
+                             32 * kColumnWarps, stream, a, o, (n + parts - 1) / parts);
+    if (err == cudaSuccess && n > 0)
+      err = launch_dependent(rms_norm_grad_wide_kernel<T, W>, static_cast<unsigned>(n),
+                             kWideThreads, stream, a, o, weight);
   }
-  const cudaError_t e2 = cudaGetLastError();
-  if (e2 != cudaSuccess || !a.dweight) return e2;
+  if (err != cudaSuccess || !a.dweight) return err;
   return launch_add_rows(partial, parts, a.d, a.dweight, a.bounds, stream);
 }
 
@@ -281,10 +287,10 @@ cudaError_t launch_weight(const RmsNormGradArgs& a, float* partial, int sms,
 
 cudaError_t launch_add_rows(const float* rows, int count, int cols, float* out,
                             BoundsRecord* bounds, cudaStream_t stream) {
-  add_rows_kernel<<<(cols + 31) / 32, 1024, 0, stream>>>(
-      {rows, cols, static_cast<int64_t>(count) * cols, bounds}, count, cols,
-      {out, cols, cols, bounds});
-  return cudaGetLastError();
+  return launch_dependent(
+      add_rows_kernel, dim3((cols + 31) / 32), 1024, stream,
+      Matrix<const float>{rows, cols, static_cast<int64_t>(count) * cols, bounds}, count, cols,
+      Matrix<float>{out, cols, cols, bounds});
 }
 
 int64_t rms_norm_grad_workspace(const RmsNormGradArgs& a, int sms) {

@@ -83,6 +83,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
       : "memory");
 }
 
+// The same box into L2 only (a hint; completes on no barrier).
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
@@ -340,12 +348,16 @@ struct WaitCtx {
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const WaitCtx& w,
                                            bool honour_abort = true,
                                            uint64_t limit_ns = TIMEOUT_NS) {
-  const uint64_t t0 = globaltimer();
+  // The clock is read only once a wait has failed several times: reading it
+  // takes long next to a phase that is (almost) complete.
+  uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 15u) == 15u) {
       if (honour_abort && *w.abort_flag) return false;
-      if (globaltimer() - t0 > limit_ns) {
+      const uint64_t now = globaltimer();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
         *w.abort_flag = 1;
         atomicOr(w.status, 1u);
         return false;
