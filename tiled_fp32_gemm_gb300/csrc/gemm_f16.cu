@@ -221,9 +221,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 // K slice's partial tile.
 struct CUpdate {
   static constexpr bool DEPENDENT_LAUNCH = false;
+  static constexpr int WARPS = 4;
   Epilogue ep;
-  __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int lane,
-                                             const Sched& sched, float* square,
+  __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int /*half*/,
+                                             int lane, const Sched& sched, float* square,
                                              int rank) const {
     store_accumulator<PAIR_HALF, PAIR_TILE, PAIR_TILE>(t_row, w, q, lane, ep, sched.partial,
                                                        square, rank * PAIR_HALF);

@@ -102,11 +102,12 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int j) {
 //   even CTA, warp 1: per K tile 4 pair MMAs 256 x 256 x 16, then a commit
 //     multicast to empty[s] of both CTAs, and after a unit's last K tile to
 //     acc_full[b] of both;
-//   both CTAs, warps 2-5: drain their own TMEM half (128 rows x 256) to
+//   both CTAs, warps 2 on: drain their own TMEM half (128 rows x 256) to
 //     memory, then one arrival per warp on the even CTA's acc_empty[b].
-// E: the element type (Half or E4m3); drain(t_row, unit, q, lane, sched,
+// E: the element type (Half or E4m3); drain(t_row, unit, q, half, lane, sched,
 // square, rank) takes the 32 x 256 accumulator of warp q's lanes at TMEM
-// address t_row (rows q * 32 .. of CTA `rank`'s half) to memory.
+// address t_row (rows q * 32 .. of CTA `rank`'s half) to memory; with
+// Drain::WARPS = 8 two warps share it (half 0 and 1).
 // Drain::DEPENDENT_LAUNCH: the kernel is launched as a programmatic dependent
 // and lets its own dependents launch early.
 // ACC_BUFS accumulators of 256 columns each (1 or 2) sit in TMEM.
@@ -126,8 +127,14 @@ struct PairGeometry {
                                    EPI_STAGE_BYTES;
 };
 
+// Threads of the pair kernel: the copy warp, the MMA warp, the drain's warps.
+template <class Drain>
+constexpr int pair_threads() {
+  return 64 + 32 * Drain::WARPS;
+}
+
 template <class E, bool A_MN, bool B_MN, int ACC_BUFS, class Drain>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(pair_threads<Drain>(), 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 const __grid_constant__ CUtensorMap tmap_b, uint32_t idesc, Drain drain, int Kt,
                 int tiles_m, int tiles_n, int group_m, Sched sched, int fault_inject) {
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < ACC_BUFS; ++b) {
       mbar_init(bar(ACC_FULL + b), 1);   // pair MMA commit
-      mbar_init(bar(ACC_EMPTY + b), 8);  // one arrival per epilogue warp of both CTAs
+      mbar_init(bar(ACC_EMPTY + b), 2 * Drain::WARPS);  // every epilogue warp of both CTAs
     }
     mbar_init(bar(DRAIN), 1);
     *abort_flag = 0;
@@ -272,8 +279,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       __syncwarp();
       const Unit w = unit_at(u, cluster, clusters, sched, tiles_m, tiles_n, group_m, Kt);
-      drain(tmem + lane_base + static_cast<uint32_t>(b * PAIR_TILE), w, q, lane, sched,
-            epi_square, static_cast<int>(rank));
+      drain(tmem + lane_base + static_cast<uint32_t>(b * PAIR_TILE), w, q, (warp - 2) / 4, lane,
+            sched, epi_square, static_cast<int>(rank));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty_even + 8u * static_cast<uint32_t>(b));

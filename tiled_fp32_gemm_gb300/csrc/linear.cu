@@ -16,8 +16,7 @@ namespace {
 using namespace linear;
 
 constexpr int kRowBytes = 128;  // K of one staged tile row, in bytes
-constexpr int kThreads = 192;
-constexpr int kMaxSplit = 8;    // CTAs of a cluster (portable size)
+constexpr int kThreads = 192, kPairThreads = 320;
 constexpr int kPair = 256;      // columns and rows of Y per CTA pair
 
 // Padded copies of operands TMA cannot read in place (row pitch not a
@@ -95,6 +94,22 @@ bool encode(CUtensorMap* map, int dtype, const Stored& m, bool mn, int rows) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// CTAs that share a tile's K, each at least four K tiles.  Two CTAs fit an SM
+// (clusters of 3 or 4 reach nine tenths of those places, clusters of 8 three
+// quarters); a second round of CTAs costs more than slices gain, and past
+// four slices the clusters' barriers cost more than they save unless a CTA
+// has an SM to itself.  Measured (bf16, one token, weight N x K, us by
+// slices 1 / 2 / 4 / 8): 8192 x 4096 20.3 / 16.2 / 15.2 / 23.5; 4096 x 4096
+// 19.9 / 13.5 / 10.9 / 12.1; 19456 x 4096 28.1 / 27.4 / 38.2 / 53.6;
+// 1024 x 1024 6.6 / 5.9 / 5.6 / 6.9; 128 x 8192 36.1 / 21.2 / 13.2 / 10.4.
+int split_of(int64_t tiles, int64_t ktiles, int sms) {
+  const int64_t most = ktiles / 4;
+  if (most >= 8 && tiles * 8 <= sms * 3 / 4) return 8;
+  for (int s = 4; s > 1; --s)
+    if (s <= most && tiles * s <= (s > 2 ? 2 * sms * 9 / 10 : 2 * sms)) return s;
+  return 1;
+}
+
 }  // namespace
 
 bool tma_readable(const void* p, int64_t ld, int elem) {
@@ -106,12 +121,16 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
   LinearPlan p{};
   const int elem = dtype_bytes(a.dtype);
   const int64_t ktiles = ceil_div(a.K * elem, kRowBytes);
-  p.threads = kThreads;
   const int64_t pairs = ceil_div(a.C, kPair) * ceil_div(a.T, kPair);
-  // CTA pairs when their tiles fill the GPU, and with tokens, not with padding.
-  p.pair = a.K > 0 && pairs >= sms / 2 && a.T > 128;
+  // CTA pairs when their tiles fill three tenths of the GPU, and with tokens,
+  // not padding.  Measured (bf16, gelu, bias and residual, N = K = 4096, us
+  // for pairs against the split kernel): 512 tokens (32 pairs) 32.0 / 28.0,
+  // 768 (48) 33.1 / 38.5, 1024 (64) 33.2 / 39.0, 2048 (128) 55.1 / 74.7;
+  // e4m3 512 tokens 23.9 / 21.5, 768 25.2 / 27.1, 2048 38.8 / 52.4.
+  p.pair = a.K > 0 && 10 * pairs >= 3 * sms && a.T > 128;
   if (p.pair) {
     const LinearKernel k = linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn);
+    p.threads = kPairThreads;
     p.bt = p.bc = kPair;
     p.split = 1;
     p.stages = k.stages;
@@ -120,11 +139,10 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
   } else {
     p.bt = a.T <= 16 && !a.x_mn ? 16 : a.T <= 32 && !a.x_mn ? 32 : a.T <= 64 ? 64 : 128;
     p.bc = LINEAR_BC;
+    p.threads = kThreads;
     const LinearKernel k = linear_split_kernel_for(a.dtype, p.bt, a.w_mn, a.x_mn);
     const int64_t tiles = ceil_div(a.C, p.bc) * ceil_div(a.T, p.bt);
-    // Slices of K: as many CTAs as two per SM hold, each at least four K tiles.
-    const int64_t split = std::min<int64_t>({kMaxSplit, 2 * sms / tiles, ktiles / 4});
-    p.split = static_cast<int>(std::max<int64_t>(1, split));
+    p.split = split_of(tiles, ktiles, sms);
     p.stages = k.stages;
     p.smem_bytes = k.smem;
     p.grid = tiles * p.split;

@@ -16,22 +16,20 @@ namespace linear {
 
 using namespace f16tc;
 
-// Takes warp q's 32 columns of Y, 256 rows, from tensor memory to Y while the
-// next tile's MMAs run on the other accumulator.
+// Takes warp q's 32 columns of Y from tensor memory to Y while the next
+// tile's MMAs run on the other accumulator; two warps share the 256 rows of
+// a column block.
 struct PairDrain {
   static constexpr bool DEPENDENT_LAUNCH = true;
+  static constexpr int WARPS = 8;
   LinearEpilogue ep;
-  __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int lane,
-                                             const Sched&, float*, int rank) const {
+  __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int half,
+                                             int lane, const Sched&, float*, int rank) const {
     const int c = w.tm * PAIR_TILE + rank * PAIR_HALF + q * 32 + lane;
-    const int t0 = w.tn * PAIR_TILE;
-    const int rows = min(PAIR_TILE, ep.T - t0);
-#pragma unroll 1
-    for (int t = 0; t < rows; t += FINISH_ROWS) {
-      Rows v;
-      tmem_ld16(t_row + t, v);
-      finish(ep, c, t0 + t, ep.T, v);
-    }
+    const int t0 = w.tn * PAIR_TILE, first = t0 + half * PAIR_HALF;
+    const int last = min(ep.T, first + PAIR_HALF);
+    if (first < last)
+      finish(ep, c, first, last, [&](int row, Rows& v) { tmem_ld16(t_row + (row - t0), v); });
   }
 };
 
@@ -67,7 +65,8 @@ cudaError_t launch_linear_pair(const LinearKernel& k, const CUtensorMap& map_w,
   CUtensorMap w = map_w, x = map_x;
   void* args[] = {&w,       &x,       &idesc, &drain, &kt,
                   &tiles_c, &tiles_t, &group, &sched, &fault_inject};
-  return launch_dependent(k.kernel, dim3(2 * static_cast<unsigned>(clusters)), THREADS, k.smem, 2,
+  return launch_dependent(k.kernel, dim3(2 * static_cast<unsigned>(clusters)),
+                          pair_threads<PairDrain>(), k.smem, 2,
                           stream, args);
 }
 

@@ -194,24 +194,22 @@ __global__ void __launch_bounds__(THREADS, 2)
     const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int rows = min(BT, ep.T - t0), per = (rows + split - 1) / split;
     const int first = rank * per, last = min(rows, first + per);
-#pragma unroll 1
-    for (int t = first; t < last; t += FINISH_ROWS) {
-      Rows v;
+    finish(ep, c0 + c, t0 + first, t0 + last, [&](int row, Rows& v) {
+      const int t = row - t0;
       if (split == 1) {
         load_sums(t_row + t, kt1 > kt0, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < FINISH_ROWS; ++i) v[i] = 0.0f;
-#pragma unroll 1
-        for (int s = 0; s < split; ++s) {
-          const uint32_t from = map_to_cta(smem_u32(sums + t * BC + c), s);
-#pragma unroll
-          for (int i = 0; i < FINISH_ROWS; ++i)
-            if (t + i < last) v[i] += ld_cluster_f32(from + i * BC * 4);
-        }
+        return;
       }
-      finish(ep, c0 + c, t0 + t, t0 + last, v);
-    }
+#pragma unroll
+      for (int i = 0; i < FINISH_ROWS; ++i) v[i] = 0.0f;
+#pragma unroll 1
+      for (int s = 0; s < split; ++s) {
+        const uint32_t from = map_to_cta(smem_u32(sums + t * BC + c), s);
+#pragma unroll
+        for (int i = 0; i < FINISH_ROWS; ++i)
+          if (t + i < last) v[i] += ld_cluster_f32(from + i * BC * 4);
+      }
+    });
   }
   if (split > 1) {
     __syncwarp();
