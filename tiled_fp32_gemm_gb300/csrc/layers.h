@@ -125,10 +125,17 @@ struct LinearPlan {
 };
 
 LinearPlan plan_linear(const LinearArgs& a, int sms);
-// Shared-memory limits of the kernels, once per device.
+// Two products that do not depend on one another: planned for one launch when
+// both take the split kernel.
+void plan_linear_two(const LinearArgs& a, const LinearArgs& b, int sms, LinearPlan* pa,
+                     LinearPlan* pb);
+// Attributes of the kernels, once per device.
 cudaError_t linear_prepare();
 cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
                           cudaStream_t stream, int fault_inject = 0);
+cudaError_t launch_linear_two(const LinearArgs& a, const LinearPlan& pa, void* wa,
+                              const LinearArgs& b, const LinearPlan& pb, void* wb,
+                              cudaStream_t stream);
 cudaError_t linear_read_and_clear_status(unsigned int* status);
 
 // Whether TMA reads a matrix of `elem`-byte values in place: 16-byte aligned

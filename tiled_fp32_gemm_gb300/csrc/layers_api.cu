@@ -354,8 +354,13 @@ mt_status mt_linear_backward(const mt_linear_backward_args* g, cudaStream_t stre
   };
   bind(make_dz ? nullptr : g->dY, make_dz ? lddz : g->lddy);
   mt::LinearPlan plan_a{}, plan_b{};
-  if (want_a) plan_a = mt::plan_linear(pa, info.sms);
-  if (want_b) plan_b = mt::plan_linear(pb, info.sms);
+  // Planned as if both were wanted: a gradient's bits do not depend on which
+  // others are asked for.
+  if (M > 0 && N > 0 && K > 0) mt::plan_linear_two(pa, pb, info.sms, &plan_a, &plan_b);
+  else if (want_a) plan_a = mt::plan_linear(pa, info.sms);
+  else if (want_b) plan_b = mt::plan_linear(pb, info.sms);
+  if (!want_a) plan_a.workspace_bytes = 0;
+  if (!want_b) plan_b.workspace_bytes = 0;
   if (plan_a.grid > INT32_MAX || plan_b.grid > INT32_MAX) return MT_ERR_UNSUPPORTED;
   Scratch ws(stream);
   st = ws.get(dev, dz_bytes + sum_bytes + plan_a.workspace_bytes + plan_b.workspace_bytes);
@@ -368,9 +373,13 @@ mt_status mt_linear_backward(const mt_linear_backward_args* g, cudaStream_t stre
   cudaError_t e = cudaSuccess;
   if (make_dz || want_bias) e = mt::launch_linear_dz(dz, base + dz_bytes, info.sms, stream);
   char* wa = base + dz_bytes + sum_bytes;
-  if (e == cudaSuccess && want_a) e = mt::launch_linear(pa, plan_a, wa, stream);
-  if (e == cudaSuccess && want_b)
-    e = mt::launch_linear(pb, plan_b, wa + plan_a.workspace_bytes, stream);
+  char* wb = wa + plan_a.workspace_bytes;
+  if (e == cudaSuccess && want_a && want_b)
+    e = mt::launch_linear_two(pa, plan_a, wa, pb, plan_b, wb, stream);
+  else if (e == cudaSuccess && want_a)
+    e = mt::launch_linear(pa, plan_a, wa, stream);
+  else if (e == cudaSuccess && want_b)
+    e = mt::launch_linear(pb, plan_b, wb, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return MT_ERR_LAUNCH;

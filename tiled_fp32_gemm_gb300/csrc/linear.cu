@@ -110,6 +110,23 @@ int split_of(int64_t tiles, int64_t ktiles, int sms) {
   return 1;
 }
 
+int64_t ktiles_of(const LinearArgs& a) {
+  return ceil_div(a.K * dtype_bytes(a.dtype), kRowBytes);
+}
+int64_t split_tiles(const LinearArgs& a, int bt) {
+  return ceil_div(a.C, LINEAR_BC) * ceil_div(a.T, bt);
+}
+
+// Sets the fields of a split-kernel plan that its tile and split decide.
+void use_split(const LinearArgs& a, int bt, int split, LinearPlan* p) {
+  const LinearKernel k = linear_split_kernel_for(a.dtype, bt);
+  p->bt = bt;
+  p->split = split;
+  p->stages = k.stages;
+  p->smem_bytes = k.smem;
+  p->grid = split_tiles(a, bt) * split;
+}
+
 }  // namespace
 
 bool tma_readable(const void* p, int64_t ld, int elem) {
@@ -120,7 +137,6 @@ bool tma_readable(const void* p, int64_t ld, int elem) {
 LinearPlan plan_linear(const LinearArgs& a, int sms) {
   LinearPlan p{};
   const int elem = dtype_bytes(a.dtype);
-  const int64_t ktiles = ceil_div(a.K * elem, kRowBytes);
   const int64_t pairs = ceil_div(a.C, kPair) * ceil_div(a.T, kPair);
   // CTA pairs when their tiles fill three tenths of the GPU, and with tokens,
   // not padding.  Measured (bf16, gelu, bias and residual, N = K = 4096, us
@@ -137,15 +153,10 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
     p.smem_bytes = k.smem;
     p.grid = 2 * std::min<int64_t>(pairs, sms / 2);
   } else {
-    p.bt = a.T <= 16 && !a.x_mn ? 16 : a.T <= 32 && !a.x_mn ? 32 : a.T <= 64 ? 64 : 128;
+    const int bt = a.T <= 16 && !a.x_mn ? 16 : a.T <= 32 && !a.x_mn ? 32 : a.T <= 64 ? 64 : 128;
     p.bc = LINEAR_BC;
     p.threads = kThreads;
-    const LinearKernel k = linear_split_kernel_for(a.dtype, p.bt, a.w_mn, a.x_mn);
-    const int64_t tiles = ceil_div(a.C, p.bc) * ceil_div(a.T, p.bt);
-    p.split = split_of(tiles, ktiles, sms);
-    p.stages = k.stages;
-    p.smem_bytes = k.smem;
-    p.grid = tiles * p.split;
+    use_split(a, bt, split_of(split_tiles(a, bt), ktiles_of(a), sms), &p);
   }
   p.copy_x_bytes = a.K > 0 ? copy_bytes(stored_x(a), elem) : 0;
   p.copy_w_bytes = a.K > 0 ? copy_bytes(stored_w(a), elem) : 0;
@@ -153,27 +164,51 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
   return p;
 }
 
-cudaError_t linear_prepare() {
-  for (int dtype : {DT_F16, DT_E4M3})
-    for (int bt : {16, 32, 64, 128, kPair})
-      for (int mn = 0; mn < 4; ++mn) {
-        const LinearKernel k = bt == kPair
-                                   ? linear_pair_kernel_for(dtype, mn & 1, mn >> 1)
-                                   : linear_split_kernel_for(dtype, bt, mn & 1, mn >> 1);
-        if (!k.kernel) continue;
-        cudaError_t r =
-            cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-        // Without this the SM is configured for one CTA's shared memory.
-        if (r == cudaSuccess)
-          r = cudaFuncSetAttribute(k.kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                   cudaSharedmemCarveoutMaxShared);
-        if (r != cudaSuccess) return r;
-      }
-  return cudaSuccess;
+void plan_linear_two(const LinearArgs& a, const LinearArgs& b, int sms, LinearPlan* pa,
+                     LinearPlan* pb) {
+  *pa = plan_linear(a, sms);
+  *pb = plan_linear(b, sms);
+  if (pa->pair || pb->pair) return;
+  const int bt = std::max(pa->bt, pb->bt);
+  const int split = split_of(split_tiles(a, bt) + split_tiles(b, bt),
+                             std::min(ktiles_of(a), ktiles_of(b)), sms);
+  use_split(a, bt, split, pa);
+  use_split(b, bt, split, pb);
 }
 
-cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
-                          cudaStream_t stream, int fault_inject) {
+cudaError_t linear_prepare() {
+  auto prepare = [](const LinearKernel& k) {
+    if (!k.kernel) return cudaSuccess;
+    cudaError_t r =
+        cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    // Two CTAs of the split kernel share an SM.
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(k.kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    return r;
+  };
+  cudaError_t r = cudaSuccess;
+  for (int dtype : {DT_F16, DT_E4M3}) {
+    for (int bt : {16, 32, 64, 128})
+      if (r == cudaSuccess) r = prepare(linear_split_kernel_for(dtype, bt));
+    for (int mn = 0; mn < 4; ++mn)
+      if (r == cudaSuccess) r = prepare(linear_pair_kernel_for(dtype, mn & 1, mn >> 1));
+  }
+  return r;
+}
+
+namespace {
+
+// A product ready to launch: its operands in a form TMA reads.
+struct Ready {
+  CUtensorMap map_w, map_x;
+  LinearEpilogue ep;
+  uint32_t idesc;
+};
+
+// Copies what TMA cannot read in place and encodes the maps.
+cudaError_t make_ready(const LinearArgs& a, const LinearPlan& p, void* workspace,
+                       cudaStream_t stream, Ready* out) {
   const int elem = dtype_bytes(a.dtype);
   Stored x = stored_x(a), w = stored_w(a);
   char* ws = static_cast<char*>(workspace);
@@ -185,28 +220,67 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* worksp
     const cudaError_t r = copy_operand(&w, elem, ws + p.copy_x_bytes, stream);
     if (r != cudaSuccess) return r;
   }
-  const LinearKernel k = p.pair ? linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn)
-                                : linear_split_kernel_for(a.dtype, p.bt, a.w_mn, a.x_mn);
-  if (!k.kernel) return cudaErrorInvalidValue;
-  CUtensorMap map_w{}, map_x{};
   // A pair's CTAs load half a tile of each operand; without a product (K = 0)
   // the maps are not read.
   const int box_w = p.pair ? kPair / 2 : p.bc, box_x = p.pair ? kPair / 2 : p.bt;
-  if (a.K > 0 && (!encode(&map_w, a.dtype, w, a.w_mn, box_w) ||
-                  !encode(&map_x, a.dtype, x, a.x_mn, box_x)))
+  if (a.K > 0 && (!encode(&out->map_w, a.dtype, w, a.w_mn, box_w) ||
+                  !encode(&out->map_x, a.dtype, x, a.x_mn, box_x)))
     return cudaErrorInvalidValue;
   const uint32_t fmt = a.dtype == DT_BF16 ? 1u : 0u;  // f16 0, bf16 1; e4m3 0
-  uint32_t idesc = tc::instr_desc(p.bc, p.bt, fmt, fmt, a.w_mn ? 1u : 0u, a.x_mn ? 1u : 0u);
-  LinearEpilogue ep{a.Y, a.ldy, a.Z, a.ldz, a.residual, a.ldr, a.bias, a.row_scale, a.col_scale,
-                    static_cast<int>(a.T), static_cast<int>(a.C), a.out_dtype, a.act, a.bounds};
-  int kt = static_cast<int>(ceil_div(a.K * elem, kRowBytes));
+  out->idesc = tc::instr_desc(p.bc, p.bt, fmt, fmt, a.w_mn ? 1u : 0u, a.x_mn ? 1u : 0u);
+  out->ep = LinearEpilogue{a.Y, a.ldy, a.Z, a.ldz, a.residual, a.ldr, a.bias, a.row_scale,
+                           a.col_scale, static_cast<int>(a.T), static_cast<int>(a.C),
+                           a.out_dtype, a.act, a.bounds};
+  return cudaSuccess;
+}
+
+SplitProblem problem_of(const LinearArgs& a, const LinearPlan& p, const Ready& r, int first_cta) {
+  return SplitProblem{r.map_w, r.map_x, r.ep, r.idesc, static_cast<int>(ktiles_of(a)),
+                      static_cast<int>(ceil_div(a.T, p.bt)), first_cta, a.w_mn, a.x_mn};
+}
+
+cudaError_t launch_split(const LinearPlan& p, int dtype, int64_t grid, SplitProblems* problems,
+                         int fault_inject, cudaStream_t stream) {
+  int split = p.split;
+  void* args[] = {problems, &split, &fault_inject};
+  return launch_dependent(linear_split_kernel_for(dtype, p.bt).kernel,
+                          dim3(static_cast<unsigned>(grid)), kThreads, p.smem_bytes, split,
+                          stream, args);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
+                          cudaStream_t stream, int fault_inject) {
+  Ready r{};
+  const cudaError_t e = make_ready(a, p, workspace, stream, &r);
+  if (e != cudaSuccess) return e;
   if (p.pair)
-    return launch_linear_pair(k, map_w, map_x, idesc, ep, kt, static_cast<int>(p.grid / 2),
-                              fault_inject, stream);
-  int tiles_t = static_cast<int>(ceil_div(a.T, p.bt)), split = p.split;
-  void* args[] = {&map_w, &map_x, &idesc, &ep, &kt, &tiles_t, &split, &fault_inject};
-  return launch_dependent(k.kernel, dim3(static_cast<unsigned>(p.grid)), kThreads, p.smem_bytes,
-                          split, stream, args);
+    return launch_linear_pair(linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn), r.map_w, r.map_x,
+                              r.idesc, r.ep, static_cast<int>(ktiles_of(a)),
+                              static_cast<int>(p.grid / 2), fault_inject, stream);
+  SplitProblems problems{};
+  problems.p[0] = problem_of(a, p, r, 0);
+  problems.p[1].first_cta = INT32_MAX;
+  return launch_split(p, a.dtype, p.grid, &problems, fault_inject, stream);
+}
+
+cudaError_t launch_linear_two(const LinearArgs& a, const LinearPlan& pa, void* wa,
+                              const LinearArgs& b, const LinearPlan& pb, void* wb,
+                              cudaStream_t stream) {
+  if (pa.pair || pb.pair || pa.bt != pb.bt || pa.split != pb.split || a.dtype != b.dtype ||
+      pa.grid + pb.grid > INT32_MAX) {
+    const cudaError_t e = launch_linear(a, pa, wa, stream);
+    return e != cudaSuccess ? e : launch_linear(b, pb, wb, stream);
+  }
+  Ready ra{}, rb{};
+  cudaError_t e = make_ready(a, pa, wa, stream, &ra);
+  if (e == cudaSuccess) e = make_ready(b, pb, wb, stream, &rb);
+  if (e != cudaSuccess) return e;
+  SplitProblems problems{};
+  problems.p[0] = problem_of(a, pa, ra, 0);
+  problems.p[1] = problem_of(b, pb, rb, static_cast<int>(pa.grid));
+  return launch_split(pa, a.dtype, pa.grid + pb.grid, &problems, 0, stream);
 }
 
 cudaError_t linear_read_and_clear_status(unsigned int* status) {

@@ -214,9 +214,21 @@ struct LinearKernel {
 
 constexpr int LINEAR_BC = 128;  // columns of Y per tile of the split kernels
 
+// One product of a split-kernel launch: its CTAs are first_cta and on.
+struct SplitProblem {
+  CUtensorMap map_w, map_x;
+  LinearEpilogue ep;
+  uint32_t idesc;
+  int ktiles, tiles_t, first_cta;
+  int w_mn, x_mn;
+};
+struct SplitProblems {
+  SplitProblem p[2];
+};
+
 }  // namespace linear
 
-linear::LinearKernel linear_split_kernel_for(int dtype, int bt, bool w_mn, bool x_mn);
+linear::LinearKernel linear_split_kernel_for(int dtype, int bt);
 cudaError_t linear_split_read_and_clear_status(unsigned int* status);
 linear::LinearKernel linear_pair_kernel_for(int dtype, bool w_mn, bool x_mn);
 cudaError_t launch_linear_pair(const linear::LinearKernel& k, const CUtensorMap& map_w,

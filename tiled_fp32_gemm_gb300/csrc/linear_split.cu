@@ -12,6 +12,8 @@
 //     shared memory (the ring, idle by then), and after a cluster barrier CTA
 //     r adds rows r * q .. of all of them, in slice order, so the result does
 //     not depend on timing.
+// One launch takes one product or two that do not depend on one another (the
+// layer's two gradients), of the same type and tile.
 // Every wait is bounded, as in the other tcgen05 kernels; a CTA that gave up
 // leaves its flag where its cluster sees it, and none of them stores.
 #include <cstdint>
@@ -28,7 +30,6 @@ namespace linear {
 
 using namespace f16tc;
 
-constexpr int PREFETCH_STAGES = 1;  // rings of the weight's tiles prefetched to L2
 constexpr int BC = LINEAR_BC;  // columns of Y per tile
 
 template <int BT_>
@@ -46,17 +47,6 @@ struct SplitGeometry {
   static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs on an SM");
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // FINISH_ROWS columns of this thread's TMEM lane; zeros for an empty slice of
 // K, whose tensor memory holds nothing.  (Warp w may access TMEM lanes
 // 32*(w%4) .. +31.)
@@ -69,15 +59,20 @@ __device__ __forceinline__ void load_sums(uint32_t addr, bool any, Rows& v) {
   }
 }
 
-template <class E, int BT, bool W_MN, bool X_MN>
+template <class E, int BT>
 __global__ void __launch_bounds__(THREADS, 2)
-    linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                        const __grid_constant__ CUtensorMap tmap_x, uint32_t idesc,
-                        const LinearEpilogue ep, int Kt, int tiles_t, int split, int fault_inject) {
-  static_assert(E::BYTES == 2 || (!W_MN && !X_MN), "8-bit operands are K-major");
+    linear_split_kernel(const __grid_constant__ SplitProblems problems, int split,
+                        int fault_inject) {
   using G = SplitGeometry<BT>;
   constexpr int STAGES = G::STAGES;
   constexpr int BK_ELEMS = ROW_BYTES / E::BYTES;
+  // Transposed operands: 16-bit only, and their boxes are 64 rows.
+  constexpr bool CAN_W_MN = E::BYTES == 2, CAN_X_MN = CAN_W_MN && BT >= MN_BOX;
+  const SplitProblem& P =
+      problems.p[static_cast<int>(blockIdx.x) >= problems.p[1].first_cta ? 1 : 0];
+  const LinearEpilogue& ep = P.ep;
+  const int Kt = P.ktiles;
+  const bool w_mn = CAN_W_MN && P.w_mn, x_mn = CAN_X_MN && P.x_mn;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -91,17 +86,17 @@ __global__ void __launch_bounds__(THREADS, 2)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int tile = (static_cast<int>(blockIdx.x) - P.first_cta) / split;
   // Tiles of one weight panel follow each other, so the panel is read from
   // memory once and found in L2 by the rest.
-  const int c0 = tile / tiles_t * BC, t0 = tile % tiles_t * BT;
+  const int c0 = tile / P.tiles_t * BC, t0 = tile % P.tiles_t * BT;
   const int kt0 = static_cast<int>(static_cast<int64_t>(Kt) * rank / split);
   const int kt1 = static_cast<int>(static_cast<int64_t>(Kt) * (rank + 1) / split);
 
   if (threadIdx.x == 0) {
     if (Kt > 0) {  // without a product the maps hold nothing
-      prefetch_tmap(&tmap_w);
-      prefetch_tmap(&tmap_x);
+      prefetch_tmap(&P.map_w);
+      prefetch_tmap(&P.map_x);
     }
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar(FULL + s), 1);   // producer arrival + tx bytes
@@ -120,8 +115,10 @@ __global__ void __launch_bounds__(THREADS, 2)
   // While the kernel before this one ends, the first of the weight's tiles
   // travel to L2 (a hint: nothing is read before grid_wait).
   if (warp == 0 && lane == 0)
-    for (int kt = kt0; kt < min(kt1, kt0 + PREFETCH_STAGES * STAGES); ++kt)
-      prefetch_operand<BC, W_MN>(&tmap_w, c0, kt * BK_ELEMS);
+    for (int kt = kt0; kt < min(kt1, kt0 + STAGES); ++kt) {
+      if (w_mn) prefetch_operand<BC, true>(&P.map_w, c0, kt * BK_ELEMS);
+      else prefetch_operand<BC, false>(&P.map_w, c0, kt * BK_ELEMS);
+    }
   grid_wait();
 
   float* const sums = reinterpret_cast<float*>(smem);  // [row][column], over the ring
@@ -134,8 +131,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (issued >= STAGES && !wait_phase(bar(EMPTY + s), (round + 1) & 1u, wc)) break;
         const uint32_t st = smem_u32(smem + s * G::STAGE_BYTES);
         mbar_arrive_expect_tx(bar(FULL + s), G::STAGE_BYTES);
-        load_operand<BC, W_MN>(st, &tmap_w, c0, kt * BK_ELEMS, bar(FULL + s));
-        load_operand<BT, X_MN>(st + G::W_BYTES, &tmap_x, t0, kt * BK_ELEMS, bar(FULL + s));
+        if (w_mn) load_operand<BC, true>(st, &P.map_w, c0, kt * BK_ELEMS, bar(FULL + s));
+        else load_operand<BC, false>(st, &P.map_w, c0, kt * BK_ELEMS, bar(FULL + s));
+        if (x_mn) load_operand<BT, true>(st + G::W_BYTES, &P.map_x, t0, kt * BK_ELEMS, bar(FULL + s));
+        else load_operand<BT, false>(st + G::W_BYTES, &P.map_x, t0, kt * BK_ELEMS, bar(FULL + s));
       }
     }
   } else if (warp == 1) {
@@ -152,7 +151,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         const uint32_t x_base = w_base + G::W_BYTES;
 #pragma unroll
         for (int j = 0; j < ROW_BYTES / 32; ++j)
-          E::mma(tmem, operand_desc<W_MN>(w_base, j), operand_desc<X_MN>(x_base, j), idesc,
+          E::mma(tmem, w_mn ? operand_desc<true>(w_base, j) : operand_desc<false>(w_base, j),
+                 x_mn ? operand_desc<true>(x_base, j) : operand_desc<false>(x_base, j), P.idesc,
                  g > 0 || j > 0);
         mma_commit(bar(EMPTY + s));
       }
@@ -230,44 +230,28 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 }
 
-template <class E, int BT, bool W_MN, bool X_MN>
+template <class E, int BT>
 LinearKernel entry() {
-  return LinearKernel{reinterpret_cast<const void*>(linear_split_kernel<E, BT, W_MN, X_MN>),
+  return LinearKernel{reinterpret_cast<const void*>(linear_split_kernel<E, BT>),
                       SplitGeometry<BT>::SMEM_BYTES, SplitGeometry<BT>::STAGES};
 }
 
-template <bool W_MN>
-LinearKernel entry_16(int bt) {
+template <class E>
+LinearKernel entry_for(int bt) {
   switch (bt) {
-    case 16: return entry<Half, 16, W_MN, false>();
-    case 32: return entry<Half, 32, W_MN, false>();
-    case 64: return entry<Half, 64, W_MN, false>();
-    case 128: return entry<Half, 128, W_MN, false>();
+    case 16: return entry<E, 16>();
+    case 32: return entry<E, 32>();
+    case 64: return entry<E, 64>();
+    default: return entry<E, 128>();
   }
-  return LinearKernel{};
 }
 
 }  // namespace linear
 
 using namespace linear;
 
-LinearKernel linear_split_kernel_for(int dtype, int bt, bool w_mn, bool x_mn) {
-  if (dtype == DT_E4M3) {
-    if (w_mn || x_mn) return LinearKernel{};
-    switch (bt) {
-      case 16: return entry<E4m3, 16, false, false>();
-      case 32: return entry<E4m3, 32, false, false>();
-      case 64: return entry<E4m3, 64, false, false>();
-      case 128: return entry<E4m3, 128, false, false>();
-    }
-    return LinearKernel{};
-  }
-  if (!x_mn) return w_mn ? entry_16<true>(bt) : entry_16<false>(bt);
-  // Transposed X comes with transposed W only (the weight gradient), and its
-  // boxes are 64 rows.
-  if (!w_mn) return LinearKernel{};
-  if (bt == 64) return entry<Half, 64, true, true>();
-  return bt == 128 ? entry<Half, 128, true, true>() : LinearKernel{};
+LinearKernel linear_split_kernel_for(int dtype, int bt) {
+  return dtype == DT_E4M3 ? entry_for<E4m3>(bt) : entry_for<Half>(bt);
 }
 
 cudaError_t linear_split_read_and_clear_status(unsigned int* status) {
