@@ -109,13 +109,13 @@ def mt_linear_backward(args: mt_linear_backward_args, stream: int = 0) -> int:
 # for a few tokens the host's time is what a call takes.
 _torch = None
 _codes = {}
-_FLOATS = _HALVES = _F32 = _F8 = None
+_FLOATS = _HALVES = _PRODUCTS = _F32 = _F8 = None
 _empty = _raw_stream = _device_now = None
 _functions = {}
 
 
 def _setup():
-    global _torch, _FLOATS, _HALVES, _F32, _F8, _empty, _raw_stream, _device_now
+    global _torch, _FLOATS, _HALVES, _PRODUCTS, _F32, _F8, _empty, _raw_stream, _device_now
     import torch
     from . import lib
     handle = lib()
@@ -126,6 +126,7 @@ def _setup():
     _HALVES = (torch.float16, torch.bfloat16)
     _FLOATS = (*_HALVES, torch.float32)
     _F32, _F8 = torch.float32, torch.float8_e4m3fn
+    _PRODUCTS = (*_HALVES, _F8)
     _empty, _device_now = torch.empty, torch.cuda.current_device
     # The current stream's handle without building a Stream object.
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -134,45 +135,59 @@ def _setup():
 
 
 def _first(t, name, dtypes):
-    """(rows, columns, dtype, device) of the operand whose device and type the
-    others follow."""
+    """(rows, columns, dtype, device, pointer, row pitch) of the operand whose
+    device and type the others follow."""
     if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
+    dtype, shape, device = t.dtype, t.shape, t.device
+    if dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}")
-    shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    return shape[0], shape[1], t.dtype, t.device
+    rows, cols = shape
+    return rows, cols, dtype, device, *_matrix(t, name, rows, cols, dtype, device)
 
 
 def _matrix(t, name, rows, cols, dtype, device):
-    """(pointer, row pitch) of a rows x cols CUDA matrix with unit column
-    stride; any pitch that holds a row serves a single row."""
-    if not isinstance(t, _torch.Tensor) or t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    """(pointer, row pitch) of a rows x cols matrix on `device` with unit
+    column stride; any pitch that holds a row serves a single row."""
+    try:
+        right = t.dtype == dtype and t.device == device
+    except AttributeError:
+        right = False
+    if not right:
+        _refuse(t, name, (dtype,), device)
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {rows} x {cols}")
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     if rows <= 1:
-        ld = cols or 1
-    elif ld < 1:
+        return t.data_ptr(), cols or 1
+    if ld < 1:
         raise ValueError(f"{name}'s rows overlap")
     return t.data_ptr(), ld
 
 
 def _vector(t, name, n, dtypes, device):
+    """(pointer, dtype code) of a contiguous vector of n values on `device`."""
+    try:
+        dtype = t.dtype
+        right = dtype in dtypes and t.device == device
+    except AttributeError:
+        right = False
+    if not right:
+        _refuse(t, name, dtypes, device)
+    if t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+    return t.data_ptr(), _codes[dtype]
+
+
+def _refuse(t, name, dtypes, device):
+    """Says what is wrong with an operand of another type or place."""
     if not isinstance(t, _torch.Tensor) or t.dtype not in dtypes or not t.is_cuda:
         raise TypeError(f"{name} must be a {' or '.join(map(str, dtypes))} CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
 
 
 def _result(out, name, rows, cols, dtype, device):
@@ -213,16 +228,14 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, out=None, h_out
     and h when given; h_out may be residual or x."""
     if _torch is None:
         _setup()
-    rows, d, dt, dev = _first(x, "x", _FLOATS)
+    rows, d, dt, dev, xp, ldx = _first(x, "x", _FLOATS)
     if out_dtype is None:
         out_dtype = dt
     elif out_dtype != dt and out_dtype != _F8:
         raise TypeError("out_dtype must be x's dtype or torch.float8_e4m3fn")
-    xp, ldx = _matrix(x, "x", rows, d, dt, dev)
     rp = ldr = hp = ldh = wp = sp = wcode = 0
     if weight is not None:
-        wp = _vector(weight, "weight", d, (dt, _F32), dev)
-        wcode = _codes[weight.dtype]
+        wp, wcode = _vector(weight, "weight", d, (dt, _F32), dev)
     h = x
     if residual is not None:
         rp, ldr = _matrix(residual, "residual", rows, d, dt, dev)
@@ -252,14 +265,12 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, need_weight=True, out=None, 
     given and may be dy or dh."""
     if _torch is None:
         _setup()
-    rows, d, dt, dev = _first(dy, "dy", _FLOATS)
-    dyp, lddy = _matrix(dy, "dy", rows, d, dt, dev)
+    rows, d, dt, dev, dyp, lddy = _first(dy, "dy", _FLOATS)
     hp, ldh = _matrix(h, "h", rows, d, dt, dev)
-    rp = _vector(rstd, "rstd", rows, (_F32,), dev)
+    rp, _ = _vector(rstd, "rstd", rows, (_F32,), dev)
     wp = wcode = dhp = lddh = dwp = 0
     if weight is not None:
-        wp = _vector(weight, "weight", d, (dt, _F32), dev)
-        wcode = _codes[weight.dtype]
+        wp, wcode = _vector(weight, "weight", d, (dt, _F32), dev)
     if dh is not None:
         dhp, lddh = _matrix(dh, "dh", rows, d, dt, dev)
     dx, dxp, lddx = _result(out, "out", rows, d, dt, dev)
@@ -297,10 +308,9 @@ def linear(a, b, bias=None, activation=None, residual=None, trans_b=False, scale
     dtype when ``preact`` is set."""
     if _torch is None:
         _setup()
-    M, K, dt, dev = _first(a, "a", (*_HALVES, _F8))
+    M, K, dt, dev, ap, lda = _first(a, "a", _PRODUCTS)
     if not isinstance(b, _torch.Tensor) or b.dim() != 2:
         raise ValueError("b must be a 2-D CUDA tensor")
-    ap, lda = _matrix(a, "a", M, K, dt, dev)
     bias_p = rp = ldr = zp = ldz = sap = sbp = 0
     if trans_b:
         N = b.shape[0]
@@ -311,8 +321,8 @@ def linear(a, b, bias=None, activation=None, residual=None, trans_b=False, scale
     if dt == _F8:
         if not trans_b:
             raise ValueError("8-bit inputs need b stored N x K (trans_b)")
-        sap = _vector(scale_a, "scale_a", M, (_F32,), dev)
-        sbp = _vector(scale_b, "scale_b", N, (_F32,), dev)
+        sap, _ = _vector(scale_a, "scale_a", M, (_F32,), dev)
+        sbp, _ = _vector(scale_b, "scale_b", N, (_F32,), dev)
         out_dtype = out_dtype or _torch.bfloat16
         if out_dtype not in _FLOATS:
             raise TypeError("out_dtype must be float16, bfloat16 or float32")
@@ -324,7 +334,7 @@ def linear(a, b, bias=None, activation=None, residual=None, trans_b=False, scale
         elif out_dtype != dt and out_dtype != _F32:
             raise TypeError("out_dtype must be a's dtype or float32")
     if bias is not None:
-        bias_p = _vector(bias, "bias", N, (_F32,), dev)
+        bias_p, _ = _vector(bias, "bias", N, (_F32,), dev)
     if residual is not None:
         rp, ldr = _matrix(residual, "residual", M, N, out_dtype, dev)
     y, yp, ldy = _result(out, "out", M, N, out_dtype, dev)
@@ -350,7 +360,7 @@ def linear_backward(dy, a, b, z=None, activation=None, trans_b=False, need_a=Tru
     float32), dbias is float32."""
     if _torch is None:
         _setup()
-    M, N, dt, dev = _first(dy, "dy", _HALVES)
+    M, N, dt, dev, dyp, lddy = _first(dy, "dy", _HALVES)
     act = _activation(activation)
     if not isinstance(a, _torch.Tensor) or a.dim() != 2:
         raise ValueError("a must be a 2-D CUDA tensor")
@@ -359,7 +369,6 @@ def linear_backward(dy, a, b, z=None, activation=None, trans_b=False, need_a=Tru
         db_dtype = dt
     elif db_dtype != dt and db_dtype != _F32:
         raise TypeError("db_dtype must be a's dtype or float32")
-    dyp, lddy = _matrix(dy, "dy", M, N, dt, dev)
     ap, lda = _matrix(a, "a", M, K, dt, dev)
     rows, cols = (N, K) if trans_b else (K, N)
     bp, ldb = _matrix(b, "b", rows, cols, dt, dev)
