@@ -1525,14 +1525,15 @@ mt_status mt_check_device_status(cudaStream_t stream) {
     cudaGetLastError();
     return MT_ERR_CUDA;
   }
-  unsigned int flags = 0, flags16 = 0, flags_linear = 0;
+  unsigned int flags = 0, flags16 = 0, flags_linear = 0, flags_norm = 0;
   if (mt::tf32x3_read_and_clear_status(&flags) != cudaSuccess ||
       mt::f16tc_read_and_clear_status(&flags16) != cudaSuccess ||
-      mt::linear_read_and_clear_status(&flags_linear) != cudaSuccess) {
+      mt::linear_read_and_clear_status(&flags_linear) != cudaSuccess ||
+      mt::rms_norm_grad_read_and_clear_status(&flags_norm) != cudaSuccess) {
     cudaGetLastError();
     return MT_ERR_CUDA;
   }
-  flags |= flags16 | flags_linear;
+  flags |= flags16 | flags_linear | flags_norm;
   return flags ? MT_ERR_TIMEOUT : MT_OK;
 }
 

@@ -73,6 +73,8 @@ int64_t rms_norm_grad_workspace(const RmsNormGradArgs& a, int sms);
 cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, void* workspace, int sms,
                                  cudaStream_t stream);
 
+cudaError_t rms_norm_grad_read_and_clear_status(unsigned int* status);
+
 // Adds `count` rows of `cols` floats (packed, in row order) to out[cols].
 cudaError_t launch_add_rows(const float* rows, int count, int cols, float* out,
                             BoundsRecord* bounds, cudaStream_t stream);

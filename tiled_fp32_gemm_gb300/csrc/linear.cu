@@ -26,11 +26,12 @@ constexpr int kPair = 256;      // columns and rows of Y per CTA pair
 template <class T>
 __global__ void __launch_bounds__(256) copy_rows_kernel(const T* src, int64_t lds, uint8_t* dst,
                                                         int64_t pitch, int64_t rows,
-                                                        int64_t cols) {
+                                                        int64_t cols, BoundsRecord* rec) {
   constexpr int N = 16 / sizeof(T);
   grid_launch_dependents();
   grid_wait();
   const int64_t per_row = pitch / 16, total = rows * per_row;
+  const int64_t src_extent = view_extent(rows, cols, lds);
   for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < total;
        e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t r = e / per_row, c0 = (e % per_row) * N;
@@ -38,13 +39,16 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const T* src, int64_t ld
       T v[N];
       uint4 u;
     } o;
-    const T* s = src + r * lds;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = c0 + i < cols ? s[c0 + i] : T(0);
-    *reinterpret_cast<uint4*>(dst + r * pitch + (e % per_row) * 16) = o.u;
+    for (int i = 0; i < N; ++i) {
+      const int64_t at = r * lds + c0 + i;
+      o.v[i] = c0 + i < cols && bounds_ok(rec, SITE_PREP_SRC, at, 1, src_extent) ? src[at] : T(0);
+    }
+    const int64_t to = r * pitch + c0 * static_cast<int64_t>(sizeof(T));
+    if (bounds_ok(rec, SITE_PREP_DST, to, 16, rows * pitch))
+      *reinterpret_cast<uint4*>(dst + to) = o.u;
   }
 }
-
 
 // The stored matrix of an operand: rows and columns in memory.
 struct Stored {
@@ -65,17 +69,18 @@ int64_t copy_bytes(const Stored& m, int elem) {
   return (m.rows * copy_pitch_bytes(m.cols, elem) + 255) / 256 * 256;
 }
 
-cudaError_t copy_operand(Stored* m, int elem, void* dst, cudaStream_t stream) {
+cudaError_t copy_operand(Stored* m, int elem, void* dst, BoundsRecord* rec,
+                         cudaStream_t stream) {
   const int64_t pitch = copy_pitch_bytes(m->cols, elem);
   const int64_t work = m->rows * (pitch / 16);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(1216, (work + 255) / 256));
   const cudaError_t e =
       elem == 1 ? launch_dependent(copy_rows_kernel<uint8_t>, grid, 256, stream,
                                    static_cast<const uint8_t*>(m->p), m->ld,
-                                   static_cast<uint8_t*>(dst), pitch, m->rows, m->cols)
+                                   static_cast<uint8_t*>(dst), pitch, m->rows, m->cols, rec)
                 : launch_dependent(copy_rows_kernel<uint16_t>, grid, 256, stream,
                                    static_cast<const uint16_t*>(m->p), m->ld,
-                                   static_cast<uint8_t*>(dst), pitch, m->rows, m->cols);
+                                   static_cast<uint8_t*>(dst), pitch, m->rows, m->cols, rec);
   m->p = dst;
   m->ld = pitch / elem;
   return e;
@@ -213,11 +218,11 @@ cudaError_t make_ready(const LinearArgs& a, const LinearPlan& p, void* workspace
   Stored x = stored_x(a), w = stored_w(a);
   char* ws = static_cast<char*>(workspace);
   if (p.copy_x_bytes) {
-    const cudaError_t r = copy_operand(&x, elem, ws, stream);
+    const cudaError_t r = copy_operand(&x, elem, ws, a.bounds, stream);
     if (r != cudaSuccess) return r;
   }
   if (p.copy_w_bytes) {
-    const cudaError_t r = copy_operand(&w, elem, ws + p.copy_x_bytes, stream);
+    const cudaError_t r = copy_operand(&w, elem, ws + p.copy_x_bytes, a.bounds, stream);
     if (r != cudaSuccess) return r;
   }
   // A pair's CTAs load half a tile of each operand; without a product (K = 0)

@@ -173,6 +173,16 @@ struct Held {
       for (int i = 0; i < S::COUNT; ++i) item[i].keep();
     }
   }
+  __device__ __forceinline__ void fill(float value) {
+    float v[S::STEP];
+#pragma unroll
+    for (int k = 0; k < S::STEP; ++k) v[k] = value;
+#pragma unroll
+    for (int i = 0; i < S::COUNT; ++i) {
+      if constexpr (VEC) item[i].set(v);
+      else item[i] = from_f32<T>(value);
+    }
+  }
   // The values of step i, in order.
   __device__ __forceinline__ void get(int i, float (&v)[S::STEP]) const {
     if constexpr (VEC) item[i].get(v);
