@@ -20,33 +20,68 @@ constexpr int kThreads = 192, kPairThreads = 320;
 constexpr int kPair = 256;      // columns and rows of Y per CTA pair
 
 // Padded copies of operands TMA cannot read in place (row pitch not a
-// multiple of 16 bytes, or base not 16-byte aligned): dst rows of `pitch`
-// bytes (a multiple of 16), the bytes past `bytes` zero.  E: element bytes,
-// which the source is aligned to.
-template <class T>
-__global__ void __launch_bounds__(256) copy_rows_kernel(const T* src, int64_t lds, uint8_t* dst,
-                                                        int64_t pitch, int64_t rows,
-                                                        int64_t cols, BoundsRecord* rec) {
-  constexpr int N = 16 / sizeof(T);
+// multiple of 16 bytes, or base not 16-byte aligned): rows of `pitch` bytes (a
+// multiple of 16), the bytes past `bytes` zero.  Source rows start on any
+// element, so an output's 16 bytes straddle two aligned 16-byte words of the
+// source: both are read (a neighbour's are found in L1) and shifted into
+// place.  Words that reach outside the source are read byte by byte.
+struct CopyJob {
+  const uint8_t* src;
+  int64_t pitch_src, bytes, extent;  // bytes: of a row, of the whole source
+  uint8_t* dst;
+  int64_t pitch;
+  int rows;
+  int first_block, blocks, row_threads;  // threads side by side on a row
+};
+struct CopyJobs {
+  CopyJob job[2];
+  BoundsRecord* rec;
+};
+
+constexpr int kCopyThreads = 256;
+
+__global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyJobs jobs) {
   grid_launch_dependents();
   grid_wait();
-  const int64_t per_row = pitch / 16, total = rows * per_row;
-  const int64_t src_extent = view_extent(rows, cols, lds);
-  for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < total;
-       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = e / per_row, c0 = (e % per_row) * N;
-    union {
-      T v[N];
-      uint4 u;
-    } o;
+  const CopyJob& j = jobs.job[static_cast<int>(blockIdx.x) >= jobs.job[1].first_block ? 1 : 0];
+  const int x0 = threadIdx.x % j.row_threads, row_step = kCopyThreads / j.row_threads;
+  const int chunks = static_cast<int>(j.pitch / 16);
+  for (int64_t r = static_cast<int64_t>(blockIdx.x - j.first_block) * row_step +
+                   threadIdx.x / j.row_threads;
+       r < j.rows; r += static_cast<int64_t>(j.blocks) * row_step) {
+    for (int x = x0; x < chunks; x += j.row_threads) {
+      const int64_t c0 = 16 * static_cast<int64_t>(x), at = r * j.pitch_src + c0;
+      const int left = static_cast<int>(min(int64_t(16), j.bytes - c0));  // of the row, or < 0
+      uint32_t o[4] = {0u, 0u, 0u, 0u};
+      const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(j.src + at) & 15u);
+      if (left > 0 && at >= shift && at - shift + 32 <= j.extent) {
+        const uint4* p = reinterpret_cast<const uint4*>(j.src + (at - shift));
+        const uint4 lo = p[0], hi = p[1];
+        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (shift & 8) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int64_t at = r * lds + c0 + i;
-      o.v[i] = c0 + i < cols && bounds_ok(rec, SITE_PREP_SRC, at, 1, src_extent) ? src[at] : T(0);
+          for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (shift & 4) {
+#pragma unroll
+          for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[i] = __funnelshift_r(w[i], w[i + 1], 8 * (shift & 3));
+          const int keep = left - 4 * i;  // bytes of this word inside the row
+          if (keep < 4) o[i] = keep <= 0 ? 0u : o[i] & ((1u << (8 * keep)) - 1u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < left && bounds_ok(jobs.rec, SITE_PREP_SRC, at + i, 1, j.extent))
+            o[i / 4] |= static_cast<uint32_t>(j.src[at + i]) << (8 * (i % 4));
+      }
+      const int64_t to = r * j.pitch + c0;
+      if (bounds_ok(jobs.rec, SITE_PREP_DST, to, 16, j.rows * j.pitch))
+        *reinterpret_cast<uint4*>(j.dst + to) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    const int64_t to = r * pitch + c0 * static_cast<int64_t>(sizeof(T));
-    if (bounds_ok(rec, SITE_PREP_DST, to, 16, rows * pitch))
-      *reinterpret_cast<uint4*>(dst + to) = o.u;
   }
 }
 
@@ -69,21 +104,25 @@ int64_t copy_bytes(const Stored& m, int elem) {
   return (m.rows * copy_pitch_bytes(m.cols, elem) + 255) / 256 * 256;
 }
 
-cudaError_t copy_operand(Stored* m, int elem, void* dst, BoundsRecord* rec,
-                         cudaStream_t stream) {
-  const int64_t pitch = copy_pitch_bytes(m->cols, elem);
-  const int64_t work = m->rows * (pitch / 16);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(1216, (work + 255) / 256));
-  const cudaError_t e =
-      elem == 1 ? launch_dependent(copy_rows_kernel<uint8_t>, grid, 256, stream,
-                                   static_cast<const uint8_t*>(m->p), m->ld,
-                                   static_cast<uint8_t*>(dst), pitch, m->rows, m->cols, rec)
-                : launch_dependent(copy_rows_kernel<uint16_t>, grid, 256, stream,
-                                   static_cast<const uint16_t*>(m->p), m->ld,
-                                   static_cast<uint8_t*>(dst), pitch, m->rows, m->cols, rec);
+// The copy of *m into dst, which *m then stands for.
+CopyJob copy_job(Stored* m, int elem, void* dst, int first_block) {
+  CopyJob j{};
+  j.src = static_cast<const uint8_t*>(m->p);
+  j.pitch_src = m->ld * elem;
+  j.bytes = m->cols * elem;
+  j.extent = view_extent(m->rows, m->cols, m->ld) * elem;
+  j.dst = static_cast<uint8_t*>(dst);
+  j.pitch = copy_pitch_bytes(m->cols, elem);
+  j.rows = static_cast<int>(m->rows);
+  j.first_block = first_block;
+  j.row_threads = 8;
+  while (j.row_threads < kCopyThreads && j.row_threads * 16 < j.pitch) j.row_threads *= 2;
+  const int64_t rows_per_block = kCopyThreads / j.row_threads;
+  j.blocks = static_cast<int>(
+      std::min<int64_t>(2432, (m->rows + rows_per_block - 1) / rows_per_block));
   m->p = dst;
-  m->ld = pitch / elem;
-  return e;
+  m->ld = j.pitch / elem;
+  return j;
 }
 
 bool encode(CUtensorMap* map, int dtype, const Stored& m, bool mn, int rows) {
@@ -217,12 +256,19 @@ cudaError_t make_ready(const LinearArgs& a, const LinearPlan& p, void* workspace
   const int elem = dtype_bytes(a.dtype);
   Stored x = stored_x(a), w = stored_w(a);
   char* ws = static_cast<char*>(workspace);
-  if (p.copy_x_bytes) {
-    const cudaError_t r = copy_operand(&x, elem, ws, a.bounds, stream);
-    if (r != cudaSuccess) return r;
-  }
-  if (p.copy_w_bytes) {
-    const cudaError_t r = copy_operand(&w, elem, ws + p.copy_x_bytes, a.bounds, stream);
+  if (p.copy_x_bytes || p.copy_w_bytes) {
+    CopyJobs jobs{};
+    jobs.rec = a.bounds;
+    int count = 0, blocks = 0;
+    auto add = [&](Stored* m, void* dst) {
+      jobs.job[count] = copy_job(m, elem, dst, blocks);
+      blocks += jobs.job[count++].blocks;
+    };
+    if (p.copy_x_bytes) add(&x, ws);
+    if (p.copy_w_bytes) add(&w, ws + p.copy_x_bytes);
+    if (count == 1) jobs.job[1].first_block = INT32_MAX;
+    const cudaError_t r = launch_dependent(copy_rows_kernel, dim3(static_cast<unsigned>(blocks)),
+                                           kCopyThreads, stream, jobs);
     if (r != cudaSuccess) return r;
   }
   // A pair's CTAs load half a tile of each operand; without a product (K = 0)

@@ -99,110 +99,123 @@ __device__ __forceinline__ void activate_rows(Rows& v) {
   for (int i = 0; i < FINISH_ROWS; ++i) v[i] = activate<ACT>(v[i]);
 }
 
-// What finishing FINISH_ROWS rows of a column reads besides the sums: the
-// residual's bits, and lane i's share of the rows' scales.
-struct Ahead {
-  uint32_t residual[FINISH_ROWS];
-  float row_scale;
+__device__ __forceinline__ void activate_rows(int act, Rows& v) {
+  switch (act) {
+    case ACT_RELU: return activate_rows<ACT_RELU>(v);
+    case ACT_GELU: return activate_rows<ACT_GELU>(v);
+    case ACT_GELU_TANH: return activate_rows<ACT_GELU_TANH>(v);
+    case ACT_SILU: return activate_rows<ACT_SILU>(v);
+    default: return;
+  }
+}
 
-  __device__ __forceinline__ void load(const LinearEpilogue& e, int c, int t, int t_end) {
-    const int rows = c < e.C ? t_end - t : 0;
-    if (e.residual) {
-      const int64_t extent = view_extent(e.T, e.C, e.ldr);
-      int64_t at = static_cast<int64_t>(t) * e.ldr + c;
-      if (e.out_dtype == DT_F32) {
+// One column of a T x C matrix of T values with row pitch ld.
+template <class T>
+struct Column {
+  T* p;  // row 0
+  int64_t ld, extent;
+  int c;
+  BoundsRecord* rec;
+
+  __device__ __forceinline__ Column(const LinearEpilogue& e, const void* m, int64_t ld_, int c_)
+      : p(static_cast<T*>(const_cast<void*>(m)) + c_), ld(ld_),
+        extent(view_extent(e.T, e.C, ld_)), c(c_), rec(e.bounds) {}
+  __device__ __forceinline__ bool ok(int row) const {
+    return bounds_ok(rec, SITE_C_STORE, row * ld + c, 1, extent);
+  }
+  // FINISH_ROWS rows from t on, the first `rows` of them: a whole block
+  // without a test per row.
+  __device__ __forceinline__ void load(int t, int rows, T (&v)[FINISH_ROWS]) const {
+    const T* q = p + t * ld;
+    if (rows >= FINISH_ROWS) {
 #pragma unroll
-        for (int i = 0; i < FINISH_ROWS; ++i, at += e.ldr)
-          residual[i] = i < rows && bounds_ok(e.bounds, SITE_C_STORE, at, 1, extent)
-                            ? static_cast<const uint32_t*>(e.residual)[at]
-                            : 0u;
-      } else {
+      for (int i = 0; i < FINISH_ROWS; ++i, q += ld) v[i] = ok(t + i) ? *q : T(0.0f);
+    } else {
 #pragma unroll
-        for (int i = 0; i < FINISH_ROWS; ++i, at += e.ldr)
-          residual[i] = i < rows && bounds_ok(e.bounds, SITE_C_STORE, at, 1, extent)
-                            ? static_cast<const uint16_t*>(e.residual)[at]
-                            : 0u;
-      }
+      for (int i = 0; i < FINISH_ROWS; ++i, q += ld)
+        v[i] = i < rows && ok(t + i) ? *q : T(0.0f);
     }
-    if (e.row_scale) {
-      const int lane = threadIdx.x % 32;
-      row_scale = lane < FINISH_ROWS && t + lane < t_end &&
-                          bounds_ok(e.bounds, SITE_BIAS, t + lane, 1, e.T)
-                      ? e.row_scale[t + lane]
-                      : 0.0f;
+  }
+  __device__ __forceinline__ void store(int t, int rows, const Rows& v) const {
+    T* q = p + t * ld;
+    if (rows >= FINISH_ROWS) {
+#pragma unroll
+      for (int i = 0; i < FINISH_ROWS; ++i, q += ld)
+        if (ok(t + i)) *q = row::from_f32<T>(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < FINISH_ROWS; ++i, q += ld)
+        if (i < rows && ok(t + i)) *q = row::from_f32<T>(v[i]);
     }
   }
 };
 
-// Column c, rows t .. of a T x C matrix with row pitch ld: v rounded and
-// stored to `rows` of them.
-template <class T>
-__device__ __forceinline__ void store_rows(const LinearEpilogue& e, void* m, int64_t ld, int c,
-                                           int t, int rows, const Rows& v) {
-  T* base = static_cast<T*>(m);
-  T* p = base + static_cast<int64_t>(t) * ld + c;
-#pragma unroll
-  for (int i = 0; i < FINISH_ROWS; ++i, p += ld)
-    if (i < rows && bounds_ok(e.bounds, SITE_C_STORE, p - base, 1, view_extent(e.T, e.C, ld)))
-      *p = row::from_f32<T>(v[i]);
-}
-__device__ __forceinline__ void store_rows(const LinearEpilogue& e, void* m, int64_t ld, int c,
-                                           int t, int rows, const Rows& v) {
-  if (e.out_dtype == DT_F16) store_rows<__half>(e, m, ld, c, t, rows, v);
-  else if (e.out_dtype == DT_BF16) store_rows<__nv_bfloat16>(e, m, ld, c, t, rows, v);
-  else store_rows<float>(e, m, ld, c, t, rows, v);
-}
-
-// Finishes column c of Y, rows t_begin .. t_end - 1 (t_end <= e.T; columns at
-// or past e.C are dropped), the whole warp together: sums(t, v) gives the
-// sums of rows t .. t + FINISH_ROWS - 1.  What the next rows need is read
-// while these are computed.  The residual may be Y itself: each element is
-// read and then written by this thread.
-template <class Sums>
-__device__ __forceinline__ void finish(const LinearEpilogue& e, int c, int t_begin, int t_end,
-                                       Sums&& sums) {
+// finish for results of type T.  What the next rows need is read while these
+// are computed; the residual may be Y itself (each element is read and then
+// written by this thread).
+template <class T, class Sums>
+__device__ __forceinline__ void finish_typed(const LinearEpilogue& e, int c, int t_begin,
+                                             int t_end, Sums&& sums) {
   const bool live = c < e.C;
+  const int lane = threadIdx.x % 32;
   const float b =
       e.bias && live && bounds_ok(e.bounds, SITE_BIAS, c, 1, e.C) ? e.bias[c] : 0.0f;
   const float s =
       e.col_scale && live && bounds_ok(e.bounds, SITE_BIAS, c, 1, e.C) ? e.col_scale[c] : 0.0f;
-  Ahead next;
-  next.load(e, c, t_begin, t_end);
+  const Column<T> y(e, e.Y, e.ldy, c), z(e, e.Z, e.ldz, c), r(e, e.residual, e.ldr, c);
+  // Lane i's share of the rows' scales.
+  auto scale_of = [&](int t) {
+    return lane < FINISH_ROWS && t + lane < t_end &&
+                   bounds_ok(e.bounds, SITE_BIAS, t + lane, 1, e.T)
+               ? e.row_scale[t + lane]
+               : 0.0f;
+  };
+  T next_res[FINISH_ROWS];
+  float next_scale = 0.0f;
+  if (e.residual && live) r.load(t_begin, t_end - t_begin, next_res);
+  if (e.row_scale) next_scale = scale_of(t_begin);
 #pragma unroll 1
   for (int t = t_begin; t < t_end; t += FINISH_ROWS) {
-    const Ahead now = next;
-    if (t + FINISH_ROWS < t_end) next.load(e, c, t + FINISH_ROWS, t_end);
+    const int rows = t_end - t;
+    T res[FINISH_ROWS];
+    const float scale = next_scale;
+    if (e.residual) {
+#pragma unroll
+      for (int i = 0; i < FINISH_ROWS; ++i) res[i] = next_res[i];
+      if (live && rows > FINISH_ROWS)
+        r.load(t + FINISH_ROWS, rows - FINISH_ROWS, next_res);
+    }
+    if (e.row_scale && rows > FINISH_ROWS) next_scale = scale_of(t + FINISH_ROWS);
     Rows v;
     sums(t, v);
-    const int rows = live ? t_end - t : 0;
     if (e.row_scale) {
 #pragma unroll
       for (int i = 0; i < FINISH_ROWS; ++i)
-        v[i] = fmaf(v[i], __shfl_sync(0xffffffffu, now.row_scale, i) * s, b);
-    } else {
+        v[i] = fmaf(v[i], __shfl_sync(0xffffffffu, scale, i) * s, b);
+    } else if (e.bias) {
 #pragma unroll
       for (int i = 0; i < FINISH_ROWS; ++i) v[i] += b;
     }
-    if (e.Z) store_rows(e, e.Z, e.ldz, c, t, rows, v);
-    switch (e.act) {
-      case ACT_RELU: activate_rows<ACT_RELU>(v); break;
-      case ACT_GELU: activate_rows<ACT_GELU>(v); break;
-      case ACT_GELU_TANH: activate_rows<ACT_GELU_TANH>(v); break;
-      case ACT_SILU: activate_rows<ACT_SILU>(v); break;
-      default: break;
-    }
+    if (!live) continue;
+    if (e.Z) z.store(t, rows, v);
+    activate_rows(e.act, v);
     if (e.residual) {
 #pragma unroll
-      for (int i = 0; i < FINISH_ROWS; ++i) {
-        const uint32_t r = now.residual[i];
-        v[i] += e.out_dtype == DT_BF16  ? __uint_as_float(r << 16)
-                : e.out_dtype == DT_F16 ? __half2float(__ushort_as_half(
-                                              static_cast<unsigned short>(r)))
-                                        : __uint_as_float(r);
-      }
+      for (int i = 0; i < FINISH_ROWS; ++i) v[i] += row::to_f32(res[i]);
     }
-    store_rows(e, e.Y, e.ldy, c, t, rows, v);
+    y.store(t, rows, v);
   }
+}
+
+// Finishes column c of Y, rows t_begin .. t_end - 1 (t_end <= e.T; columns at
+// or past e.C are dropped), the whole warp together: sums(t, v) gives the
+// sums of rows t .. t + FINISH_ROWS - 1.
+template <class Sums>
+__device__ __forceinline__ void finish(const LinearEpilogue& e, int c, int t_begin, int t_end,
+                                       Sums&& sums) {
+  if (e.out_dtype == DT_F16) finish_typed<__half>(e, c, t_begin, t_end, sums);
+  else if (e.out_dtype == DT_BF16) finish_typed<__nv_bfloat16>(e, c, t_begin, t_end, sums);
+  else finish_typed<float>(e, c, t_begin, t_end, sums);
 }
 
 // A built kernel (kernel null: no such form), its dynamic shared memory and
