@@ -144,8 +144,9 @@ cudaError_t linear_read_and_clear_status(unsigned int* status);
 // base, row pitch a multiple of 16 bytes.
 bool tma_readable(const void* p, int64_t ld, int elem);
 
-// linear_grad.cu: dz = dY * act'(Z) rounded to `dtype` (dZ null: not
-// written), and the column sums of the unrounded dz (dbias null: not
+// linear_grad.cu: dz = dY * act'(Z) rounded to `dtype` (dZ null: not written;
+// else 16-byte aligned rows of lddz >= N values, lddz a multiple of 8, whose
+// last chunk of eight is padded with zeros), and the column sums of the unrounded dz (dbias null: not
 // computed), through `partial` (linear_dz_workspace bytes).
 struct LinearDzArgs {
   int64_t M;

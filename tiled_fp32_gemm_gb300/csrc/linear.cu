@@ -56,19 +56,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyJobs 
       const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(j.src + at) & 15u);
       if (left > 0 && at >= shift && at - shift + 32 <= j.extent) {
         const uint4* p = reinterpret_cast<const uint4*>(j.src + (at - shift));
-        const uint4 lo = p[0], hi = p[1];
-        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        if (shift & 8) {
-#pragma unroll
-          for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-        }
-        if (shift & 4) {
-#pragma unroll
-          for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-        }
+        const uint4 u = row::shifted(p[0], p[1], shift);
+        o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          o[i] = __funnelshift_r(w[i], w[i + 1], 8 * (shift & 3));
           const int keep = left - 4 * i;  // bytes of this word inside the row
           if (keep < 4) o[i] = keep <= 0 ? 0u : o[i] & ((1u << (8 * keep)) - 1u);
         }

@@ -13,25 +13,39 @@
 namespace mt {
 namespace linear {
 
+// exp(x) and 1 / x on the special-function unit, one instruction past the
+// scaling by log2(e) (the .ftz forms: what would be subnormal is 0).
+__device__ __forceinline__ float exp_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 1 / (1 + exp(-z)).  exp overflows to infinity for z below -88, which gives
 // the 0 that is wanted.
 __device__ __forceinline__ float logistic(float z) {
-  return __fdividef(1.0f, 1.0f + __expf(-z));
+  return rcp_approx(1.0f + exp_approx(-z));
 }
 
 // The normal distribution's Phi(z) = (1 + erf(z / sqrt 2)) / 2 by Hastings'
 // approximation of erf (Abramowitz and Stegun, Handbook of Mathematical
 // Functions, 7.1.26: five coefficients, one exponential, absolute error below
 // 1.5e-7), without the branches of a correctly scaled erf: every lane of a
-// warp takes the same path.
-__device__ __forceinline__ float normal_cdf(float z) {
+// warp takes the same path.  *bell: exp(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf(float z, float* bell) {
   const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+  const float t = rcp_approx(fmaf(0.3275911f, x, 1.0f));
   float p = fmaf(1.061405429f, t, -1.453152027f);
   p = fmaf(p, t, 1.421413741f);
   p = fmaf(p, t, -0.284496736f);
   p = fmaf(p, t, 0.254829592f);
-  const float tail = 0.5f * p * t * __expf(-x * x);  // Phi(-|z|)
+  *bell = exp_approx(-x * x);
+  const float tail = 0.5f * p * t * *bell;  // Phi(-|z|)
   return z > 0.0f ? 1.0f - tail : tail;
 }
 
@@ -41,7 +55,8 @@ __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == ACT_RELU) {
     return z < 0.0f ? 0.0f : z;  // a NaN stays one
   } else if constexpr (ACT == ACT_GELU) {
-    return z * normal_cdf(z);
+    float bell;
+    return z * normal_cdf(z, &bell);
   } else if constexpr (ACT == ACT_GELU_TANH) {
     return z * logistic(1.5957691216057308f * fmaf(0.044715f * z * z, z, z));
   } else if constexpr (ACT == ACT_SILU) {
@@ -58,9 +73,9 @@ __device__ __forceinline__ float activate_grad(float z) {
   if constexpr (ACT == ACT_RELU) {
     return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
   } else if constexpr (ACT == ACT_GELU) {
-    // Phi(z) + z * phi(z)
-    return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z),
-                normal_cdf(z));
+    float bell;
+    const float cdf = normal_cdf(z, &bell);
+    return fmaf(z * 0.39894228040143268f, bell, cdf);  // Phi(z) + z * phi(z)
   } else if constexpr (ACT == ACT_GELU_TANH) {
     const float x = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;
     const float p = logistic(1.5957691216057308f * fmaf(0.044715f * x * x, x, x));

@@ -137,6 +137,65 @@ struct Pack8<__nv_bfloat16> {
   }
 };
 
+// The 16 bytes at `p` plus `shift` bytes (shift < 16), from two aligned
+// 16-byte words.
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, int shift) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (shift & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (shift & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[i], w[i + 1], 8 * (shift & 3));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// load8_any where the aligned words reach outside the matrix (its first and
+// last rows): out of line, so the common path keeps its registers.
+template <class T>
+__device__ __noinline__ uint4 load8_single(const T* p, int count) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  for (int i = 0; i < count; ++i)
+    w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i % 2));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Columns c .. c + 7 of a row of d 16-bit values that may start on any
+// element (those at or past d zero): two aligned words, shifted, or single
+// elements where the words reach outside the matrix.
+template <class T>
+__device__ __forceinline__ Pack8<T> load8_any(const Matrix<const T>& m, int64_t row, int c,
+                                              int d) {
+  static_assert(sizeof(T) == 2, "16-bit values");
+  const int64_t at = row * m.ld + c;
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(m.p + at) & 15u);
+  const int64_t first = at - shift / 2;
+  Pack8<T> o;
+  if (first >= 0 && first + 16 <= m.extent) {
+    const uint4* p = reinterpret_cast<const uint4*>(m.p + first);
+    o.u = shifted(p[0], p[1], shift);
+    if (c + 8 > d) {
+      uint32_t w[4] = {o.u.x, o.u.y, o.u.z, o.u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int keep = d - c - 2 * i;  // values of this word
+        if (keep < 2) w[i] = keep <= 0 ? 0u : w[i] & 0xffffu;
+      }
+      o.u = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    const int count = min(8, d - c);
+    o.u = count > 0 && m.ok(at, count) ? load8_single(m.p + at, count)
+                                       : make_uint4(0u, 0u, 0u, 0u);
+  }
+  return o;
+}
+
 // A thread's E values of a row that `threads` threads share: eight
 // consecutive ones per step (VEC) or one, threads side by side.
 template <int E, bool VEC>
