@@ -117,3 +117,78 @@ def test_operators_match_the_binding_and_differentiate():
     got = torch.autograd.grad(y, (x, nw), dy)
     ref = mt.rms_norm_backward(dy, x.detach(), nw.detach(), rstd.detach())
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_native_marshalling_is_built_and_leaves_other_operands_to_python():
+    """build() makes it for the installed torch; what it does not take (here:
+    host tensors, numbers) it answers with None, never with an error."""
+    from tiled_fp32_gemm_gb300 import build
+    build.build()
+    spec = importlib.util.spec_from_file_location("mt_torch_binding", build.binding_path())
+    native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(native)
+    x = torch.ones(2, 3)
+    assert native.rms_norm(x, None, None, 1e-5, None) is None
+    assert native.rms_norm(1, 2, 3, 4, 5) is None
+    assert native.rms_norm_backward(x, x, None, x, None, True) is None
+    assert native.linear(x, x, None, 0, None, True, None, None, None, False) is None
+    assert native.linear_backward(x, x, x, None, 0, True, True, True, True, None) is None
+    with pytest.raises(TypeError):
+        native.use_library(1)
+
+
+@pytest.mark.gpu
+def test_native_and_python_marshalling_agree(monkeypatch):
+    """The same calls with and without the native marshalling: same results,
+    same refusals."""
+    from tiled_fp32_gemm_gb300 import layers
+    g = torch.Generator(device="cuda").manual_seed(8)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, r = draw(9, 80).half()[:, :72], draw(9, 72).half()
+    w, n = draw(40, 72).half(), draw(72)
+    q, s = w.to(torch.float8_e4m3fn), torch.rand(40, device="cuda")
+    z, dy, bias = draw(9, 40).half(), draw(9, 48).half()[:, :40], draw(40)
+    rstd = torch.rand(9, device="cuda")
+    calls = [
+        lambda: mt.rms_norm(x, n, residual=r),
+        lambda: mt.rms_norm(x, None, eps=0.5),
+        lambda: mt.rms_norm(x, n.half(), out_dtype=torch.float8_e4m3fn),
+        lambda: mt.rms_norm_backward(r, x, n, rstd, dh=r),
+        lambda: mt.rms_norm_backward(r, x, None, rstd, need_weight=False),
+        lambda: mt.linear(x, w, bias=bias, activation="gelu", residual=z, trans_b=True,
+                          preact=True),
+        lambda: (mt.linear(x, w.t().contiguous(), out_dtype=torch.float32),),
+        lambda: (mt.linear(q, q, trans_b=True, scale_a=s, scale_b=s),),
+        lambda: mt.linear_backward(dy, x, w, z=z, activation="silu", trans_b=True),
+        lambda: mt.linear_backward(dy, x, w.t().contiguous(), need_a=False,
+                                   db_dtype=torch.float32),
+    ]
+    refusals = [lambda: mt.rms_norm(x, n, eps=-1.0), lambda: mt.rms_norm(x, n[:5]),
+                lambda: mt.rms_norm(x, n, out_dtype=torch.bfloat16),
+                lambda: mt.linear(x, w), lambda: mt.linear(x, w.bfloat16(), trans_b=True),
+                lambda: mt.linear(x, w, trans_b=True, residual=z[:3]),
+                lambda: mt.linear_backward(dy, x, w, activation="relu", trans_b=True),
+                lambda: mt.rms_norm_backward(r, x, n, rstd.half())]
+    mt.rms_norm(x, n)
+    assert layers._native is not None
+    fast = [f() for f in calls]
+
+    def answer(f):
+        try:
+            f()
+        except Exception as e:
+            return type(e), str(e)
+
+    errors = [answer(f) for f in refusals]
+    assert all(errors)
+    monkeypatch.setattr(layers, "_native", None)
+    for want, f in zip(fast, calls):
+        got = f()
+        assert len(got) == len(want)
+        for a, b in zip(want, got):
+            if a is None or b is None:
+                assert a is b
+            else:
+                assert a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride()
+                assert torch.equal(a.float(), b.float())
+    assert [answer(f) for f in refusals] == errors

@@ -32,8 +32,10 @@ def checked(monkeypatch):
         with monkeypatch.context() as m:
             for name in layers.SIGNATURES:
                 m.setitem(layers._functions, name, getattr(handle, name))
+            layers._point_native()
             got = call()
             torch.cuda.synchronize()
+        layers._point_native()
         status = mt.bounds_status(handle)
         assert status["count"] == 0, status
         for w, g in zip(want, got):

@@ -11,6 +11,10 @@ GEMM, its operand copies and K-slice reduce, the one-warp kernel) test every
 global and shared access against its buffer, skip any that falls outside and
 count it (``mt_bounds_status``).  For tests; slower than the normal build.
 
+The torch binding's native marshalling (csrc/torch_binding.cpp) is compiled
+beside it with g++ against the installed torch into a module of its own,
+named after that torch; a call's work is the library's either way.
+
     python -m tiled_fp32_gemm_gb300.build [--force] [--verbose] [--checked]
 """
 from __future__ import annotations
@@ -21,6 +25,7 @@ import os
 import shutil
 import subprocess
 import sys
+import threading
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -67,11 +72,52 @@ def _compile(src: str, obj: str, verbose: bool, defines=()) -> str:
     return r.stderr if verbose else ""
 
 
+def binding_path() -> str:
+    """The native marshalling module for the installed torch and Python."""
+    import sysconfig
+
+    import torch
+    return os.path.join(BUILD, f"torch_{torch.__version__}",
+                        "mt_torch_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def _compile_binding(force: bool):
+    """Compile the native marshalling if anything changed."""
+    import sysconfig
+
+    import torch
+    src, out = os.path.join(CSRC, "torch_binding.cpp"), binding_path()
+    if not force and not _stale(out, [src, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
+        return
+    os.makedirs(os.path.dirname(out), exist_ok=True)
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", cuda, "-I", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_binding.cpp:\n{r.stderr[-4000:]}")
+    os.replace(tmp, out)
+
+
 def _variant(checked: bool):
     """(object dir, library, extra nvcc flags) of the normal or checked build."""
     if checked:
         return CHECKED_BUILD, CHECKED_LIB, ["-DMT_BOUNDS_CHECK=1"]
     return BUILD, LIB, []
+
+
+def _in_thread(f, arg, errors):
+    try:
+        f(arg)
+    except Exception as e:  # re-raised by the thread that waits
+        errors.append(e)
 
 
 def build_many(variants, force: bool = False, verbose: bool = False):
@@ -91,6 +137,8 @@ def build_many(variants, force: bool = False, verbose: bool = False):
             if force or _stale(obj, [src, *headers]):
                 jobs.append((src, obj, defines))
         plans.append((lib, objects))
+    binding = threading.Thread(target=_in_thread, args=(_compile_binding, force, errors := []))
+    binding.start()
     if jobs:
         # The longest translation units first, so they overlap the rest.
         jobs.sort(key=lambda j: -os.path.getsize(j[0]))
@@ -107,6 +155,9 @@ def build_many(variants, force: bool = False, verbose: bool = False):
             if r.returncode != 0:
                 raise RuntimeError(f"link failed:\n{r.stderr}")
             os.replace(tmp, lib)
+    binding.join()
+    if errors:
+        raise errors[0]
     return [lib for lib, _ in plans]
 
 
