@@ -253,16 +253,19 @@ constexpr int kSmThreads = 512;
 constexpr int ctas_per_sm(int threads) { return kSmThreads > threads ? kSmThreads / threads : 1; }
 
 // A row held in the registers of THREADS threads, E values each; rows
-// strided over the grid.  The next row's values are loaded before this row's
-// reduction, so a barrier leaves loads in flight.  Each thread reads its
-// values of a row before it writes them, so dx may be dy or dh.
-template <class T, class W, int THREADS, int E>
+// strided over the grid.  Up to 512 threads the next row's values are loaded
+// before this row's reduction, so a barrier leaves loads in flight; 1024 have
+// no registers for that (with them, 8000 x 8191 took 309 us, without 137).
+// Each thread reads its values of a row before it writes them, so dx may be
+// dy or dh.
+template <class T, class W, int THREADS, int E, bool DH>
 __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS),
                                   ctas_per_sm(THREADS* rows_per_cta(THREADS)))
     rms_norm_grad_kernel(const RmsNormGradArgs a, const Operands<T> o,
                          const Matrix<const W> weight) {
   using S = Slots<E, false>;
   constexpr int ROWS = rows_per_cta(THREADS), WARPS = THREADS / 32;
+  constexpr bool AHEAD = THREADS <= 512;
   __shared__ float sums[2][WARPS];  // by turns, so one barrier a row is enough
   const int tid = threadIdx.x % THREADS, lane = threadIdx.x % 32, warp = tid / 32;
   const int64_t group = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / THREADS;
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS),
       if (row >= a.rows) return;
       dy.load(o.dy, row, a.d, tid, THREADS);
       h.load(o.h, row, a.d, tid, THREADS);
-      if (a.dh) dh.load(o.dh, row, a.d, tid, THREADS);
+      if (DH) dh.load(o.dh, row, a.d, tid, THREADS);
       r = o.rstd.load(row, 0);
     }
   };
@@ -283,29 +286,36 @@ __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS),
   grid_wait();
   Held<W, E, false> w;
   if (a.weight) w.load(weight, 0, a.d, tid, THREADS);
+  else w.fill(1.0f);
   float dw[S::COUNT][S::STEP];
 #pragma unroll
   for (int i = 0; i < S::COUNT; ++i)
 #pragma unroll
     for (int k = 0; k < S::STEP; ++k) dw[i][k] = 0.0f;
   Row next;
-  next.load(a, o, group, tid);
+  if (AHEAD) next.load(a, o, group, tid);
   int turn = 0;
   for (int64_t row = group; row < a.rows; row += groups, turn ^= 1) {
-    Row now = next;
-    next.load(a, o, row + groups, tid);
+    Row now;
+    if constexpr (AHEAD) {
+      now = next;
+      next.load(a, o, row + groups, tid);
+    } else {
+      now.load(a, o, row, tid);
+    }
+    const float r = now.r;
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < S::COUNT; ++i) {
       float vy[S::STEP], vh[S::STEP], vw[S::STEP];
       now.dy.get(i, vy);
       now.h.get(i, vh);
-      if (a.weight) w.get(i, vw);
+      w.get(i, vw);
 #pragma unroll
       for (int k = 0; k < S::STEP; ++k) {
-        const float xhat = vh[k] * now.r;
+        const float xhat = vh[k] * r;
         dw[i][k] = fmaf(vy[k], xhat, dw[i][k]);
-        dot = fmaf(a.weight ? vy[k] * vw[k] : vy[k], xhat, dot);
+        dot = fmaf(vy[k] * vw[k], xhat, dot);
       }
     }
     dot = warp_sum(dot);
@@ -322,12 +332,12 @@ __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS),
       float vy[S::STEP], vh[S::STEP], vw[S::STEP], vd[S::STEP];
       now.dy.get(i, vy);
       now.h.get(i, vh);
-      if (a.weight) w.get(i, vw);
-      if (a.dh) now.dh.get(i, vd);
+      w.get(i, vw);
+      if (DH) now.dh.get(i, vd);
 #pragma unroll
       for (int k = 0; k < S::STEP; ++k) {
-        const float g = a.weight ? vy[k] * vw[k] : vy[k];
-        vy[k] = fmaf(now.r, fmaf(-mean, vh[k] * now.r, g), a.dh ? vd[k] : 0.0f);
+        const float g = vy[k] * vw[k];
+        vy[k] = fmaf(r, fmaf(-mean, vh[k] * r, g), DH ? vd[k] : 0.0f);
       }
       store_step<T, false>(o.dx, row, c, vy);
     }
@@ -507,8 +517,9 @@ cudaError_t launch(const RmsNormGradArgs& a, float* partial, int sms, cudaStream
     row_layout<8>(a.d, [&](auto threads, auto values) {
       constexpr int THREADS = decltype(threads)::value, E = decltype(values)::value;
       constexpr int ROWS = rows_per_cta(THREADS);
-      err = launch_dependent(rms_norm_grad_kernel<T, W, THREADS, E>, parts / ROWS,
-                             THREADS * ROWS, stream, a, o, weight);
+      err = launch_dependent(a.dh ? rms_norm_grad_kernel<T, W, THREADS, E, true>
+                                  : rms_norm_grad_kernel<T, W, THREADS, E, false>,
+                             parts / ROWS, THREADS * ROWS, stream, a, o, weight);
     });
   } else {
     // The column sums come first: dx may overwrite dy.
