@@ -36,6 +36,7 @@ struct CopyJob {
 struct CopyJobs {
   CopyJob job[2];
   BoundsRecord* rec;
+  int count, blocks;
 };
 
 constexpr int kCopyThreads = 256;
@@ -205,8 +206,11 @@ void plan_linear_two(const LinearArgs& a, const LinearArgs& b, int sms, LinearPl
   *pb = plan_linear(b, sms);
   if (pa->pair || pb->pair) return;
   const int bt = std::max(pa->bt, pb->bt);
+  // The longer contraction decides (a cluster's CTA may have no slice of the
+  // shorter one): else 419 x 3655 x 345, whose gradients contract over 3655
+  // and over 419, would run the first unsplit.
   const int split = split_of(split_tiles(a, bt) + split_tiles(b, bt),
-                             std::min(ktiles_of(a), ktiles_of(b)), sms);
+                             std::max(ktiles_of(a), ktiles_of(b)), sms);
   use_split(a, bt, split, pa);
   use_split(b, bt, split, pb);
 }
@@ -241,27 +245,21 @@ struct Ready {
   uint32_t idesc;
 };
 
-// Copies what TMA cannot read in place and encodes the maps.
-cudaError_t make_ready(const LinearArgs& a, const LinearPlan& p, void* workspace,
-                       cudaStream_t stream, Ready* out) {
+// Adds the copies of what TMA cannot read in place and encodes the maps.
+cudaError_t make_ready(const LinearArgs& a, const LinearPlan& p, void* workspace, CopyJobs* jobs,
+                       Ready* out) {
   const int elem = dtype_bytes(a.dtype);
   Stored x = stored_x(a), w = stored_w(a);
   char* ws = static_cast<char*>(workspace);
-  if (p.copy_x_bytes || p.copy_w_bytes) {
-    CopyJobs jobs{};
-    jobs.rec = a.bounds;
-    int count = 0, blocks = 0;
-    auto add = [&](Stored* m, void* dst) {
-      jobs.job[count] = copy_job(m, elem, dst, blocks);
-      blocks += jobs.job[count++].blocks;
-    };
-    if (p.copy_x_bytes) add(&x, ws);
-    if (p.copy_w_bytes) add(&w, ws + p.copy_x_bytes);
-    if (count == 1) jobs.job[1].first_block = INT32_MAX;
-    const cudaError_t r = launch_dependent(copy_rows_kernel, dim3(static_cast<unsigned>(blocks)),
-                                           kCopyThreads, stream, jobs);
-    if (r != cudaSuccess) return r;
-  }
+  jobs->rec = a.bounds;
+  auto add = [&](Stored* m, void* dst) {
+    jobs->job[jobs->count] = copy_job(m, elem, dst, jobs->blocks);
+    jobs->blocks += jobs->job[jobs->count++].blocks;
+  };
+  if ((p.copy_x_bytes != 0) + (p.copy_w_bytes != 0) + jobs->count > 2)
+    return cudaErrorInvalidValue;
+  if (p.copy_x_bytes) add(&x, ws);
+  if (p.copy_w_bytes) add(&w, ws + p.copy_x_bytes);
   // A pair's CTAs load half a tile of each operand; without a product (K = 0)
   // the maps are not read.
   const int box_w = p.pair ? kPair / 2 : p.bc, box_x = p.pair ? kPair / 2 : p.bt;
@@ -274,6 +272,13 @@ cudaError_t make_ready(const LinearArgs& a, const LinearPlan& p, void* workspace
                            a.col_scale, static_cast<int>(a.T), static_cast<int>(a.C),
                            a.out_dtype, a.act, a.bounds};
   return cudaSuccess;
+}
+
+cudaError_t launch_copies(CopyJobs* jobs, cudaStream_t stream) {
+  if (jobs->count == 0) return cudaSuccess;
+  if (jobs->count == 1) jobs->job[1].first_block = INT32_MAX;
+  return launch_dependent(copy_rows_kernel, dim3(static_cast<unsigned>(jobs->blocks)),
+                          kCopyThreads, stream, *jobs);
 }
 
 SplitProblem problem_of(const LinearArgs& a, const LinearPlan& p, const Ready& r, int first_cta) {
@@ -295,7 +300,9 @@ cudaError_t launch_split(const LinearPlan& p, int dtype, int64_t grid, SplitProb
 cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
                           cudaStream_t stream, int fault_inject) {
   Ready r{};
-  const cudaError_t e = make_ready(a, p, workspace, stream, &r);
+  CopyJobs jobs{};
+  cudaError_t e = make_ready(a, p, workspace, &jobs, &r);
+  if (e == cudaSuccess) e = launch_copies(&jobs, stream);
   if (e != cudaSuccess) return e;
   if (p.pair)
     return launch_linear_pair(linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn), r.map_w, r.map_x,
@@ -315,9 +322,12 @@ cudaError_t launch_linear_two(const LinearArgs& a, const LinearPlan& pa, void* w
     const cudaError_t e = launch_linear(a, pa, wa, stream);
     return e != cudaSuccess ? e : launch_linear(b, pb, wb, stream);
   }
+  // At most two copies: dz is made for TMA to read.
   Ready ra{}, rb{};
-  cudaError_t e = make_ready(a, pa, wa, stream, &ra);
-  if (e == cudaSuccess) e = make_ready(b, pb, wb, stream, &rb);
+  CopyJobs jobs{};
+  cudaError_t e = make_ready(a, pa, wa, &jobs, &ra);
+  if (e == cudaSuccess) e = make_ready(b, pb, wb, &jobs, &rb);
+  if (e == cudaSuccess) e = launch_copies(&jobs, stream);
   if (e != cudaSuccess) return e;
   SplitProblems problems{};
   problems.p[0] = problem_of(a, pa, ra, 0);
