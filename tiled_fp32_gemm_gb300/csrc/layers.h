@@ -121,6 +121,7 @@ struct LinearArgs {
 struct LinearPlan {
   int pair;
   int bt, bc, split, stages, threads;
+  int cluster;  // CTAs of the launch's clusters: split, or 1 < cluster with split = 1
   int64_t smem_bytes, grid;
   int64_t copy_x_bytes, copy_w_bytes;  // padded copies of operands TMA cannot read
   int64_t workspace_bytes;

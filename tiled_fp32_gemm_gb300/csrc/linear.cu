@@ -153,14 +153,18 @@ int64_t split_tiles(const LinearArgs& a, int bt) {
   return ceil_div(a.C, LINEAR_BC) * ceil_div(a.T, bt);
 }
 
-// Sets the fields of a split-kernel plan that its tile and split decide.
-void use_split(const LinearArgs& a, int bt, int split, LinearPlan* p) {
+// A split-kernel plan with `split` CTAs to a tile in clusters of `cluster`.
+void use_split(const LinearArgs& a, int bt, int split, int cluster, LinearPlan* p) {
   const LinearKernel k = linear_split_kernel_for(a.dtype, bt);
+  p->pair = 0;
   p->bt = bt;
+  p->bc = LINEAR_BC;
+  p->threads = kThreads;
   p->split = split;
+  p->cluster = cluster;
   p->stages = k.stages;
   p->smem_bytes = k.smem;
-  p->grid = split_tiles(a, bt) * split;
+  p->grid = ceil_div(split_tiles(a, bt) * split, cluster) * cluster;
 }
 
 }  // namespace
@@ -185,14 +189,14 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
     p.threads = kPairThreads;
     p.bt = p.bc = kPair;
     p.split = 1;
+    p.cluster = 2;
     p.stages = k.stages;
     p.smem_bytes = k.smem;
     p.grid = 2 * std::min<int64_t>(pairs, sms / 2);
   } else {
     const int bt = a.T <= 16 && !a.x_mn ? 16 : a.T <= 32 && !a.x_mn ? 32 : a.T <= 64 ? 64 : 128;
-    p.bc = LINEAR_BC;
-    p.threads = kThreads;
-    use_split(a, bt, split_of(split_tiles(a, bt), ktiles_of(a), sms), &p);
+    const int split = split_of(split_tiles(a, bt), ktiles_of(a), sms);
+    use_split(a, bt, split, split, &p);
   }
   p.copy_x_bytes = a.K > 0 ? copy_bytes(stored_x(a), elem) : 0;
   p.copy_w_bytes = a.K > 0 ? copy_bytes(stored_w(a), elem) : 0;
@@ -204,15 +208,34 @@ void plan_linear_two(const LinearArgs& a, const LinearArgs& b, int sms, LinearPl
                      LinearPlan* pb) {
   *pa = plan_linear(a, sms);
   *pb = plan_linear(b, sms);
-  if (pa->pair || pb->pair) return;
-  const int bt = std::max(pa->bt, pb->bt);
-  // The longer contraction decides (a cluster's CTA may have no slice of the
-  // shorter one): else 419 x 3655 x 345, whose gradients contract over 3655
-  // and over 419, would run the first unsplit.
-  const int split = split_of(split_tiles(a, bt) + split_tiles(b, bt),
-                             std::max(ktiles_of(a), ktiles_of(b)), sms);
-  use_split(a, bt, split, pa);
-  use_split(b, bt, split, pb);
+  // Two products that fill the GPU by pairs run one after the other; one that
+  // does so less than twice joins the other's launch instead.
+  if (pa->pair && pb->pair) return;
+  const LinearArgs& paired = pa->pair ? a : b;
+  if ((pa->pair || pb->pair) && ceil_div(paired.C, kPair) * ceil_div(paired.T, kPair) >= sms)
+    return;
+  const int bt = std::max(pa->pair ? 128 : pa->bt, pb->pair ? 128 : pb->bt);
+  const int64_t ta = split_tiles(a, bt), tb = split_tiles(b, bt);
+  const int64_t ka = ktiles_of(a), kb = ktiles_of(b);
+  // The cluster: the most CTAs (of at least four K tiles each) that the split
+  // product or products find places for beside the other, or, where one
+  // contraction is four times the other's, beside its own tiles alone: else
+  // 527 x 4472 x 512, whose gradients contract over 4472 and over 527, would
+  // wait for 20 CTAs with 70 K tiles each.
+  auto slices = [](int64_t k, int s) { return k >= 4 * s ? s : 1; };
+  int cluster = 1;
+  for (int s : {8, 4, 3, 2}) {
+    const int64_t places = s == 8 ? sms * 3 / 4 : s > 2 ? 2 * sms * 9 / 10 : 2 * sms;
+    const int64_t ca = ta * slices(ka, s), cb = tb * slices(kb, s);
+    const bool lone = std::max(ka, kb) >= 4 * std::min(ka, kb) && s < 8;
+    if (std::max(ka, kb) >= 4 * s &&
+        (ca + cb <= places || (lone && (ka > kb ? ca : cb) <= places))) {
+      cluster = s;
+      break;
+    }
+  }
+  use_split(a, bt, slices(ka, cluster), cluster, pa);
+  use_split(b, bt, slices(kb, cluster), cluster, pb);
 }
 
 cudaError_t linear_prepare() {
@@ -283,15 +306,16 @@ cudaError_t launch_copies(CopyJobs* jobs, cudaStream_t stream) {
 
 SplitProblem problem_of(const LinearArgs& a, const LinearPlan& p, const Ready& r, int first_cta) {
   return SplitProblem{r.map_w, r.map_x, r.ep, r.idesc, static_cast<int>(ktiles_of(a)),
-                      static_cast<int>(ceil_div(a.T, p.bt)), first_cta, a.w_mn, a.x_mn};
+                      static_cast<int>(split_tiles(a, p.bt)),
+                      static_cast<int>(ceil_div(a.T, p.bt)), first_cta, p.split, a.w_mn,
+                      a.x_mn};
 }
 
 cudaError_t launch_split(const LinearPlan& p, int dtype, int64_t grid, SplitProblems* problems,
                          int fault_inject, cudaStream_t stream) {
-  int split = p.split;
-  void* args[] = {problems, &split, &fault_inject};
+  void* args[] = {problems, &fault_inject};
   return launch_dependent(linear_split_kernel_for(dtype, p.bt).kernel,
-                          dim3(static_cast<unsigned>(grid)), kThreads, p.smem_bytes, split,
+                          dim3(static_cast<unsigned>(grid)), kThreads, p.smem_bytes, p.cluster,
                           stream, args);
 }
 
@@ -317,7 +341,7 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* worksp
 cudaError_t launch_linear_two(const LinearArgs& a, const LinearPlan& pa, void* wa,
                               const LinearArgs& b, const LinearPlan& pb, void* wb,
                               cudaStream_t stream) {
-  if (pa.pair || pb.pair || pa.bt != pb.bt || pa.split != pb.split || a.dtype != b.dtype ||
+  if (pa.pair || pb.pair || pa.bt != pb.bt || pa.cluster != pb.cluster || a.dtype != b.dtype ||
       pa.grid + pb.grid > INT32_MAX) {
     const cudaError_t e = launch_linear(a, pa, wa, stream);
     return e != cudaSuccess ? e : launch_linear(b, pb, wb, stream);
@@ -330,8 +354,14 @@ cudaError_t launch_linear_two(const LinearArgs& a, const LinearPlan& pa, void* w
   if (e == cudaSuccess) e = launch_copies(&jobs, stream);
   if (e != cudaSuccess) return e;
   SplitProblems problems{};
-  problems.p[0] = problem_of(a, pa, ra, 0);
-  problems.p[1] = problem_of(b, pb, rb, static_cast<int>(pa.grid));
+  // The longer contraction's CTAs start first.
+  if (ktiles_of(a) >= ktiles_of(b)) {
+    problems.p[0] = problem_of(a, pa, ra, 0);
+    problems.p[1] = problem_of(b, pb, rb, static_cast<int>(pa.grid));
+  } else {
+    problems.p[0] = problem_of(b, pb, rb, 0);
+    problems.p[1] = problem_of(a, pa, ra, static_cast<int>(pb.grid));
+  }
   return launch_split(pa, a.dtype, pa.grid + pb.grid, &problems, 0, stream);
 }
 

@@ -247,7 +247,8 @@ struct SplitProblem {
   CUtensorMap map_w, map_x;
   LinearEpilogue ep;
   uint32_t idesc;
-  int ktiles, tiles_t, first_cta;
+  int ktiles, tiles, tiles_t, first_cta;
+  int split;  // CTAs that share a tile: the launch's cluster, or 1
   int w_mn, x_mn;
 };
 struct SplitProblems {

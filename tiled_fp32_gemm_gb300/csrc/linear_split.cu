@@ -13,7 +13,8 @@
 //     r adds rows r * q .. of all of them, in slice order, so the result does
 //     not depend on timing.
 // One launch takes one product or two that do not depend on one another (the
-// layer's two gradients), of the same type and tile.
+// layer's two gradients), of the same type and tile; each either splits its
+// tiles over the launch's clusters or takes a tile per CTA.
 // Every wait is bounded, as in the other tcgen05 kernels; a CTA that gave up
 // leaves its flag where its cluster sees it, and none of them stores.
 #include <cstdint>
@@ -61,8 +62,7 @@ __device__ __forceinline__ void load_sums(uint32_t addr, bool any, Rows& v) {
 
 template <class E, int BT>
 __global__ void __launch_bounds__(THREADS, 2)
-    linear_split_kernel(const __grid_constant__ SplitProblems problems, int split,
-                        int fault_inject) {
+    linear_split_kernel(const __grid_constant__ SplitProblems problems, int fault_inject) {
   using G = SplitGeometry<BT>;
   constexpr int STAGES = G::STAGES;
   constexpr int BK_ELEMS = ROW_BYTES / E::BYTES;
@@ -85,8 +85,10 @@ __global__ void __launch_bounds__(THREADS, 2)
   auto bar = [&](int i) { return smem_u32(bars + i); };
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int split = P.split;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = (static_cast<int>(blockIdx.x) - P.first_cta) / split;
+  if (tile >= P.tiles) return;  // fills up an unsplit product's last cluster
   // Tiles of one weight panel follow each other, so the panel is read from
   // memory once and found in L2 by the rest.
   const int c0 = tile / P.tiles_t * BC, t0 = tile % P.tiles_t * BT;
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
 #pragma unroll
       for (int i = 0; i < FINISH_ROWS; ++i) v[i] = 0.0f;
-#pragma unroll 1
+#pragma unroll 4
       for (int s = 0; s < split; ++s) {
         const uint32_t from = map_to_cta(smem_u32(sums + t * BC + c), s);
 #pragma unroll
