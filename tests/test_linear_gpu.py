@@ -244,6 +244,26 @@ def test_a_wait_that_runs_out_is_reported():
     assert (y == 2048).all()
 
 
+def test_a_wait_that_runs_out_on_cta_pairs_is_reported():
+    """As above on the persistent kernel (90 tiles of 256 x 256)."""
+    a = torch.ones(2304, 64, dtype=torch.bfloat16, device="cuda")
+    b = torch.ones(64, 2560, dtype=torch.bfloat16, device="cuda")
+    y = torch.full((2304, 2560), 7.0, dtype=torch.bfloat16, device="cuda")
+    p = mt.mt_linear_args(M=2304, N=2560, K=64, A=a.data_ptr(), lda=64, B=b.data_ptr(), ldb=2560,
+                          Y=y.data_ptr(), ldy=2560, dtype=mt.MT_DTYPE_BF16,
+                          out_dtype=mt.MT_DTYPE_BF16, fault_inject=1)
+    st, plan = mt.mt_linear_plan(p, 152)
+    assert st == mt.MT_OK and plan.bm == 256
+    torch.cuda.synchronize()
+    assert mt.mt_linear(p, 0) == mt.MT_OK
+    assert mt.mt_check_device_status(0) == mt.MT_ERR_TIMEOUT
+    assert (y == 7).all()
+    p.fault_inject = 0
+    assert mt.mt_linear(p, 0) == mt.MT_OK
+    assert mt.mt_check_device_status(0) == mt.MT_OK
+    assert (y == 64).all()
+
+
 def test_refusals():
     a = torch.zeros(4, 8, dtype=torch.bfloat16, device="cuda")
     b = torch.zeros(8, 16, dtype=torch.bfloat16, device="cuda")

@@ -116,12 +116,12 @@ bool aligned(const LinearDzArgs& a) {
          (a.act == ACT_NONE || rows_aligned(a.Z, a.ldz, 2));
 }
 
-// Groups of rows: four CTAs on every SM, but no CTA with fewer than 32 rows
+// Groups of rows: four CTAs on every SM, but no CTA with fewer than 16 rows
 // once there is one group.
 int row_groups(const LinearDzArgs& a, int sms) {
   const int64_t strips = (a.N - 1) / STRIP + 1;
   const int64_t want = 4 * static_cast<int64_t>(sms) / (strips * CLUSTER);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, a.M / (32 * CLUSTER))));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, a.M / (16 * CLUSTER))));
 }
 
 template <class T, int ACT>
