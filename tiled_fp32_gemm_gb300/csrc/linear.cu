@@ -178,12 +178,12 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
   LinearPlan p{};
   const int elem = dtype_bytes(a.dtype);
   const int64_t pairs = ceil_div(a.C, kPair) * ceil_div(a.T, kPair);
-  // CTA pairs when their tiles fill three tenths of the GPU, and with tokens,
-  // not padding.  Measured (bf16, gelu, bias and residual, N = K = 4096, us
+  // CTA pairs when their tiles fill two sevenths of the GPU's SMs, and with
+  // tokens, not padding.  Measured (bf16, gelu, bias and residual, N = K = 4096, us
   // for pairs against the split kernel): 512 tokens (32 pairs) 32.0 / 28.0,
   // 768 (48) 33.1 / 38.5, 1024 (64) 33.2 / 39.0, 2048 (128) 55.1 / 74.7;
   // e4m3 512 tokens 23.9 / 21.5, 768 25.2 / 27.1, 2048 38.8 / 52.4.
-  p.pair = a.K > 0 && 10 * pairs >= 3 * sms && a.T > 128;
+  p.pair = a.K > 0 && 7 * pairs >= 2 * sms && a.T > 128;
   if (p.pair) {
     const LinearKernel k = linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn);
     p.threads = kPairThreads;
@@ -209,7 +209,8 @@ void plan_linear_two(const LinearArgs& a, const LinearArgs& b, int sms, LinearPl
   *pa = plan_linear(a, sms);
   *pb = plan_linear(b, sms);
   // Two products that fill the GPU by pairs run one after the other; one that
-  // does so less than twice joins the other's launch instead.
+  // has fewer pairs than the GPU has SMs joins the other's launch instead
+  // (128 x 2048 x 4096, 128 pairs: 29.9 us apart, 26.0 together).
   if (pa->pair && pb->pair) return;
   const LinearArgs& paired = pa->pair ? a : b;
   if ((pa->pair || pb->pair) && ceil_div(paired.C, kPair) * ceil_div(paired.T, kPair) >= sms)
