@@ -179,11 +179,12 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
   const int elem = dtype_bytes(a.dtype);
   const int64_t pairs = ceil_div(a.C, kPair) * ceil_div(a.T, kPair);
   // CTA pairs when their tiles fill two sevenths of the GPU's SMs, and with
-  // tokens, not padding.  Measured (bf16, gelu, bias and residual, N = K = 4096, us
-  // for pairs against the split kernel): 512 tokens (32 pairs) 32.0 / 28.0,
-  // 768 (48) 33.1 / 38.5, 1024 (64) 33.2 / 39.0, 2048 (128) 55.1 / 74.7;
-  // e4m3 512 tokens 23.9 / 21.5, 768 25.2 / 27.1, 2048 38.8 / 52.4.
-  p.pair = a.K > 0 && 7 * pairs >= 2 * sms && a.T > 128;
+  // tokens, not padding (and the kernel's tile indices are 32-bit).  Measured
+  // (bf16, gelu, bias and residual, N = K = 4096, us for pairs against the
+  // split kernel): 512 tokens (32 pairs) 32.0 / 28.0, 768 (48) 33.1 / 38.5,
+  // 1024 (64) 33.2 / 39.0, 2048 (128) 55.1 / 74.7; e4m3 512 tokens 23.9 / 21.5,
+  // 768 25.2 / 27.1, 2048 38.8 / 52.4.
+  p.pair = a.K > 0 && 7 * pairs >= 2 * sms && a.T > 128 && pairs <= INT32_MAX / 8;
   if (p.pair) {
     const LinearKernel k = linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn);
     p.threads = kPairThreads;

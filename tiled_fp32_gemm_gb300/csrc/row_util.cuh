@@ -77,7 +77,6 @@ struct Pack8;
 template <>
 struct Pack8<float> {
   float4 lo, hi;
-  __device__ __forceinline__ void keep() {}
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
@@ -90,9 +89,6 @@ struct Pack8<float> {
 template <>
 struct Pack8<__half> {
   uint4 u;
-  __device__ __forceinline__ void keep() {
-    asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
-  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -115,9 +111,6 @@ struct Pack8<__half> {
 template <>
 struct Pack8<__nv_bfloat16> {
   uint4 u;
-  __device__ __forceinline__ void keep() {
-    asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
-  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -222,14 +215,6 @@ struct Held {
       const int64_t at = row * m.ld + c;
       if (c < d && m.ok(at, S::STEP)) item[i] = *reinterpret_cast<const Item*>(m.p + at);
       else item[i] = Item{};
-    }
-  }
-  // Between two uses: the packed form is what stays in registers (else the
-  // compiler keeps the first use's fp32 values for the second).
-  __device__ __forceinline__ void keep() {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < S::COUNT; ++i) item[i].keep();
     }
   }
   __device__ __forceinline__ void fill(float value) {
