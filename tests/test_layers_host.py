@@ -273,3 +273,17 @@ def test_arguments_have_the_c_layout(tmp_path):
                     "-I", cuda, str(src), "-o", str(exe)], check=True)
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
     assert [int(v) for v in out.split()] == want
+
+
+def test_linear_plans_hold_their_tile_indices_in_32_bits():
+    """256 x 256 tiles go to CTA pairs up to 2^28 - 1 of them; past that to the
+    128 x 128 tiles of the split kernel, whose grid is refused past 2^31 - 1."""
+    def status(M, N):
+        a = linear_args(M=M, N=N, K=64, lda=64, ldb=N, ldy=N, ldz=N, ldr=N)
+        return mt.mt_linear_plan(a, 152)
+    st, p = status(2 ** 22 - 256, 2 ** 22)             # 2^28 - 2^14 pair tiles
+    assert st == mt.MT_OK and p.bn == 256
+    st, p = status(2 ** 22, 2 ** 22)                   # 2^28
+    assert st == mt.MT_OK and p.bn == 128 and p.grid == 2 ** 30
+    st, _ = status(2 ** 23, 2 ** 22)                   # a grid of 2^31
+    assert st == mt.MT_ERR_UNSUPPORTED
