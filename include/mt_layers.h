@@ -73,9 +73,9 @@ typedef struct {
  * be x or residual itself, and y may be x itself (same pointer and pitch);
  * any other overlap of an output with an input or another output is
  * MT_ERR_ALIAS.  Pointers must be aligned to their element.  Other errors:
- * MT_ERR_INVALID_ARG (NULL args, negative or too large size, pitch shorter
- * than a row, missing pointer, unknown type combination, eps negative or
- * not finite), MT_ERR_NO_DEVICE, MT_ERR_LAUNCH.
+ * MT_ERR_INVALID_ARG (NULL args, a negative size, d past 2^31 - 512, rows past
+ * 2^31 - 1, pitch shorter than a row, missing pointer, unknown type
+ * combination, eps negative or not finite), MT_ERR_NO_DEVICE, MT_ERR_LAUNCH.
  */
 MT_API mt_status mt_rms_norm(const mt_rms_norm_args *args, cudaStream_t stream);
 

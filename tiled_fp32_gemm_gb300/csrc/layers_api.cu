@@ -27,6 +27,9 @@ static_assert(MT_ACT_RELU == mt::ACT_RELU && MT_ACT_GELU == mt::ACT_GELU &&
 // Largest row, column or contraction count of a product: tile coordinates
 // past the edge stay inside 32 bits.
 constexpr int64_t kMaxSize = INT32_MAX - 255;
+// Longest row of a norm: the row-wise kernels step a 32-bit column by up to
+// 512, and round the columns up to whole strips of 32.
+constexpr int64_t kMaxRow = INT32_MAX - 511;
 
 // A rows x cols view of `elem`-byte values with row pitch ld, for the checks.
 struct View {
@@ -132,7 +135,7 @@ mt_status prepare_linear(int dev) {
 extern "C" {
 
 mt_status mt_rms_norm(const mt_rms_norm_args* g, cudaStream_t stream) {
-  if (!g || g->rows < 0 || g->d < 0 || g->d > INT32_MAX || g->rows > INT32_MAX)
+  if (!g || g->rows < 0 || g->d < 0 || g->d > kMaxRow || g->rows > INT32_MAX)
     return MT_ERR_INVALID_ARG;
   if (!half_type(g->dtype) && g->dtype != MT_DTYPE_F32) return MT_ERR_INVALID_ARG;
   if (g->out_dtype != g->dtype && g->out_dtype != MT_DTYPE_E4M3) return MT_ERR_INVALID_ARG;
@@ -176,7 +179,7 @@ mt_status mt_rms_norm(const mt_rms_norm_args* g, cudaStream_t stream) {
 }
 
 mt_status mt_rms_norm_backward(const mt_rms_norm_backward_args* g, cudaStream_t stream) {
-  if (!g || g->rows < 0 || g->d < 0 || g->d > INT32_MAX || g->rows > INT32_MAX)
+  if (!g || g->rows < 0 || g->d < 0 || g->d > kMaxRow || g->rows > INT32_MAX)
     return MT_ERR_INVALID_ARG;
   if (!half_type(g->dtype) && g->dtype != MT_DTYPE_F32) return MT_ERR_INVALID_ARG;
   if (g->weight && g->weight_dtype != g->dtype && g->weight_dtype != MT_DTYPE_F32)
