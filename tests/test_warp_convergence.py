@@ -1,0 +1,28 @@
+"""Warp-wide instructions of the feed-forward kernels (PTX `.aligned`: every
+lane executes the same one together) follow a point where the warp has met.
+After a lane-dependent branch nothing but a warp barrier promises that, so it
+stands in the source; which lanes reconverge on their own shows in no result."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "tiled_fp32_gemm_gb300", "csrc")
+
+
+def source(name):
+    """A source file without its comments, blanks run together."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    text = re.sub(r"//[^\n]*|/\*.*?\*/", " ", text, flags=re.S)
+    return re.sub(r"\s+", " ", text)
+
+
+def test_drain_reads_its_sums_with_a_whole_warp():
+    """Lanes at or past the last column skip the stores of a block of rows
+    (and the residual's loads); the next block's sums come from tensor memory
+    by a warp-wide load."""
+    text = source("linear.cuh")
+    calls = [m.start() for m in re.finditer(r"\bsums\(t, v\);", text)]
+    assert calls
+    for at in calls:
+        assert text[:at].rstrip().endswith("__syncwarp();")

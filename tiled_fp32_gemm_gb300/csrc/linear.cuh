@@ -202,6 +202,9 @@ __device__ __forceinline__ void finish_typed(const LinearEpilogue& e, int c, int
     }
     if (e.row_scale && rows > FINISH_ROWS) next_scale = scale_of(t + FINISH_ROWS);
     Rows v;
+    // Lanes past the last column have left the last round early, and the
+    // residual's loads are theirs alone: the sums are read by the whole warp.
+    __syncwarp();
     sums(t, v);
     if (e.row_scale) {
 #pragma unroll
@@ -223,8 +226,8 @@ __device__ __forceinline__ void finish_typed(const LinearEpilogue& e, int c, int
 }
 
 // Finishes column c of Y, rows t_begin .. t_end - 1 (t_end <= e.T; columns at
-// or past e.C are dropped), the whole warp together: sums(t, v) gives the
-// sums of rows t .. t + FINISH_ROWS - 1.
+// or past e.C are dropped), the whole warp together: sums(t, v), called by a
+// converged warp, gives the sums of rows t .. t + FINISH_ROWS - 1.
 template <class Sums>
 __device__ __forceinline__ void finish(const LinearEpilogue& e, int c, int t_begin, int t_end,
                                        Sums&& sums) {
