@@ -26,3 +26,20 @@ def test_drain_reads_its_sums_with_a_whole_warp():
     assert calls
     for at in calls:
         assert text[:at].rstrip().endswith("__syncwarp();")
+
+
+def test_cluster_barrier_meets_the_warp_first():
+    """Its callers arrive from lane-dependent branches (a store for the last
+    columns alone, a bounded spin)."""
+    body = re.search(r"void cluster_sync\(\) \{(.*?)\}", source("tcgen05.cuh")).group(1)
+    assert body.index("__syncwarp();") < body.index("barrier.cluster.arrive.release.aligned")
+
+
+def test_named_barrier_meets_the_warp_first():
+    """bar.sync is barrier.sync.aligned; lane 0 alone has just written the
+    row's sum or arrived on the stage's barrier."""
+    text = source("rms_norm_grad.cu")
+    calls = [m.start() for m in re.finditer(r'asm volatile\("bar\.sync', text)]
+    assert calls
+    for at in calls:
+        assert text[:at].rstrip().endswith("__syncwarp(); if (warps > 1)")

@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 
   if (split > 1) {
-    __syncwarp();
     cluster_sync();  // every CTA's sums (or its abort flag) are in place
     if (warp >= 2)
       for (int s = 0; s < split; ++s)
@@ -214,7 +213,6 @@ __global__ void __launch_bounds__(THREADS, 2)
     });
   }
   if (split > 1) {
-    __syncwarp();
     cluster_sync();  // no CTA leaves while its sums are being read
   }
 

@@ -171,10 +171,9 @@ __global__ void __launch_bounds__(MOST + 32, 1)
       if (lane == 0) sums[n & 1][warp] = dot;
     };
     auto meet = [&] {
+      __syncwarp();  // lane 0 alone wrote or arrived last; bar.sync wants the warp converged
       if (warps > 1)
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(g.threads) : "memory");
-      else
-        __syncwarp();
     };
     float r = rstd_of(row_0 + group), r_next = rstd_of(row_0 + step + group);
     if (row_0 < a.rows) first_sweep(0, row_0 + group < a.rows, r);

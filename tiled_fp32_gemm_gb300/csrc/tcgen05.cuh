@@ -130,8 +130,11 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// Every thread of every CTA of the cluster (release / acquire).
+// Every thread of every CTA of the cluster (release / acquire).  Both
+// instructions want a converged warp, which a lane-dependent branch before
+// them does not leave.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
