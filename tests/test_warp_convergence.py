@@ -43,3 +43,15 @@ def test_named_barrier_meets_the_warp_first():
     assert calls
     for at in calls:
         assert text[:at].rstrip().endswith("__syncwarp(); if (warps > 1)")
+
+
+def test_products_read_their_accumulator_with_a_whole_warp():
+    """Each chunk of the drain ends in stores that rows past the last (or
+    columns past it) skip, and the next begins with a warp-wide load."""
+    text = source("tcgen05.cuh")
+    body = text[text.index("store_accumulator("):]
+    loops = body.split("for (int ch = 0; ch < BN / 32; ++ch)")[1:]
+    assert len(loops) == 2
+    assert loops[0].rstrip().startswith("{ float v[32]; tmem_ld32(")
+    assert loops[0].split("return;")[0].rstrip(" }").endswith("__syncwarp();")
+    assert loops[1].lstrip().startswith("{ float v[32]; __syncwarp(); tmem_ld32(")

@@ -584,6 +584,7 @@ __device__ __forceinline__ void store_accumulator(uint32_t t_row, const Unit& w,
 #pragma unroll 1
   for (int ch = 0; ch < BN / 32; ++ch) {
     float v[32];
+    __syncwarp();  // rows past M skipped the last chunk's stores
     tmem_ld32(t_row + ch * 32, v);
     const int col0 = w.tn * BN + ch * 32;
     if (w.pidx >= 0) {
