@@ -52,6 +52,6 @@ def test_products_read_their_accumulator_with_a_whole_warp():
     body = text[text.index("store_accumulator("):]
     loops = body.split("for (int ch = 0; ch < BN / 32; ++ch)")[1:]
     assert len(loops) == 2
-    assert loops[0].rstrip().startswith("{ float v[32]; tmem_ld32(")
+    assert loops[0].lstrip().startswith("{ float v[32]; tmem_ld32(")
     assert loops[0].split("return;")[0].rstrip(" }").endswith("__syncwarp();")
     assert loops[1].lstrip().startswith("{ float v[32]; __syncwarp(); tmem_ld32(")
