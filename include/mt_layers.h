@@ -116,8 +116,11 @@ MT_API mt_status mt_rms_norm_backward(const mt_rms_norm_backward_args *args,
                                       cudaStream_t stream);
 
 /* Activations of mt_linear, in fp32: identity, max(z, 0) (a NaN stays one),
- * z * Phi(z) with the normal distribution's Phi (by erf), its tanh form
- * z / 2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))), z / (1 + exp(-z)). */
+ * z * Phi(z) with the normal distribution's Phi, its tanh form
+ * z / 2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))), z / (1 + exp(-z)).
+ * Evaluated to 2^-20 of the result where Y is fp32 (the tanh form's argument,
+ * -2 u say, adds 5 |u| 2^-24 of it), to 2^-15 of it before its rounding where
+ * Y is 16-bit; there, what is below 2^-110 may be zero. */
 typedef enum {
     MT_ACT_NONE = 0,
     MT_ACT_RELU = 1,

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -26,41 +27,57 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// 1 / (1 + exp(-z)).  exp overflows to infinity for z below -88, which gives
-// the 0 that is wanted.
+// 1 / (1 + exp(-z)), for 16-bit results.  exp overflows to infinity for z
+// below -88, which gives the 0 that is wanted.
 __device__ __forceinline__ float logistic(float z) {
   return rcp_approx(1.0f + exp_approx(-z));
 }
+// The same for fp32 results: no overflow, and the digits of CUDA's expf and
+// division.
+__device__ __forceinline__ float logistic_f32(float z) {
+  const float e = expf(-fabsf(z));
+  return (z < 0.0f ? e : 1.0f) / (1.0f + e);
+}
 
-// The normal distribution's Phi(z) = (1 + erf(z / sqrt 2)) / 2 by Hastings'
-// approximation of erf (Abramowitz and Stegun, Handbook of Mathematical
-// Functions, 7.1.26: five coefficients, one exponential, absolute error below
-// 1.5e-7), without the branches of a correctly scaled erf: every lane of a
-// warp takes the same path.  *bell: exp(-z^2 / 2).
+// The normal distribution's Phi(z) and *bell = exp(-z^2 / 2), for 16-bit
+// results and the derivative.  With x = |z| / sqrt 2, Phi(-|z|) is bell *
+// erfcx(x) / 2, erfcx(x) = exp(x^2) erfc(x).  That falls from 1 to 1 / (x
+// sqrt pi) without ever being small, so a polynomial in t = 1 / (1 + 0.43 x)
+// without constant term holds it to a *relative* error, which is what keeps
+// the tail's digits: these eight coefficients are a minimax fit (Lawson's
+// reweighted least squares) over 0 <= x <= 10, within 1.0e-7, 4.5e-7 as
+// evaluated here.  No branches: every lane of a warp takes the same path.
 __device__ __forceinline__ float normal_cdf(float z, float* bell) {
   const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = rcp_approx(fmaf(0.3275911f, x, 1.0f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
+  const float t = rcp_approx(fmaf(0.43f, x, 1.0f));
+  float p = fmaf(0.0731455436f, t, -0.308094499f);
+  p = fmaf(p, t, 0.379885357f);
+  p = fmaf(p, t, -0.0823025803f);
+  p = fmaf(p, t, 0.245079788f);
+  p = fmaf(p, t, 0.205472764f);
+  p = fmaf(p, t, 0.244293791f);
+  p = fmaf(p, t, 0.242519823f);
   *bell = exp_approx(-x * x);
   const float tail = 0.5f * p * t * *bell;  // Phi(-|z|)
   return z > 0.0f ? 1.0f - tail : tail;
 }
 
 // The activations, in fp32.  (1 + tanh u) / 2 is the logistic function of 2u.
-template <int ACT>
+// 16-bit results (F32 false) take the special-function unit's exponential,
+// whose argument's rounding costs up to 2^-15 of a result far out in a tail,
+// an eighth of half a step of fp16; fp32 results take CUDA's functions.
+template <int ACT, bool F32>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == ACT_RELU) {
     return z < 0.0f ? 0.0f : z;  // a NaN stays one
   } else if constexpr (ACT == ACT_GELU) {
     float bell;
-    return z * normal_cdf(z, &bell);
+    return z * (F32 ? normcdff(z) : normal_cdf(z, &bell));
   } else if constexpr (ACT == ACT_GELU_TANH) {
-    return z * logistic(1.5957691216057308f * fmaf(0.044715f * z * z, z, z));
+    const float u = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
+    return z * (F32 ? logistic_f32(u) : logistic(u));
   } else if constexpr (ACT == ACT_SILU) {
-    return z * logistic(z);
+    return z * (F32 ? logistic_f32(z) : logistic(z));
   } else {
     return z;
   }
@@ -108,18 +125,19 @@ struct LinearEpilogue {
 constexpr int FINISH_ROWS = 16;
 using Rows = float[FINISH_ROWS];
 
-template <int ACT>
+template <int ACT, bool F32>
 __device__ __forceinline__ void activate_rows(Rows& v) {
 #pragma unroll
-  for (int i = 0; i < FINISH_ROWS; ++i) v[i] = activate<ACT>(v[i]);
+  for (int i = 0; i < FINISH_ROWS; ++i) v[i] = activate<ACT, F32>(v[i]);
 }
 
+template <bool F32>
 __device__ __forceinline__ void activate_rows(int act, Rows& v) {
   switch (act) {
-    case ACT_RELU: return activate_rows<ACT_RELU>(v);
-    case ACT_GELU: return activate_rows<ACT_GELU>(v);
-    case ACT_GELU_TANH: return activate_rows<ACT_GELU_TANH>(v);
-    case ACT_SILU: return activate_rows<ACT_SILU>(v);
+    case ACT_RELU: return activate_rows<ACT_RELU, F32>(v);
+    case ACT_GELU: return activate_rows<ACT_GELU, F32>(v);
+    case ACT_GELU_TANH: return activate_rows<ACT_GELU_TANH, F32>(v);
+    case ACT_SILU: return activate_rows<ACT_SILU, F32>(v);
     default: return;
   }
 }
@@ -216,7 +234,7 @@ __device__ __forceinline__ void finish_typed(const LinearEpilogue& e, int c, int
     }
     if (!live) continue;
     if (e.Z) z.store(t, rows, v);
-    activate_rows(e.act, v);
+    activate_rows<std::is_same<T, float>::value>(e.act, v);
     if (e.residual) {
 #pragma unroll
       for (int i = 0; i < FINISH_ROWS; ++i) v[i] += row::to_f32(res[i]);
