@@ -24,8 +24,8 @@
 extern "C" {
 #endif
 
-/* An unused fp8 scale is never smaller than this (2^-126): a row of zeros
- * gets it, and its 8-bit values are zeros. */
+/* No fp8 scale is smaller than this (2^-126): a row of zeros gets it, and its
+ * 8-bit values are zeros. */
 #define MT_SCALE_MIN 1.17549435082228751e-38f
 /* Largest finite e4m3 value. */
 #define MT_E4M3_MAX 448.0f
@@ -34,10 +34,12 @@ extern "C" {
  * Root-mean-square norm with the residual's addition:
  *
  *     h[i][k] = x[i][k] + residual[i][k]            (residual NULL: x)
- *     r[i]    = 1 / sqrt(mean_k h[i][k]^2 + eps)
+ *     r[i]    = 1 / sqrt(mean_k h[i][k]^2 + eps)    (0 for 1 / 0)
  *     y[i][k] = h[i][k] * r[i] * weight[k]          (weight NULL: ones)
  *
- * h is summed in fp32 and enters the norm unrounded.  Written: h in x's type
+ * A row whose mean square is 0 with eps 0 gets r = 0: its y is zeros, and the
+ * gradient below leaves it dh alone.  h is summed in fp32 and enters the norm
+ * unrounded.  Written: h in x's type
  * (h NULL: not written), r to `rstd` (rows floats; NULL: not written; the
  * gradient reads it), and y either in x's type (out_dtype == dtype) or in 8
  * bits with one scale per row (out_dtype == MT_DTYPE_E4M3):
@@ -45,7 +47,8 @@ extern "C" {
  *     scale[i] = max(max_k |y[i][k]| / 448, 2^-126)
  *     y8[i][k] = e4m3(y[i][k] / scale[i])           (nearest even)
  *
- * A NaN in a row makes the whole row, its r and its scale NaN; an infinite
+ * A NaN in a row makes the whole row, its r and its scale NaN; a mean square
+ * past fp32's range (values past 1.8e19) makes r and a finite y 0; an infinite
  * element makes r 0 and its own y NaN (and, in 8 bits, the whole row and its
  * scale NaN).
  */

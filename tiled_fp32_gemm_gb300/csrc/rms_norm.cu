@@ -34,7 +34,8 @@ template <class T, bool E4M3>
 __device__ __forceinline__ float row_factors(const RmsNormArgs& a, const Operands<T>& o,
                                              int64_t row, float sum, float top, bool writer,
                                              float* inv) {
-  const float r = rsqrtf((a.d > 0 ? sum / static_cast<float>(a.d) : 0.0f) + a.eps);
+  const float m = (a.d > 0 ? sum / static_cast<float>(a.d) : 0.0f) + a.eps;
+  const float r = m == 0.0f ? 0.0f : rsqrtf(m);  // zeros stay zeros without an eps
   if (writer && a.rstd) o.rstd.store(row, 0, r);
   if (E4M3) {
     const float t = top * r / 448.0f;
