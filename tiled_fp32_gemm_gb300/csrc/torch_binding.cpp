@@ -81,6 +81,17 @@ cudaStream_t stream_of(const at::Tensor& t) {
 
 bool flag(PyObject* o) { return o == Py_True; }
 
+// Leaves the interpreter to other threads for a scope: allocations and launches
+// may wait (for the device, a full queue, a host callback written in Python).
+// The operands stay alive through the caller's references.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 PyObject* none() { Py_RETURN_NONE; }
 PyObject* refused(mt_status st) { return PyLong_FromLong(st); }
 
@@ -136,28 +147,34 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       g.weight = w.t->data_ptr();
       g.weight_dtype = code_of(w.t->scalar_type());
     }
-    at::Tensor h, y, rstd, scale;
     if (r.t) {
       if (!m.read(*r.t, g.rows, g.d, type, dev)) return none();
       g.residual = m.p;
       g.ldr = m.ld;
-      h = make({g.rows, g.d}, type, *x.t);
-      g.h = h.data_ptr();
-      g.ldh = g.d > 0 ? g.d : 1;
-    }
-    y = make({g.rows, g.d}, out, *x.t);
-    g.y = y.data_ptr();
-    g.ldy = g.d > 0 ? g.d : 1;
-    rstd = make({g.rows}, ScalarType::Float, *x.t);
-    g.rstd = static_cast<float*>(rstd.data_ptr());
-    if (e4m3) {
-      scale = make({g.rows}, ScalarType::Float, *x.t);
-      g.scale = static_cast<float*>(scale.data_ptr());
     }
     g.eps = static_cast<float>(PyFloat_AS_DOUBLE(a[3]));
     g.dtype = code_of(type);
     g.out_dtype = code_of(out);
-    const mt_status st = g_rms_norm(&g, stream_of(*x.t));
+    at::Tensor h, y, rstd, scale;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      if (r.t) {
+        h = make({g.rows, g.d}, type, *x.t);
+        g.h = h.data_ptr();
+        g.ldh = g.d > 0 ? g.d : 1;
+      }
+      y = make({g.rows, g.d}, out, *x.t);
+      g.y = y.data_ptr();
+      g.ldy = g.d > 0 ? g.d : 1;
+      rstd = make({g.rows}, ScalarType::Float, *x.t);
+      g.rstd = static_cast<float*>(rstd.data_ptr());
+      if (e4m3) {
+        scale = make({g.rows}, ScalarType::Float, *x.t);
+        g.scale = static_cast<float*>(scale.data_ptr());
+      }
+      st = g_rms_norm(&g, stream_of(*x.t));
+    }
     if (st != MT_OK) return refused(st);
     PyObject* hp = a[0];
     if (r.t) hp = wrap(h);
@@ -198,15 +215,21 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       g.dh = m.p;
       g.lddh = m.ld;
     }
-    at::Tensor dx = make({g.rows, g.d}, type, *dy.t), dw;
-    g.dx = dx.data_ptr();
-    g.lddx = g.d > 0 ? g.d : 1;
-    if (flag(a[5])) {
-      dw = make({g.d}, ScalarType::Float, *dy.t);
-      g.dweight = static_cast<float*>(dw.data_ptr());
-    }
     g.dtype = code_of(type);
-    const mt_status st = g_rms_norm_backward(&g, stream_of(*dy.t));
+    const bool need_weight = flag(a[5]);
+    at::Tensor dx, dw;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      dx = make({g.rows, g.d}, type, *dy.t);
+      g.dx = dx.data_ptr();
+      g.lddx = g.d > 0 ? g.d : 1;
+      if (need_weight) {
+        dw = make({g.d}, ScalarType::Float, *dy.t);
+        g.dweight = static_cast<float*>(dw.data_ptr());
+      }
+      st = g_rms_norm_backward(&g, stream_of(*dy.t));
+    }
     if (st != MT_OK) return refused(st);
     return tuple(wrap(dx), wrap(dw));
   });
@@ -258,19 +281,24 @@ PyObject* linear(PyObject*, PyObject* const* o, Py_ssize_t n) {
       g.residual = m.p;
       g.ldr = m.ld;
     }
-    at::Tensor y = make({g.M, g.N}, out, *a.t), z;
-    g.Y = y.data_ptr();
-    g.ldy = g.ldz = g.N > 0 ? g.N : 1;
     const bool preact = flag(o[9]);
-    if (preact) {
-      z = make({g.M, g.N}, out, *a.t);
-      g.Z = z.data_ptr();
-    }
     g.trans_b = trans;
     g.dtype = code_of(type);
     g.out_dtype = code_of(out);
     g.activation = static_cast<int32_t>(PyLong_AsLong(o[3]));
-    const mt_status st = g_linear(&g, stream_of(*a.t));
+    at::Tensor y, z;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      y = make({g.M, g.N}, out, *a.t);
+      g.Y = y.data_ptr();
+      g.ldy = g.ldz = g.N > 0 ? g.N : 1;
+      if (preact) {
+        z = make({g.M, g.N}, out, *a.t);
+        g.Z = z.data_ptr();
+      }
+      st = g_linear(&g, stream_of(*a.t));
+    }
     if (st != MT_OK) return refused(st);
     return preact ? tuple(wrap(y), wrap(z)) : wrap(y);
   });
@@ -315,25 +343,30 @@ PyObject* linear_backward(PyObject*, PyObject* const* o, Py_ssize_t n) {
       g.Z = m.p;
       g.ldz = m.ld;
     }
-    at::Tensor da, db, dbias;
-    if (flag(o[6])) {
-      da = make({g.M, g.K}, type, *dy.t);
-      g.dA = da.data_ptr();
-      g.ldda = g.K > 0 ? g.K : 1;
-    }
-    if (flag(o[7])) {
-      db = make({rows, cols}, db_type, *dy.t);
-      g.dB = db.data_ptr();
-      g.lddb = cols > 0 ? cols : 1;
-    }
-    if (flag(o[8])) {
-      dbias = make({g.N}, ScalarType::Float, *dy.t);
-      g.dbias = static_cast<float*>(dbias.data_ptr());
-    }
     g.trans_b = trans;
     g.dtype = code_of(type);
     g.db_dtype = code_of(db_type);
-    const mt_status st = g_linear_backward(&g, stream_of(*dy.t));
+    const bool need_a = flag(o[6]), need_b = flag(o[7]), need_bias = flag(o[8]);
+    at::Tensor da, db, dbias;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      if (need_a) {
+        da = make({g.M, g.K}, type, *dy.t);
+        g.dA = da.data_ptr();
+        g.ldda = g.K > 0 ? g.K : 1;
+      }
+      if (need_b) {
+        db = make({rows, cols}, db_type, *dy.t);
+        g.dB = db.data_ptr();
+        g.lddb = cols > 0 ? cols : 1;
+      }
+      if (need_bias) {
+        dbias = make({g.N}, ScalarType::Float, *dy.t);
+        g.dbias = static_cast<float*>(dbias.data_ptr());
+      }
+      st = g_linear_backward(&g, stream_of(*dy.t));
+    }
     if (st != MT_OK) return refused(st);
     return tuple(wrap(da), wrap(db), wrap(dbias));
   });
