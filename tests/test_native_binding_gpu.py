@@ -80,3 +80,14 @@ def test_other_threads_run_while_a_call_waits(held, call):
         calls[call]()          # MtError (status 8) when nobody could release it
     finally:
         other.join()
+
+
+def test_output_that_does_not_fit_raises_torchs_error(monkeypatch):
+    """2^41 bytes of output from 32 MB of inputs: the allocation fails, with
+    the exception it has everywhere else in torch, native or not."""
+    a = torch.ones(1 << 20, 8, device="cuda", dtype=torch.bfloat16)
+    for unload in (False, True):
+        if unload:
+            monkeypatch.setattr(layers, "_native", None)
+        with pytest.raises(torch.OutOfMemoryError):
+            mt.linear(a, a, trans_b=True)

@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "mt_layers.h"
@@ -108,13 +109,14 @@ PyObject* wrap(const at::Tensor& t) {
   Py_RETURN_NONE;
 }
 
-// Runs f, turning a C++ exception into a Python one.
+// Runs f, turning a C++ exception into the Python one that torch raises for
+// it (torch.OutOfMemoryError for an allocation that fails).
 template <class F>
 PyObject* guarded(F&& f) {
   try {
     return f();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }
