@@ -6,12 +6,16 @@ Marshalling only, as in the package's ``__init__``, which re-exports
 everything here.  A call that allocates its outputs and runs on the current
 stream of the current device is marshalled natively (csrc/torch_binding.cpp,
 built beside the library): 5.8 us of the host's time for an rms_norm with a
-residual, 16 us here.
+residual, 16 us here.  ``stream`` (a handle; None: the current stream) runs a
+call elsewhere, its outputs in that stream's memory; operands have to stay
+until its work is done.
 """
 from __future__ import annotations
 
 import ctypes
 import struct
+
+from .streams import elsewhere
 
 _I64, _I32, _P, _F = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
 
@@ -235,11 +239,10 @@ def _result(out, name, rows, cols, dtype, device):
     return (out, *_matrix(out, name, rows, cols, dtype, device))
 
 
-def _call(name, packed, device, stream):
-    """Runs one packed C call on the operands' device and stream."""
+def _call(name, packed, device):
+    """Runs one packed C call on the operands' device, on its current stream."""
     index = device.index
-    if stream is None:
-        stream = _raw_stream(index)
+    stream = _raw_stream(index)
     if index == _device_now():
         st = _functions[name](packed, stream)
     else:
@@ -265,7 +268,9 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, out=None, h_out
     and h when given; h_out may be residual or x."""
     if _torch is None:
         _setup()
-    if _native is not None and out is None and h_out is None and stream is None:
+    if stream is not None:
+        return elsewhere(rms_norm, stream, x, weight, residual, eps, out_dtype, out, h_out)
+    if _native is not None and out is None and h_out is None:
         r = _native.rms_norm(x, weight, residual, float(eps), out_dtype)
         if r is not None:
             return _done(r, "mt_rms_norm")
@@ -291,7 +296,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, out=None, h_out
         sp = scale.data_ptr()
     _call("mt_rms_norm",
           _pack_rms_norm(rows, d, xp, ldx, rp, ldr, wp, hp, ldh, yp, ldy, sp, rstd.data_ptr(),
-                         eps, _codes[dt], _codes[out_dtype], wcode), dev, stream)
+                         eps, _codes[dt], _codes[out_dtype], wcode), dev)
     return (y, h, rstd) if scale is None else (y, scale, h, rstd)
 
 
@@ -306,7 +311,9 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, need_weight=True, out=None, 
     given and may be dy or dh."""
     if _torch is None:
         _setup()
-    if _native is not None and out is None and stream is None:
+    if stream is not None:
+        return elsewhere(rms_norm_backward, stream, dy, h, weight, rstd, dh, need_weight, out)
+    if _native is not None and out is None:
         r = _native.rms_norm_backward(dy, h, weight, rstd, dh, bool(need_weight))
         if r is not None:
             return _done(r, "mt_rms_norm_backward")
@@ -325,7 +332,7 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, need_weight=True, out=None, 
         dwp = dweight.data_ptr()
     _call("mt_rms_norm_backward",
           _pack_rms_norm_backward(rows, d, dyp, lddy, hp, ldh, wp, rp, dhp, lddh, dxp, lddx, dwp,
-                                  _codes[dt], wcode), dev, stream)
+                                  _codes[dt], wcode), dev)
     return dx, dweight
 
 
@@ -353,8 +360,11 @@ def linear(a, b, bias=None, activation=None, residual=None, trans_b=False, scale
     dtype when ``preact`` is set."""
     if _torch is None:
         _setup()
+    if stream is not None:
+        return elsewhere(linear, stream, a, b, bias, activation, residual, trans_b, scale_a,
+                         scale_b, out_dtype, out, preact)
     act = _activation(activation)
-    if _native is not None and out is None and stream is None:
+    if _native is not None and out is None:
         r = _native.linear(a, b, bias, act, residual, bool(trans_b), scale_a, scale_b, out_dtype,
                            bool(preact))
         if r is not None:
@@ -395,7 +405,7 @@ def linear(a, b, bias=None, activation=None, residual=None, trans_b=False, scale
     _call("mt_linear",
           _pack_linear(M, N, K, ap, lda, bp, ldb, yp, ldy, zp, ldz, rp, ldr, bias_p, sap, sbp,
                        1 if trans_b else 0, _codes[dt], _codes[out_dtype], act, 0, 0),
-          dev, stream)
+          dev)
     return (y, z) if preact else y
 
 
@@ -411,8 +421,11 @@ def linear_backward(dy, a, b, z=None, activation=None, trans_b=False, need_a=Tru
     float32), dbias is float32."""
     if _torch is None:
         _setup()
+    if stream is not None:
+        return elsewhere(linear_backward, stream, dy, a, b, z, activation, trans_b, need_a, need_b,
+                         need_bias, db_dtype)
     act = _activation(activation)
-    if _native is not None and stream is None:
+    if _native is not None:
         r = _native.linear_backward(dy, a, b, z, act, bool(trans_b), bool(need_a), bool(need_b),
                                     bool(need_bias), db_dtype)
         if r is not None:
@@ -442,5 +455,5 @@ def linear_backward(dy, a, b, z=None, activation=None, trans_b=False, need_a=Tru
     _call("mt_linear_backward",
           _pack_linear_backward(M, N, K, dyp, lddy, zp, ldz, ap, lda, bp, ldb, dap, ldda, dbp,
                                 lddb, dbiasp, 1 if trans_b else 0, _codes[dt],
-                                _codes[db_dtype], act), dev, stream)
+                                _codes[db_dtype], act), dev)
     return da, db, dbias
