@@ -139,3 +139,30 @@ def test_refusals_are_the_same_on_another_stream():
     with pytest.raises(mt.MtError) as e:
         mt.rms_norm(x, None, eps=-1.0, stream=s)
     assert e.value.status == mt.MT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("call", ["sgemm", "gemm", "gemm_mixed"])
+def test_products_take_their_output_from_the_stream_given(call):
+    """The older calls, the same way."""
+    x, r, _, _ = operands()
+    a, b = x.float(), r.float().t().contiguous()
+    bias = torch.ones(256, device="cuda")
+    f = {"sgemm": lambda **k: mt.sgemm(a, b, **k),
+         "gemm": lambda **k: mt.gemm(a, b, alpha=2.0, bias=bias, **k),
+         "gemm_mixed": lambda **k: mt.gemm_mixed(x, r, trans_b=True, **k)}[call]
+    s = torch.cuda.Stream()
+    want = f()
+    f(stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = torch.full((256, 256), 3.0, device="cuda")
+    seen = torch.empty_like(old)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(CYCLES)
+    seen.copy_(old)
+    where = old.data_ptr()
+    del old
+    y = f(stream=s.cuda_stream)
+    assert y.data_ptr() != where
+    torch.cuda.synchronize()
+    assert (seen == 3).all() and torch.equal(y, want)

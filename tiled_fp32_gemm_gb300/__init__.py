@@ -140,6 +140,7 @@ SIGNATURES = {
     "mt_version": (_I, []),
 }
 
+from .streams import elsewhere  # noqa: E402
 from .layers import (ACTIVATIONS, MT_ACT_GELU, MT_ACT_GELU_TANH,  # noqa: E402,F401
                      MT_ACT_NONE, MT_ACT_RELU, MT_ACT_SILU, MT_DTYPE_E4M3, MT_DTYPE_F32,
                      MT_E4M3_MAX, MT_SCALE_MIN, linear, linear_backward, mt_linear, mt_linear_args,
@@ -377,6 +378,8 @@ def _check_tensor(t, name, device=None):
 def sgemm(a, b, out=None, stream=None, **choices):
     """out = a @ b through mt_sgemm_ex on torch tensors (float32, CUDA, row-major)."""
     import torch
+    if stream is not None:
+        return elsewhere(sgemm, stream, a, b, out, **choices)
     _check_tensor(a, "a")
     _check_tensor(b, "b", a.device)
     M, K = a.shape
@@ -389,7 +392,7 @@ def sgemm(a, b, out=None, stream=None, **choices):
         _check_tensor(out, "out", a.device)
         if tuple(out.shape) != (M, N):
             raise ValueError("out has the wrong shape")
-    s = stream if stream is not None else torch.cuda.current_stream(a.device).cuda_stream
+    s = torch.cuda.current_stream(a.device).cuda_stream
     with torch.cuda.device(a.device):
         st = mt_sgemm_ex(a.data_ptr(), b.data_ptr(), out.data_ptr(), M, N, K, s,
                          make_config(**choices) if choices else None)
@@ -417,6 +420,9 @@ def gemm(a, b, c=None, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, stream
     matrix when asked.  Returns c (allocated when not given; then beta must
     be 0)."""
     import torch
+    if stream is not None:
+        return elsewhere(gemm, stream, a, b, c, alpha, beta, trans_a, trans_b, bias=bias,
+                         **choices)
     for t, name in ((a, "a"), (b, "b")):
         if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda:
             raise TypeError(f"{name} must be a float32 CUDA tensor")
@@ -445,7 +451,7 @@ def gemm(a, b, c=None, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, stream
                 not bias.is_contiguous()):
             raise ValueError("bias must be a contiguous float32 CUDA vector of N")
         _check_device(bias, "bias", a.device)
-    s = stream if stream is not None else torch.cuda.current_stream(a.device).cuda_stream
+    s = torch.cuda.current_stream(a.device).cuda_stream
     cfg = make_config(**choices) if choices else None
     with torch.cuda.device(a.device):
         if bias is None:
@@ -477,6 +483,9 @@ def gemm_mixed(a, b, c=None, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, 
     stride), through mt_gemm_mixed_general(_bias).  Returns c (allocated
     when not given; then beta must be 0)."""
     import torch
+    if stream is not None:
+        return elsewhere(gemm_mixed, stream, a, b, c, alpha, beta, trans_a, trans_b, bias=bias,
+                         **choices)
     for t, name in ((a, "a"), (b, "b")):
         _check_device(t, name, a.device if isinstance(a, torch.Tensor) else None)
         if t.dim() != 2 or t.stride(1) != 1:
@@ -507,7 +516,7 @@ def gemm_mixed(a, b, c=None, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, 
                 not bias.is_contiguous()):
             raise ValueError("bias must be a contiguous float32 CUDA vector of N")
         _check_device(bias, "bias", a.device)
-    s = stream if stream is not None else torch.cuda.current_stream(a.device).cuda_stream
+    s = torch.cuda.current_stream(a.device).cuda_stream
     cfg = make_config(**choices) if choices else None
     with torch.cuda.device(a.device):
         if bias is None:
