@@ -7,8 +7,9 @@ Importing this module registers ``torch.ops.mt.sgemm(a, b)``,
 ``sgemm``, ``gemm(..., bias=...)``, ``linear`` and ``rms_norm``, visible to
 torch's dispatcher, graph capture and tracing (each has a shape-only fake
 implementation, so tracing needs no GPU).  ``linear`` and ``rms_norm`` are
-differentiable: their gradients are ``linear_backward`` and
-``rms_norm_backward``.  Marshalling only: the work runs in the library's
+differentiable, once: their gradients are ``linear_backward`` and
+``rms_norm_backward``, which have none themselves, so a second derivative
+raises.  Marshalling only: the work runs in the library's
 kernels.
 """
 from __future__ import annotations
@@ -16,6 +17,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import gemm, linear, linear_backward, rms_norm, rms_norm_backward, sgemm
 
@@ -79,6 +81,7 @@ def _linear_setup(ctx, inputs, output):
     ctx.mark_non_differentiable(output[1])
 
 
+@once_differentiable
 def _linear_grad(ctx, dy, _):
     a, b, z = ctx.saved_tensors
     activation, trans_b = ctx.options
@@ -118,6 +121,7 @@ def _rms_norm_setup(ctx, inputs, output):
     ctx.mark_non_differentiable(rstd)
 
 
+@once_differentiable
 def _rms_norm_grad(ctx, dy, dh, _):
     h, weight, rstd = ctx.saved_tensors
     dx, dweight = rms_norm_backward(
