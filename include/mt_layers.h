@@ -10,10 +10,12 @@
  * to it on the same stream.
  *
  * Matrices are row-major with a row pitch in elements (at least the row's
- * length); rows may be strided, columns are contiguous.  Types are mt_dtype
- * codes.  "16-bit" is MT_DTYPE_F16 or MT_DTYPE_BF16.  All sums, statistics
- * and activations are computed in fp32 and rounded once, to nearest even,
- * when a result is stored.
+ * length); rows may be strided, columns are contiguous.  Matrices overlap when
+ * they share an element: columns side by side in rows of one pitch in bytes do
+ * not; of other pitches the whole spans count.  Types are mt_dtype codes.
+ * "16-bit" is MT_DTYPE_F16 or MT_DTYPE_BF16.  All sums, statistics and
+ * activations are computed in fp32 and rounded once, to nearest even, when a
+ * result is stored.
  */
 #ifndef MT_LAYERS_H
 #define MT_LAYERS_H

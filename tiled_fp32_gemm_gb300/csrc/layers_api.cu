@@ -48,7 +48,17 @@ struct View {
     return p && (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(elem - 1)) == 0;
   }
   bool same(const View& o) const { return p == o.p && ld == o.ld && elem == o.elem; }
-  bool hits(const View& o) const { return overlaps(p, bytes(), o.p, o.bytes()); }
+  // Whether the views share a byte.  Columns of one wider buffer (the same
+  // pitch) may lie side by side in spans that overlap; other pitches are
+  // judged by their spans.
+  bool hits(const View& o) const {
+    if (!overlaps(p, bytes(), o.p, o.bytes())) return false;
+    const int64_t pitch = ld * elem;
+    if (rows < 2 || o.rows < 2 || o.ld * o.elem != pitch) return true;
+    const int64_t apart = static_cast<const char*>(o.p) - static_cast<const char*>(p);
+    const int64_t first = (apart % pitch + pitch) % pitch;  // o's column 0 in a row of this
+    return first < cols * elem || first + o.cols * o.elem > pitch;
+  }
 };
 
 // Scratch from the device's pool for one call; freed on the call's stream.
