@@ -57,3 +57,16 @@ def test_norms_refuse_rows_whose_columns_pass_32_bits(d):
 def test_the_longest_row_is_taken():
     assert LONGEST - 1 + 512 == 2 ** 31 - 1 and LONGEST + 31 < 2 ** 31
     assert answers(LONGEST) == [mt.MT_ERR_NO_DEVICE] * 3
+
+
+def test_plans_for_few_sms_launch_something():
+    """A pair of CTAs wants two SMs; with one the tiles go to single CTAs."""
+    for sms in (1, 2, 3, 7):
+        for M in (1, 129, 256, 4096):
+            a = mt.mt_linear_args(M=M, N=4096, K=512, lda=512, ldb=4096, ldy=4096,
+                                  dtype=mt.MT_DTYPE_BF16, out_dtype=mt.MT_DTYPE_BF16)
+            st, p = mt.mt_linear_plan(a, sms)
+            assert st == mt.MT_OK and p.grid >= 1
+            tiles = -(-M // p.bm) * -(-4096 // p.bn)
+            assert p.grid == (2 * min(tiles, sms // 2) if p.bn == 256 else tiles * p.split_k)
+            assert p.bn == 128 or sms >= 2

@@ -184,7 +184,8 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
   // split kernel): 512 tokens (32 pairs) 32.0 / 28.0, 768 (48) 33.1 / 38.5,
   // 1024 (64) 33.2 / 39.0, 2048 (128) 55.1 / 74.7; e4m3 512 tokens 23.9 / 21.5,
   // 768 25.2 / 27.1, 2048 38.8 / 52.4.
-  p.pair = a.K > 0 && 7 * pairs >= 2 * sms && a.T > 128 && pairs <= INT32_MAX / 8;
+  p.pair = a.K > 0 && sms >= 2 && 7 * pairs >= 2 * sms && a.T > 128 &&
+           pairs <= INT32_MAX / 8;
   if (p.pair) {
     const LinearKernel k = linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn);
     p.threads = kPairThreads;
