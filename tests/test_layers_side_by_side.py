@@ -62,17 +62,22 @@ def test_results_beside_their_operands(d, gap):
     buf = torch.randn(rows, 4 * n, generator=g, device="cuda").half()
     x, r, y, h = (buf[:, i * n:i * n + d] for i in range(4))
     w = torch.randn(d, generator=g, device="cuda")
-    want = mt.rms_norm(x.clone(), w, residual=r.clone())
+
+    def apart(t):
+        """The same view (pitch and alignment) in a copy of the buffer."""
+        return torch.as_strided(buf.clone(), t.shape, t.stride(), t.storage_offset())
+
+    want = mt.rms_norm(apart(x), w, residual=apart(r), out=apart(y), h_out=apart(h))
     kept = buf.clone()
     got = mt.rms_norm(x, w, residual=r, out=y, h_out=h)
     assert got[0] is y and got[1] is h
     for i in range(3):
         assert torch.equal(got[i], want[i])
-    dx = mt.rms_norm_backward(x, h, w, got[2], dh=r, out=y)[0]
-    assert torch.equal(dx, mt.rms_norm_backward(x.clone(), h.clone(), w, got[2], dh=r.clone())[0])
+    want = mt.rms_norm_backward(apart(x), apart(h), w, got[2], dh=apart(r), out=apart(y))[0]
+    assert torch.equal(mt.rms_norm_backward(x, h, w, got[2], dh=r, out=y)[0], want)
     b = torch.randn(d, d, generator=g, device="cuda").half()
-    out = mt.linear(x, b, residual=r, activation="silu", out=h)
-    assert torch.equal(out, mt.linear(x.clone(), b, residual=r.clone(), activation="silu"))
+    want = mt.linear(apart(x), b, residual=apart(r), activation="silu", out=apart(h))
+    assert torch.equal(mt.linear(x, b, residual=r, activation="silu", out=h), want)
     # Nothing outside the outputs was written.
     for i, t in enumerate((x, r)):
         assert torch.equal(t, kept[:, i * n:i * n + d])
