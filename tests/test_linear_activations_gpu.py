@@ -5,10 +5,11 @@ rounding hides the activation's own: each result has to be right to its own
 digits, in the tails too, where gelu and silu fall towards zero.
 
 Tolerances (u = 2^-24), of the result:
-* fp32: normcdff is good to 5 ulp (10 u), expf to 2 (4 u); with at most three
-  more roundings, 16 u.  The tanh form's logistic takes exp of v = 2 u(z), good
-  to 4.5 u of itself: 5 |v| u more.  What is below the type's normal range has
-  an absolute grid: 2^-126.
+* fp32: gelu's fit is within 1.7 u, its argument and evaluation within 6 u,
+  expf within 2 ulp (4 u), and four more roundings: 16 u.  silu's expf, sum,
+  reciprocal (1 ulp) and products: 11 u.  The tanh form's logistic takes exp of
+  v = 2 u(z), good to 4.5 u of itself: 5 |v| u more.  What is below the type's
+  normal range has an absolute grid: 2^-126.
 * 16-bit: 2^-15, and the result's own rounding.  The exponentials flush to
   zero what is below 2^-110; fp16 rounds on a grid of 2^-24 at the bottom.
 """

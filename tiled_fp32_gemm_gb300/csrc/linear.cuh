@@ -27,28 +27,39 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// 1 / (1 + exp(-z)), for 16-bit results.  exp overflows to infinity for z
-// below -88, which gives the 0 that is wanted.
+// The functions below have two forms.  F32 false, for 16-bit results and the
+// derivatives: the special-function unit's exponential, whose argument's
+// rounding costs up to 2^-15 of a result far out in a tail, an eighth of half
+// a step of fp16.  F32 true, for fp32 results: CUDA's expf and arguments that
+// keep their digits.  (With normcdff and divisions there instead, 4096^3 with
+// fp32 results and gelu took 115 us, and 98 with the F32 false form.)
+
+// 1 / (1 + exp(-z)).
+template <bool F32>
 __device__ __forceinline__ float logistic(float z) {
-  return rcp_approx(1.0f + exp_approx(-z));
-}
-// The same for fp32 results: no overflow, and the digits of CUDA's expf and
-// division.
-__device__ __forceinline__ float logistic_f32(float z) {
-  const float e = expf(-fabsf(z));
-  return (z < 0.0f ? e : 1.0f) / (1.0f + e);
+  if constexpr (F32) {
+    const float e = expf(-fabsf(z));  // never overflows
+    return (z < 0.0f ? e : 1.0f) * rcp_approx(1.0f + e);
+  } else {
+    // exp overflows to infinity for z below -88, which gives the 0 that is
+    // wanted.
+    return rcp_approx(1.0f + exp_approx(-z));
+  }
 }
 
-// The normal distribution's Phi(z) and *bell = exp(-z^2 / 2), for 16-bit
-// results and the derivative.  With x = |z| / sqrt 2, Phi(-|z|) is bell *
-// erfcx(x) / 2, erfcx(x) = exp(x^2) erfc(x).  That falls from 1 to 1 / (x
-// sqrt pi) without ever being small, so a polynomial in t = 1 / (1 + 0.43 x)
-// without constant term holds it to a *relative* error, which is what keeps
-// the tail's digits: these eight coefficients are a minimax fit (Lawson's
-// reweighted least squares) over 0 <= x <= 10, within 1.0e-7, 4.5e-7 as
-// evaluated here.  No branches: every lane of a warp takes the same path.
+// The normal distribution's Phi(z) and *bell = exp(-z^2 / 2).  With x = |z| /
+// sqrt 2, Phi(-|z|) is bell * erfcx(x) / 2, erfcx(x) = exp(x^2) erfc(x).  That
+// falls from 1 to 1 / (x sqrt pi) without ever being small, so a polynomial in
+// t = 1 / (1 + 0.43 x) without constant term holds it to a *relative* error,
+// which is what keeps the tail's digits: these eight coefficients are a
+// minimax fit (Lawson's reweighted least squares) over 0 <= x <= 10, within
+// 1.0e-7, 4.5e-7 as evaluated here.  No branches: every lane of a warp takes
+// the same path.
+template <bool F32>
 __device__ __forceinline__ float normal_cdf(float z, float* bell) {
-  const float x = fabsf(z) * 0.70710678118654752f;
+  // Past 15 the tail is 0 in fp32; the clamp keeps infinity out of z^2.
+  const float y = F32 ? fminf(fabsf(z), 15.0f) : fabsf(z);
+  const float x = y * 0.70710678118654752f;
   const float t = rcp_approx(fmaf(0.43f, x, 1.0f));
   float p = fmaf(0.0731455436f, t, -0.308094499f);
   p = fmaf(p, t, 0.379885357f);
@@ -57,27 +68,30 @@ __device__ __forceinline__ float normal_cdf(float z, float* bell) {
   p = fmaf(p, t, 0.205472764f);
   p = fmaf(p, t, 0.244293791f);
   p = fmaf(p, t, 0.242519823f);
-  *bell = exp_approx(-x * x);
+  if constexpr (F32) {
+    // exp(-(s + d) / 2) with s + d = y^2, d what s lost in rounding.
+    const float s = y * y, d = fmaf(y, y, -s);
+    *bell = expf(-0.5f * s);
+    *bell = fmaf(-0.5f * d, *bell, *bell);
+  } else {
+    *bell = exp_approx(-x * x);
+  }
   const float tail = 0.5f * p * t * *bell;  // Phi(-|z|)
   return z > 0.0f ? 1.0f - tail : tail;
 }
 
 // The activations, in fp32.  (1 + tanh u) / 2 is the logistic function of 2u.
-// 16-bit results (F32 false) take the special-function unit's exponential,
-// whose argument's rounding costs up to 2^-15 of a result far out in a tail,
-// an eighth of half a step of fp16; fp32 results take CUDA's functions.
 template <int ACT, bool F32>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == ACT_RELU) {
     return z < 0.0f ? 0.0f : z;  // a NaN stays one
   } else if constexpr (ACT == ACT_GELU) {
     float bell;
-    return z * (F32 ? normcdff(z) : normal_cdf(z, &bell));
+    return z * normal_cdf<F32>(z, &bell);
   } else if constexpr (ACT == ACT_GELU_TANH) {
-    const float u = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
-    return z * (F32 ? logistic_f32(u) : logistic(u));
+    return z * logistic<F32>(1.5957691216057308f * fmaf(0.044715f * z * z, z, z));
   } else if constexpr (ACT == ACT_SILU) {
-    return z * (F32 ? logistic_f32(z) : logistic(z));
+    return z * logistic<F32>(z);
   } else {
     return z;
   }
@@ -91,15 +105,15 @@ __device__ __forceinline__ float activate_grad(float z) {
     return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
   } else if constexpr (ACT == ACT_GELU) {
     float bell;
-    const float cdf = normal_cdf(z, &bell);
+    const float cdf = normal_cdf<false>(z, &bell);
     return fmaf(z * 0.39894228040143268f, bell, cdf);  // Phi(z) + z * phi(z)
   } else if constexpr (ACT == ACT_GELU_TANH) {
     const float x = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;
-    const float p = logistic(1.5957691216057308f * fmaf(0.044715f * x * x, x, x));
+    const float p = logistic<false>(1.5957691216057308f * fmaf(0.044715f * x * x, x, x));
     return fmaf(p * (1.0f - p) * x, 1.5957691216057308f * fmaf(0.134145f * x, x, 1.0f), p);
   } else if constexpr (ACT == ACT_SILU) {
     const float x = z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z;
-    const float p = logistic(x);
+    const float p = logistic<false>(x);
     return p * fmaf(x, 1.0f - p, 1.0f);
   } else {
     return 1.0f;
