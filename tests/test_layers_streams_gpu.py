@@ -22,7 +22,7 @@ def library():
 def operands():
     g = torch.Generator(device="cuda").manual_seed(4)
     draw = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
-    return draw(256, 1024), draw(256, 1024), draw(512, 1024), torch.rand(256, device="cuda")
+    return draw(256, 1024), draw(256, 1024), draw(512, 1024), torch.rand(256, generator=g, device="cuda")
 
 
 def calls(stream):
