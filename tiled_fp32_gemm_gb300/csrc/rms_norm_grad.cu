@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(MOST + 32, 1)
              (m * g.groups + group) * a.d;
     };
     // First sweep of the group's n-th row: its dweight and, for every warp of
-    // the group, the sum of dy * weight * h.
+    // the group, the sum of dy * weight * xhat.
     auto first_sweep = [&](int n, bool live, float r) {
       tc::wait_phase(full(n % g.stages), (n / g.stages) & 1u, wc);
       const T *dy = values(n, 0), *h = values(n, 1);
@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(MOST + 32, 1)
         w.get(i, vw);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          dw[i][k] = fmaf(vy[k] * r, vh[k], dw[i][k]);
-          dot = fmaf(vy[k] * vw[k], vh[k], dot);
+          const float xhat = vh[k] * r;
+          dw[i][k] = fmaf(vy[k], xhat, dw[i][k]);
+          dot = fmaf(vy[k] * vw[k], xhat, dot);
         }
       }
       dot = warp_sum(dot);
@@ -182,9 +183,11 @@ __global__ void __launch_bounds__(MOST + 32, 1)
     for (int64_t row0 = row_0; row0 < a.rows; row0 += step, ++n) {
       const int64_t row = row0 + group;
       const bool live = row < a.rows;  // the whole group
-      // dx = r * g - r^3 * mean(g * h) * h + dh
+      // dx = r * (g - back * h) + dh, back = r * mean(g * xhat): with r factored
+      // in once more (r * g - r * back * h), r * back would pass fp32's range
+      // for rows of values near 1e-19 or 1e19, whose gradient does not.
       const float dot = warp_sum(lane < warps ? sums[n & 1][first_warp + lane] : 0.0f);
-      const float back = r * r * (r * (dot / static_cast<float>(a.d)));
+      const float back = r * (dot / static_cast<float>(a.d));
       // The next row's first sweep runs beside this row's second.
       const float r_after = rstd_of(row + 2 * step);
       if (row0 + step < a.rows) first_sweep(n + 1, row + step < a.rows, r_next);
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(MOST + 32, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float grad = vy[k] * vw[k];
-          dx[k] = fmaf(r, grad, DH ? fmaf(-back, vh[k], dx[k]) : -back * vh[k]);
+          dx[k] = fmaf(r, fmaf(-back, vh[k], grad), DH ? dx[k] : 0.0f);
         }
         store_step<T, true>(o.dx, row, c, dx);
       }
