@@ -112,6 +112,12 @@ typedef struct {
     float *dweight;
     int32_t dtype;        /* dy, h, dh, dx: MT_DTYPE_F16, _BF16 or _F32 */
     int32_t weight_dtype; /* dtype or MT_DTYPE_F32 */
+    int32_t fault_inject; /* test hook, 0 = off: 1 = the copies that rows starting
+                             on 16 bytes arrive by are not issued, so the waits
+                             on them run out, dx and dweight hold nothing of
+                             use and mt_check_device_status returns
+                             MT_ERR_TIMEOUT */
+    int32_t reserved;     /* 0 */
 } mt_rms_norm_backward_args;
 
 /* dx may be dy or dh itself (same pointer and pitch); any other overlap of an

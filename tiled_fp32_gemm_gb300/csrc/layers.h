@@ -66,6 +66,7 @@ struct RmsNormGradArgs {
   int dtype;
   int weight_f32;
   BoundsRecord* bounds;
+  int fault_inject;
 };
 
 // Scratch bytes of a call, and the call (workspace of that many bytes).

@@ -192,6 +192,7 @@ mt_status mt_rms_norm_backward(const mt_rms_norm_backward_args* g, cudaStream_t 
   if (!g || g->rows < 0 || g->d < 0 || g->d > kMaxRow || g->rows > INT32_MAX)
     return MT_ERR_INVALID_ARG;
   if (!half_type(g->dtype) && g->dtype != MT_DTYPE_F32) return MT_ERR_INVALID_ARG;
+  if (g->reserved || g->fault_inject < 0 || g->fault_inject > 1) return MT_ERR_INVALID_ARG;
   if (g->weight && g->weight_dtype != g->dtype && g->weight_dtype != MT_DTYPE_F32)
     return MT_ERR_INVALID_ARG;
   const int e = mt::dtype_bytes(g->dtype);
@@ -215,7 +216,8 @@ mt_status mt_rms_norm_backward(const mt_rms_norm_backward_args* g, cudaStream_t 
   if (st != MT_OK) return st;
   const mt::RmsNormGradArgs a{rows, static_cast<int>(d), g->dy, g->lddy, g->h, g->ldh, g->weight,
                               g->rstd, g->dh, g->lddh, g->dx, g->lddx, g->dweight, g->dtype,
-                              g->weight_dtype == MT_DTYPE_F32 ? 1 : 0, bounds_record()};
+                              g->weight_dtype == MT_DTYPE_F32 ? 1 : 0, bounds_record(),
+                              g->fault_inject};
   Scratch ws(stream);
   st = ws.get(dev, mt::rms_norm_grad_workspace(a, info.sms));
   if (st != MT_OK) return st;

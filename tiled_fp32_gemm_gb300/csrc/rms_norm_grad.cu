@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(MOST + 32, 1)
   const int tid = static_cast<int>(threadIdx.x) % g.threads;
   int issued = 0;
   if (warp == worker_warps) {
-    for (int64_t row0 = row_0; row0 < a.rows; row0 += step, ++issued) {
+    for (int64_t row0 = row_0; row0 < a.rows && !a.fault_inject; row0 += step, ++issued) {
       const int s = issued % g.stages, round = issued / g.stages;
       if (issued >= g.stages &&
           !__all_sync(0xffffffffu, tc::wait_phase(empty(s), (round + 1) & 1u, wc)))

@@ -40,7 +40,7 @@ class mt_rms_norm_backward_args(ctypes.Structure):
     _fields_ = [("rows", _I64), ("d", _I64), ("dy", _P), ("lddy", _I64), ("h", _P),
                 ("ldh", _I64), ("weight", _P), ("rstd", _P), ("dh", _P), ("lddh", _I64),
                 ("dx", _P), ("lddx", _I64), ("dweight", _P), ("dtype", _I32),
-                ("weight_dtype", _I32)]
+                ("weight_dtype", _I32), ("fault_inject", _I32), ("reserved", _I32)]
 
 
 class mt_linear_args(ctypes.Structure):
@@ -332,7 +332,7 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, need_weight=True, out=None, 
         dwp = dweight.data_ptr()
     _call("mt_rms_norm_backward",
           _pack_rms_norm_backward(rows, d, dyp, lddy, hp, ldh, wp, rp, dhp, lddh, dxp, lddx, dwp,
-                                  _codes[dt], wcode), dev)
+                                  _codes[dt], wcode, 0, 0), dev)
     return dx, dweight
 
 
