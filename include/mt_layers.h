@@ -41,13 +41,18 @@ extern "C" {
  *
  * A row whose mean square is 0 with eps 0 gets r = 0: its y is zeros, and the
  * gradient below leaves it dh alone.  h is summed in fp32 and enters the norm
- * unrounded.  Written: h in x's type
- * (h NULL: not written), r to `rstd` (rows floats; NULL: not written; the
- * gradient reads it), and y either in x's type (out_dtype == dtype) or in 8
- * bits with one scale per row (out_dtype == MT_DTYPE_E4M3):
+ * unrounded.  Written: h in x's type (h NULL: not written), r to `rstd` (rows
+ * floats; NULL: not written; the gradient reads it), and y either in x's type
+ * (out_dtype == dtype) or in 8 bits with one scale per row (out_dtype ==
+ * MT_DTYPE_E4M3):
  *
  *     scale[i] = max(max_k |y[i][k]| / 448, 2^-126)
  *     y8[i][k] = e4m3(y[i][k] / scale[i])           (nearest even)
+ *
+ * with the maximum as max_k |h * weight| * r and the quotient as y * (1 /
+ * scale), all in fp32: within 4 ulp before its rounding, so a value that near
+ * the middle between two e4m3 values may become either (h * weight has to fit
+ * fp32, as y has).
  *
  * A NaN in a row makes the whole row, its r and its scale NaN; a mean square
  * past fp32's range (values past 1.8e19) makes r and a finite y 0; an infinite

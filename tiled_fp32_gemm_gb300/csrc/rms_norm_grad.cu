@@ -42,12 +42,15 @@ constexpr int kBarrierBytes = 256;
 
 // Rows of up to 16384 values, in one of three forms: 16 values a thread and
 // 608 threads (96 registers each, which leave nothing to spill); the same
-// with 800 threads (72 registers) where they hold two rows and 608 would hold
-// one, or where 608 would not hold a row; 32 values and 512 threads past
-// that.  false when two stages do not fit.  Measured on GB300 (bf16 with dh,
-// share of the measured copy bandwidth): 2048 and 4096 values 0.90 to 0.93,
-// 8192 0.92, 7168 (one group of 448 threads) 0.85, 5120 in the 608 form 0.57
-// and in the 800 form 0.77, 12288 0.54, 16384 0.45.
+// with 800 threads (72 registers, up to 36 bytes of spill stores a thread for
+// 16-bit rows, 64 for fp32) where they hold two rows and 608 would hold one,
+// or where 608 would not hold a row; 32 values and 512 threads past that (96
+// registers: with the copy warp they are 17 warps; up to 128 bytes of spill
+// stores, 208 for fp32).  false when two stages do not fit.  Measured on GB300
+// (bf16 with dh, share of the measured copy bandwidth): 2048 values 0.98, 4096
+// 0.94, 8192 0.93, 7168 (one group of 448 threads) 0.85, 5120 in the 608 form
+// 0.57 and in the 800 form 0.76, 12288 0.58, 16384 0.51; fp32, 8192 values
+// 0.80.
 bool staging_of(int d, int elem, bool dh, Staging* s) {
   if (d > 16384) return false;
   s->e = d <= 16 * 800 ? 16 : 32;
@@ -76,7 +79,7 @@ bool staging_of(int d, int elem, bool dh, Staging* s) {
 // barrier a row is all that is waited for.  dx may be dy or dh: a row's copies
 // have landed before it is written.  Waits are bounded; after one that ran out
 // (recorded in the status word) the results are unspecified.  Measured on
-// GB300, 16384 x 8192 bf16 with dh: 174 us, 6.2 TB/s (209 us with the rows in
+// GB300, 16384 x 8192 bf16 with dh: 170 us, 6.3 TB/s (209 us with the rows in
 // registers and loads one row ahead).
 template <class T, class W, int E, int MOST, int DH>
 __global__ void __launch_bounds__(MOST + 32, 1)
@@ -257,7 +260,8 @@ constexpr int ctas_per_sm(int threads) { return kSmThreads > threads ? kSmThread
 // A row held in the registers of THREADS threads, E values each; rows
 // strided over the grid.  Up to 512 threads the next row's values are loaded
 // before this row's reduction, so a barrier leaves loads in flight; 1024 have
-// no registers for that (with them, 8000 x 8191 took 309 us, without 137).
+// no registers for that (with them, 8000 x 8191 fp16 with dh took 309 us,
+// without 135 to 139: 0.56 of the copy rate, two bytes an access).
 // Each thread reads its values of a row before it writes them, so dx may be
 // dy or dh.
 template <class T, class W, int THREADS, int E, bool DH>
@@ -353,7 +357,8 @@ __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS),
 }
 
 // dx of a row too wide for registers, on one CTA: one sweep for the mean, one
-// for dx, each element read and then written by the same thread.
+// for dx, each element read and then written by the same thread.  2048 x 40000
+// bf16 with dh and dweight: 506 us, 0.19 of the copy rate.
 constexpr int kWideThreads = 512;
 
 template <class T, class W>

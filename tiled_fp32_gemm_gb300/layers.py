@@ -5,7 +5,7 @@ entry points under their own names taking a filled argument structure.
 Marshalling only, as in the package's ``__init__``, which re-exports
 everything here.  A call that allocates its outputs and runs on the current
 stream of the current device is marshalled natively (csrc/torch_binding.cpp,
-built beside the library): 5.8 us of the host's time for an rms_norm with a
+built beside the library): 6 us of the host's time for an rms_norm with a
 residual, 16 us here.  ``stream`` (a handle; None: the current stream) runs a
 call elsewhere, its outputs in that stream's memory; operands have to stay
 until its work is done.
