@@ -97,16 +97,18 @@ __device__ __forceinline__ float activate(float z) {
   }
 }
 
-// Their derivatives.  Past the clamps the logistic forms' derivatives are 0
-// or 1 to fp32; the clamps keep 0 * infinity out of them (a NaN passes).
+// Their derivatives.  Past the clamps they are 0 or 1 to fp32; the clamps keep
+// 0 * infinity out of them (a pre-activation past its 16-bit type is stored as
+// infinity; a NaN passes).
 template <int ACT>
 __device__ __forceinline__ float activate_grad(float z) {
   if constexpr (ACT == ACT_RELU) {
     return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
   } else if constexpr (ACT == ACT_GELU) {
     float bell;
-    const float cdf = normal_cdf<false>(z, &bell);
-    return fmaf(z * 0.39894228040143268f, bell, cdf);  // Phi(z) + z * phi(z)
+    const float x = z > 15.0f ? 15.0f : z < -15.0f ? -15.0f : z;
+    const float cdf = normal_cdf<false>(x, &bell);
+    return fmaf(x * 0.39894228040143268f, bell, cdf);  // Phi(z) + z * phi(z)
   } else if constexpr (ACT == ACT_GELU_TANH) {
     const float x = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;
     const float p = logistic<false>(1.5957691216057308f * fmaf(0.044715f * x * x, x, x));
