@@ -166,3 +166,25 @@ def test_products_take_their_output_from_the_stream_given(call):
     assert y.data_ptr() != where
     torch.cuda.synchronize()
     assert (seen == 3).all() and torch.equal(y, want)
+
+
+def test_products_into_a_given_output_run_on_the_stream_given():
+    """Nothing to allocate: straight to the stream, as always."""
+    x, r, _, _ = operands()
+    a, b = x.float(), r.float().t().contiguous()
+    c = torch.zeros(256, 256, device="cuda")
+    calls = [lambda s: mt.sgemm(a, b, out=c, stream=s), lambda s: mt.gemm(a, b, c, stream=s),
+             lambda s: mt.gemm_mixed(x, r, c, trans_b=True, stream=s)]
+    for f in calls:
+        want = f(None).clone()
+        c.zero_()
+        s, done = torch.cuda.Stream(), torch.cuda.Event()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(CYCLES)
+        assert f(s.cuda_stream) is c
+        done.record(s)
+        torch.cuda.current_stream().synchronize()
+        assert not done.query()
+        s.synchronize()
+        assert torch.equal(c, want)

@@ -378,8 +378,8 @@ def _check_tensor(t, name, device=None):
 def sgemm(a, b, out=None, stream=None, **choices):
     """out = a @ b through mt_sgemm_ex on torch tensors (float32, CUDA, row-major)."""
     import torch
-    if stream is not None:
-        return elsewhere(sgemm, stream, a, b, out, **choices)
+    if stream is not None and out is None:
+        return elsewhere(sgemm, stream, a, b, **choices)
     _check_tensor(a, "a")
     _check_tensor(b, "b", a.device)
     M, K = a.shape
@@ -392,7 +392,7 @@ def sgemm(a, b, out=None, stream=None, **choices):
         _check_tensor(out, "out", a.device)
         if tuple(out.shape) != (M, N):
             raise ValueError("out has the wrong shape")
-    s = torch.cuda.current_stream(a.device).cuda_stream
+    s = stream if stream is not None else torch.cuda.current_stream(a.device).cuda_stream
     with torch.cuda.device(a.device):
         st = mt_sgemm_ex(a.data_ptr(), b.data_ptr(), out.data_ptr(), M, N, K, s,
                          make_config(**choices) if choices else None)
@@ -420,7 +420,7 @@ def gemm(a, b, c=None, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, stream
     matrix when asked.  Returns c (allocated when not given; then beta must
     be 0)."""
     import torch
-    if stream is not None:
+    if stream is not None and c is None:
         return elsewhere(gemm, stream, a, b, c, alpha, beta, trans_a, trans_b, bias=bias,
                          **choices)
     for t, name in ((a, "a"), (b, "b")):
@@ -451,7 +451,7 @@ def gemm(a, b, c=None, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, stream
                 not bias.is_contiguous()):
             raise ValueError("bias must be a contiguous float32 CUDA vector of N")
         _check_device(bias, "bias", a.device)
-    s = torch.cuda.current_stream(a.device).cuda_stream
+    s = stream if stream is not None else torch.cuda.current_stream(a.device).cuda_stream
     cfg = make_config(**choices) if choices else None
     with torch.cuda.device(a.device):
         if bias is None:
@@ -483,7 +483,7 @@ def gemm_mixed(a, b, c=None, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, 
     stride), through mt_gemm_mixed_general(_bias).  Returns c (allocated
     when not given; then beta must be 0)."""
     import torch
-    if stream is not None:
+    if stream is not None and c is None:
         return elsewhere(gemm_mixed, stream, a, b, c, alpha, beta, trans_a, trans_b, bias=bias,
                          **choices)
     for t, name in ((a, "a"), (b, "b")):
@@ -516,7 +516,7 @@ def gemm_mixed(a, b, c=None, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, 
                 not bias.is_contiguous()):
             raise ValueError("bias must be a contiguous float32 CUDA vector of N")
         _check_device(bias, "bias", a.device)
-    s = torch.cuda.current_stream(a.device).cuda_stream
+    s = stream if stream is not None else torch.cuda.current_stream(a.device).cuda_stream
     cfg = make_config(**choices) if choices else None
     with torch.cuda.device(a.device):
         if bias is None:

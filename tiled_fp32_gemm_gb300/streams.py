@@ -1,5 +1,6 @@
 """Calls on a stream that is not torch's current one (the ``stream`` argument
-of the torch calls: a stream's handle, as ``torch.cuda.Stream.cuda_stream``)."""
+of the torch calls: a stream's handle, as ``torch.cuda.Stream.cuda_stream``)
+that allocate their outputs."""
 from __future__ import annotations
 
 
