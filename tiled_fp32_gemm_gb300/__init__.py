@@ -149,7 +149,16 @@ from .layers import (ACTIVATIONS, MT_ACT_GELU, MT_ACT_GELU_TANH,  # noqa: E402,F
                      mt_rms_norm_backward_args, rms_norm, rms_norm_backward)
 from .layers import SIGNATURES as _LAYER_SIGNATURES  # noqa: E402
 
+from .model import (dropout, layer_norm, layer_norm_backward,  # noqa: E402,F401
+                    linear_cross_entropy, linear_cross_entropy_backward, mt_dropout,
+                    mt_dropout_args, mt_layer_norm, mt_layer_norm_args, mt_layer_norm_backward,
+                    mt_layer_norm_backward_args, mt_linear_cross_entropy,
+                    mt_linear_cross_entropy_args, mt_linear_cross_entropy_backward,
+                    mt_linear_cross_entropy_backward_args)
+from .model import SIGNATURES as _MODEL_SIGNATURES  # noqa: E402
+
 SIGNATURES.update(_LAYER_SIGNATURES)
+SIGNATURES.update(_MODEL_SIGNATURES)
 
 _lock = threading.Lock()
 _lib = None

@@ -15,6 +15,7 @@
 #include "host.h"
 #include "kernels.h"
 #include "layers.h"
+#include "model.h"
 #include "mt_sgemm.h"
 #include "smem_layout.cuh"
 
@@ -1525,15 +1526,16 @@ mt_status mt_check_device_status(cudaStream_t stream) {
     cudaGetLastError();
     return MT_ERR_CUDA;
   }
-  unsigned int flags = 0, flags16 = 0, flags_linear = 0, flags_norm = 0;
+  unsigned int flags = 0, flags16 = 0, flags_linear = 0, flags_norm = 0, flags_layer = 0;
   if (mt::tf32x3_read_and_clear_status(&flags) != cudaSuccess ||
       mt::f16tc_read_and_clear_status(&flags16) != cudaSuccess ||
       mt::linear_read_and_clear_status(&flags_linear) != cudaSuccess ||
-      mt::rms_norm_grad_read_and_clear_status(&flags_norm) != cudaSuccess) {
+      mt::rms_norm_grad_read_and_clear_status(&flags_norm) != cudaSuccess ||
+      mt::layer_norm_grad_read_and_clear_status(&flags_layer) != cudaSuccess) {
     cudaGetLastError();
     return MT_ERR_CUDA;
   }
-  flags |= flags16 | flags_linear | flags_norm;
+  flags |= flags16 | flags_linear | flags_norm | flags_layer;
   return flags ? MT_ERR_TIMEOUT : MT_OK;
 }
 

@@ -1,0 +1,267 @@
+// Layer norm with dropout and the residual's addition.
+//
+//   h = D(x) + residual,  m = mean h,  r = 1 / sqrt(mean (h - m)^2 + eps),
+//   y = (h - m) * r * weight + bias
+//
+// The operator is bound by memory: every element of x, residual, h and y moves
+// once, and h stays in registers between the statistics and y.  The variance
+// is the mean square of differences, in one sweep and one barrier: a warp sums
+// its values, takes their differences from its own mean, and the warps' pairs
+// (sum, squares about their mean) are joined by
+//   squares = sum_w (squares_w + n_w * (mean_w - m)^2)
+// (Chan, Golub and LeVeque, "Updating formulae and a pairwise algorithm for
+// computing sample variances", 1979).
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "model.h"
+#include "philox.cuh"
+#include "row_util.cuh"
+
+namespace mt {
+namespace {
+
+using namespace row;
+
+template <class T>
+struct Operands {
+  Matrix<const T> x, residual;
+  Matrix<T> h, y;
+  Matrix<float> mean, rstd;
+};
+
+struct Stats {
+  float mean, rstd;
+};
+
+__device__ __forceinline__ Stats stats_of(float mean, float squares, int d, float eps) {
+  const float v = (d > 0 ? squares / static_cast<float>(d) : 0.0f) + eps;
+  return Stats{mean, v == 0.0f ? 0.0f : rsqrtf(v)};  // a constant row stays one without an eps
+}
+
+// A warp's part of a row: how many values, their mean, their squares about it.
+struct Part {
+  float n, mean, squares;
+};
+
+// The row's mean and squares from the parts of the warps that share it, in
+// every thread.  One barrier.
+template <int THREADS>
+__device__ __forceinline__ Part join(const Part& mine, int d) {
+  if constexpr (THREADS == 32) {
+    return mine;
+  } else {
+    constexpr int WARPS = THREADS / 32;
+    __shared__ Part parts[WARPS];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (lane == 0) parts[warp] = mine;
+    __syncthreads();
+    const Part p = lane < WARPS ? parts[lane] : Part{0.0f, 0.0f, 0.0f};
+    const float mean = d > 0 ? warp_sum(p.n * p.mean) / static_cast<float>(d) : 0.0f;
+    const float off = p.mean - mean;
+    return Part{static_cast<float>(d), mean,
+                warp_sum(p.n > 0.0f ? fmaf(p.n * off, off, p.squares) : 0.0f)};
+  }
+}
+
+// A row held in the registers of THREADS threads, E values each: read once,
+// reduced once, written.  Each thread reads its values before it writes
+// them, so h may be x or residual and y may be x.
+template <class T, class W, bool DROP, int THREADS, int E, bool VEC>
+__global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS))
+    layer_norm_kernel(const LayerNormArgs a, const Operands<T> o, const Matrix<const W> weight,
+                      const Matrix<const W> bias) {
+  using S = Slots<E, VEC>;
+  grid_launch_dependents();
+  grid_wait();
+  const int tid = threadIdx.x % THREADS;
+  const int64_t row =
+      static_cast<int64_t>(blockIdx.x) * rows_per_cta(THREADS) + threadIdx.x / THREADS;
+  if (row >= a.rows) return;  // a whole warp
+  Held<T, E, VEC> x, res;
+  x.load(o.x, row, a.d, tid, THREADS);
+  if (a.residual) res.load(o.residual, row, a.d, tid, THREADS);
+  float h[S::COUNT][S::STEP];
+#pragma unroll
+  for (int i = 0; i < S::COUNT; ++i) x.get(i, h[i]);
+  if constexpr (DROP) {
+    Dropout drop;
+    drop.init(a.dropout);
+    const uint32_t r = static_cast<uint32_t>(row);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < S::COUNT; ++i) drop.apply8(r, S::col(i, tid, THREADS), h[i]);
+    } else {
+      uint32_t words[S::COUNT];
+      drop.words_of_columns(r, tid, THREADS, words);
+#pragma unroll
+      for (int i = 0; i < S::COUNT; ++i) h[i][0] = drop.apply(h[i][0], words[i]);
+    }
+  }
+  float sum = 0.0f;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < S::COUNT; ++i) {
+    if (S::col(i, tid, THREADS) >= a.d) break;
+    count += S::STEP;
+    if (a.residual) {
+      float v[S::STEP];
+      res.get(i, v);
+#pragma unroll
+      for (int k = 0; k < S::STEP; ++k) h[i][k] += v[k];
+    }
+#pragma unroll
+    for (int k = 0; k < S::STEP; ++k) sum += h[i][k];
+  }
+  Part part;
+  part.n = static_cast<float>(__reduce_add_sync(0xffffffffu, count));
+  part.mean = part.n > 0.0f ? warp_sum(sum) / part.n : 0.0f;
+  part.squares = 0.0f;
+#pragma unroll
+  for (int i = 0; i < S::COUNT; ++i) {
+    if (S::col(i, tid, THREADS) >= a.d) break;
+#pragma unroll
+    for (int k = 0; k < S::STEP; ++k) {
+      const float c = h[i][k] - part.mean;
+      part.squares = fmaf(c, c, part.squares);
+    }
+  }
+  part.squares = warp_sum(part.squares);
+  // Read while the row's statistics meet.
+  Held<W, E, VEC> w, b;
+  if (a.weight) w.load(weight, 0, a.d, tid, THREADS);
+  if (a.bias) b.load(bias, 0, a.d, tid, THREADS);
+  part = join<THREADS>(part, a.d);
+  const Stats s = stats_of(part.mean, part.squares, a.d, a.eps);
+  if (tid == 0) {
+    if (a.mean) o.mean.store(row, 0, s.mean);
+    if (a.rstd) o.rstd.store(row, 0, s.rstd);
+  }
+#pragma unroll
+  for (int i = 0; i < S::COUNT; ++i) {
+    const int c = S::col(i, tid, THREADS);
+    if (c >= a.d) break;
+    if (a.h) store_step<T, VEC>(o.h, row, c, h[i]);
+    float vw[S::STEP], vb[S::STEP];
+    if (a.weight) w.get(i, vw);
+    if (a.bias) b.get(i, vb);
+#pragma unroll
+    for (int k = 0; k < S::STEP; ++k) {
+      const float v = (h[i][k] - s.mean) * s.rstd;
+      h[i][k] = a.bias ? fmaf(v, a.weight ? vw[k] : 1.0f, vb[k]) : a.weight ? v * vw[k] : v;
+    }
+    store_step<T, VEC>(o.y, row, c, h[i]);
+  }
+}
+
+// A row too wide for registers, on one CTA: one sweep for the mean, one for
+// the squares about it, one for the outputs, which read x and the residual
+// again (from L2).  Each element is read and then written by the same thread,
+// in the last sweep only, so h may be x or residual.
+constexpr int kWideThreads = 512;
+
+__device__ __forceinline__ float wide_sum(float v, float (&part)[kWideThreads / 32]) {
+  v = warp_sum(v);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+  __syncthreads();
+  return warp_sum(threadIdx.x % 32 < kWideThreads / 32 ? part[threadIdx.x % 32] : 0.0f);
+}
+
+template <class T, class W, bool DROP>
+__global__ void __launch_bounds__(kWideThreads)
+    layer_norm_wide_kernel(const LayerNormArgs a, const Operands<T> o,
+                           const Matrix<const W> weight, const Matrix<const W> bias) {
+  __shared__ float sums[kWideThreads / 32], squares[kWideThreads / 32];
+  grid_launch_dependents();
+  grid_wait();
+  const int64_t row = blockIdx.x;
+  Dropout drop{};
+  if (DROP) drop.init(a.dropout);
+  // Calls f(column, h) for this thread's columns.  A warp's lanes go together
+  // as long as one of them has a column: they share their random words.
+  auto sweep = [&](auto&& f) {
+    constexpr int N = 4;
+    for (int c0 = threadIdx.x; c0 - static_cast<int>(threadIdx.x % 32) < a.d;
+         c0 += N * kWideThreads) {
+      uint32_t words[N];
+      if (DROP) drop.words_of_columns(static_cast<uint32_t>(row), c0, kWideThreads, words);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = c0 + i * kWideThreads;
+        if (c >= a.d) break;
+        float h = o.x.load(row, c);
+        if (DROP) h = drop.apply(h, words[i]);
+        f(c, h + (a.residual ? o.residual.load(row, c) : 0.0f));
+      }
+      __syncwarp();
+    }
+  };
+  float t = 0.0f;
+  sweep([&](int, float h) { t += h; });
+  const float mean = wide_sum(t, sums) / static_cast<float>(a.d);
+  t = 0.0f;
+  sweep([&](int, float h) { t = fmaf(h - mean, h - mean, t); });
+  const Stats s = stats_of(mean, wide_sum(t, squares), a.d, a.eps);
+  if (threadIdx.x == 0) {
+    if (a.mean) o.mean.store(row, 0, s.mean);
+    if (a.rstd) o.rstd.store(row, 0, s.rstd);
+  }
+  sweep([&](int c, float h) {
+    if (a.h) o.h.store(row, c, h);
+    const float v = (h - s.mean) * s.rstd;
+    o.y.store(row, c, fmaf(v, a.weight ? weight.load(0, c) : 1.0f,
+                           a.bias ? bias.load(0, c) : 0.0f));
+  });
+}
+
+template <class T, class W, bool DROP>
+cudaError_t launch(const LayerNormArgs& a, cudaStream_t stream) {
+  const int64_t n = a.rows;
+  const Operands<T> o{
+      {static_cast<const T*>(a.x), a.ldx, view_extent(n, a.d, a.ldx), a.bounds},
+      {static_cast<const T*>(a.residual), a.ldr, view_extent(n, a.d, a.ldr), a.bounds},
+      {static_cast<T*>(a.h), a.ldh, view_extent(n, a.d, a.ldh), a.bounds},
+      {static_cast<T*>(a.y), a.ldy, view_extent(n, a.d, a.ldy), a.bounds},
+      {a.mean, 1, n, a.bounds},
+      {a.rstd, 1, n, a.bounds}};
+  const Matrix<const W> weight{static_cast<const W*>(a.weight), 0, a.d, a.bounds};
+  const Matrix<const W> bias{static_cast<const W*>(a.bias), 0, a.d, a.bounds};
+  const int e = sizeof(T);
+  const bool vec = a.d % 8 == 0 && rows_aligned(a.x, a.ldx, e) &&
+                   rows_aligned(a.residual, a.residual ? a.ldr : 0, e) &&
+                   rows_aligned(a.h, a.h ? a.ldh : 0, e) && rows_aligned(a.y, a.ldy, e) &&
+                   rows_aligned(a.weight, 0, sizeof(W)) && rows_aligned(a.bias, 0, sizeof(W));
+  cudaError_t err = cudaSuccess;
+  const bool held = row_layout<16>(a.d, [&](auto threads, auto values) {
+    constexpr int THREADS = decltype(threads)::value, E = decltype(values)::value;
+    constexpr int ROWS = rows_per_cta(THREADS);
+    err = launch_dependent(vec ? layer_norm_kernel<T, W, DROP, THREADS, E, true>
+                               : layer_norm_kernel<T, W, DROP, THREADS, E, false>,
+                           static_cast<unsigned>((n + ROWS - 1) / ROWS), THREADS * ROWS, stream,
+                           a, o, weight, bias);
+  });
+  if (!held)
+    err = launch_dependent(layer_norm_wide_kernel<T, W, DROP>, static_cast<unsigned>(n),
+                           kWideThreads, stream, a, o, weight, bias);
+  return err;
+}
+
+template <class T>
+cudaError_t launch_drop(const LayerNormArgs& a, cudaStream_t stream) {
+  if (a.weight_f32)
+    return a.drop ? launch<T, float, true>(a, stream) : launch<T, float, false>(a, stream);
+  return a.drop ? launch<T, T, true>(a, stream) : launch<T, T, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t stream) {
+  switch (a.dtype) {
+    case DT_F16: return launch_drop<__half>(a, stream);
+    case DT_BF16: return launch_drop<__nv_bfloat16>(a, stream);
+    default: return launch_drop<float>(a, stream);
+  }
+}
+
+}  // namespace mt

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "head.cuh"
 #include "layers.h"
 #include "linear.cuh"
 #include "tcgen05.cuh"
@@ -259,7 +260,7 @@ cudaError_t linear_prepare() {
     for (int mn = 0; mn < 4; ++mn)
       if (r == cudaSuccess) r = prepare(linear_pair_kernel_for(dtype, mn & 1, mn >> 1));
   }
-  return r;
+  return r == cudaSuccess ? head_prepare() : r;
 }
 
 namespace {
@@ -307,19 +308,21 @@ cudaError_t launch_copies(CopyJobs* jobs, cudaStream_t stream) {
                           kCopyThreads, stream, *jobs);
 }
 
-SplitProblem problem_of(const LinearArgs& a, const LinearPlan& p, const Ready& r, int first_cta) {
-  return SplitProblem{r.map_w, r.map_x, r.ep, r.idesc, static_cast<int>(ktiles_of(a)),
-                      static_cast<int>(split_tiles(a, p.bt)),
-                      static_cast<int>(ceil_div(a.T, p.bt)), first_cta, p.split, a.w_mn,
-                      a.x_mn};
+template <class Ep>
+SplitProblemOf<Ep> problem_of(const LinearArgs& a, const LinearPlan& p, const Ready& r,
+                              const Ep& ep, int first_cta) {
+  return SplitProblemOf<Ep>{r.map_w, r.map_x, ep, r.idesc, static_cast<int>(ktiles_of(a)),
+                            static_cast<int>(split_tiles(a, p.bt)),
+                            static_cast<int>(ceil_div(a.T, p.bt)), first_cta, p.split, a.w_mn,
+                            a.x_mn};
 }
 
-cudaError_t launch_split(const LinearPlan& p, int dtype, int64_t grid, SplitProblems* problems,
-                         int fault_inject, cudaStream_t stream) {
+template <class Ep>
+cudaError_t launch_split(const LinearPlan& p, const LinearKernel& k, int64_t grid,
+                         SplitProblemsOf<Ep>* problems, int fault_inject, cudaStream_t stream) {
   void* args[] = {problems, &fault_inject};
-  return launch_dependent(linear_split_kernel_for(dtype, p.bt).kernel,
-                          dim3(static_cast<unsigned>(grid)), kThreads, p.smem_bytes, p.cluster,
-                          stream, args);
+  return launch_dependent(k.kernel, dim3(static_cast<unsigned>(grid)), kThreads, p.smem_bytes,
+                          p.cluster, stream, args);
 }
 
 }  // namespace
@@ -336,10 +339,38 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* worksp
                               r.idesc, r.ep, static_cast<int>(ktiles_of(a)),
                               static_cast<int>(p.grid / 2), fault_inject, stream);
   SplitProblems problems{};
-  problems.p[0] = problem_of(a, p, r, 0);
+  problems.p[0] = problem_of(a, p, r, r.ep, 0);
   problems.p[1].first_cta = INT32_MAX;
-  return launch_split(p, a.dtype, p.grid, &problems, fault_inject, stream);
+  return launch_split(p, linear_split_kernel_for(a.dtype, p.bt), p.grid, &problems, fault_inject,
+                      stream);
 }
+
+template <class Ep>
+cudaError_t launch_head(const LinearArgs& a, const LinearPlan& p, void* workspace, const Ep& ep,
+                        cudaStream_t stream, int fault_inject) {
+  Ready r{};
+  CopyJobs jobs{};
+  cudaError_t e = make_ready(a, p, workspace, &jobs, &r);
+  if (e == cudaSuccess) e = launch_copies(&jobs, stream);
+  if (e != cudaSuccess) return e;
+  if (p.pair) {
+    // The tokens are the MMA's M side here.
+    const uint32_t fmt = a.dtype == DT_BF16 ? 1u : 0u;
+    const uint32_t idesc = tc::instr_desc(kPair, kPair, fmt, fmt, 0u, a.w_mn ? 1u : 0u);
+    return launch_head_pair(r.map_x, r.map_w, idesc, ep, a.w_mn != 0,
+                            static_cast<int>(p.smem_bytes), static_cast<int>(ktiles_of(a)),
+                            static_cast<int>(p.grid / 2), fault_inject, stream);
+  }
+  SplitProblemsOf<Ep> problems{};
+  problems.p[0] = problem_of(a, p, r, ep, 0);
+  problems.p[1].first_cta = INT32_MAX;
+  return launch_split(p, head_split_kernel_for<Ep>(p.bt), p.grid, &problems, fault_inject,
+                      stream);
+}
+template cudaError_t launch_head(const LinearArgs&, const LinearPlan&, void*,
+                                 const head::HeadStats&, cudaStream_t, int);
+template cudaError_t launch_head(const LinearArgs&, const LinearPlan&, void*,
+                                 const head::HeadGrad&, cudaStream_t, int);
 
 cudaError_t launch_linear_two(const LinearArgs& a, const LinearPlan& pa, void* wa,
                               const LinearArgs& b, const LinearPlan& pb, void* wb,
@@ -359,20 +390,23 @@ cudaError_t launch_linear_two(const LinearArgs& a, const LinearPlan& pa, void* w
   SplitProblems problems{};
   // The longer contraction's CTAs start first.
   if (ktiles_of(a) >= ktiles_of(b)) {
-    problems.p[0] = problem_of(a, pa, ra, 0);
-    problems.p[1] = problem_of(b, pb, rb, static_cast<int>(pa.grid));
+    problems.p[0] = problem_of(a, pa, ra, ra.ep, 0);
+    problems.p[1] = problem_of(b, pb, rb, rb.ep, static_cast<int>(pa.grid));
   } else {
-    problems.p[0] = problem_of(b, pb, rb, 0);
-    problems.p[1] = problem_of(a, pa, ra, static_cast<int>(pb.grid));
+    problems.p[0] = problem_of(b, pb, rb, rb.ep, 0);
+    problems.p[1] = problem_of(a, pa, ra, ra.ep, static_cast<int>(pb.grid));
   }
-  return launch_split(pa, a.dtype, pa.grid + pb.grid, &problems, 0, stream);
+  return launch_split(pa, linear_split_kernel_for(a.dtype, pa.bt), pa.grid + pb.grid, &problems,
+                      0, stream);
 }
 
 cudaError_t linear_read_and_clear_status(unsigned int* status) {
-  unsigned int split = 0, pair = 0;
+  unsigned int split = 0, pair = 0, head_split = 0, head_pair = 0;
   cudaError_t e = linear_split_read_and_clear_status(&split);
   if (e == cudaSuccess) e = linear_pair_read_and_clear_status(&pair);
-  *status = split | pair;
+  if (e == cudaSuccess) e = head_split_read_and_clear_status(&head_split);
+  if (e == cudaSuccess) e = head_pair_read_and_clear_status(&head_pair);
+  *status = split | pair | head_split | head_pair;
   return e;
 }
 

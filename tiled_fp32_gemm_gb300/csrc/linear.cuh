@@ -279,18 +279,23 @@ struct LinearKernel {
 
 constexpr int LINEAR_BC = 128;  // columns of Y per tile of the split kernels
 
-// One product of a split-kernel launch: its CTAs are first_cta and on.
-struct SplitProblem {
+// One product of a split-kernel launch: its CTAs are first_cta and on.  Ep:
+// what finish() does with its sums.
+template <class Ep>
+struct SplitProblemOf {
   CUtensorMap map_w, map_x;
-  LinearEpilogue ep;
+  Ep ep;
   uint32_t idesc;
   int ktiles, tiles, tiles_t, first_cta;
   int split;  // CTAs that share a tile: the launch's cluster, or 1
   int w_mn, x_mn;
 };
-struct SplitProblems {
-  SplitProblem p[2];
+template <class Ep>
+struct SplitProblemsOf {
+  SplitProblemOf<Ep> p[2];
 };
+using SplitProblem = SplitProblemOf<LinearEpilogue>;
+using SplitProblems = SplitProblemsOf<LinearEpilogue>;
 
 }  // namespace linear
 

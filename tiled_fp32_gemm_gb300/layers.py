@@ -72,7 +72,7 @@ SIGNATURES = {
 def _packer(cls):
     """struct.Struct.pack with the layout of a ctypes structure: one call
     fills every field (None is not taken: NULL is 0)."""
-    code = {_I64: "q", _I32: "i", _P: "Q", _F: "f"}
+    code = {_I64: "q", _I32: "i", _P: "Q", _F: "f", ctypes.c_uint64: "Q", ctypes.c_double: "d"}
     s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_))
     assert s.size == ctypes.sizeof(cls)
     return s.pack
