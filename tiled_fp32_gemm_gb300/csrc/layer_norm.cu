@@ -17,7 +17,7 @@
 
 #include "model.h"
 #include "philox.cuh"
-#include "row_util.cuh"
+#include "row_chunk.cuh"
 
 namespace mt {
 namespace {
@@ -65,73 +65,80 @@ __device__ __forceinline__ Part join(const Part& mine, int d) {
   }
 }
 
-// A row held in the registers of THREADS threads, E values each: read once,
-// reduced once, written.  Each thread reads its values before it writes
-// them, so h may be x or residual and y may be x.
-template <class T, class W, bool DROP, int THREADS, int E, bool VEC>
+// A row held in the registers of THREADS threads, E values each in chunks of
+// eight: read once, reduced once, written.  Each thread reads its values before
+// it writes them, so h may be x or residual and y may be x.
+template <class T, class W, bool DROP, int THREADS, int E, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS))
     layer_norm_kernel(const LayerNormArgs a, const Operands<T> o, const Matrix<const W> weight,
                       const Matrix<const W> bias) {
-  using S = Slots<E, VEC>;
+  using C = Chunks<T, E, ALIGNED, THREADS>;
+  using At = Chunk<ALIGNED, THREADS>;
   grid_launch_dependents();
   grid_wait();
   const int tid = threadIdx.x % THREADS;
   const int64_t row =
       static_cast<int64_t>(blockIdx.x) * rows_per_cta(THREADS) + threadIdx.x / THREADS;
   if (row >= a.rows) return;  // a whole warp
-  Held<T, E, VEC> x, res;
-  x.load(o.x, row, a.d, tid, THREADS);
-  if (a.residual) res.load(o.residual, row, a.d, tid, THREADS);
-  float h[S::COUNT][S::STEP];
+  C x, res;
+  x.load(o.x, row, a.d, tid);
+  if (a.residual) res.load(o.residual, row, a.d, tid);
+  float h[C::COUNT][8];
 #pragma unroll
-  for (int i = 0; i < S::COUNT; ++i) x.get(i, h[i]);
+  for (int i = 0; i < C::COUNT; ++i) x.get(i, h[i]);
   if constexpr (DROP) {
     Dropout drop;
     drop.init(a.dropout);
-    const uint32_t r = static_cast<uint32_t>(row);
-    if constexpr (VEC) {
+    const Dropout::Row of_row = drop.row(static_cast<uint32_t>(row));
 #pragma unroll
-      for (int i = 0; i < S::COUNT; ++i) drop.apply8(r, S::col(i, tid, THREADS), h[i]);
-    } else {
-      uint32_t words[S::COUNT];
-      drop.words_of_columns(r, tid, THREADS, words);
-#pragma unroll
-      for (int i = 0; i < S::COUNT; ++i) h[i][0] = drop.apply(h[i][0], words[i]);
+    for (int i = 0; i < C::COUNT; ++i) {
+      const At at(i, tid);
+      at.drop(drop, of_row, at.words(drop), h[i]);
     }
   }
+  // Columns at or past d are zeros, which the sum does not feel.
   float sum = 0.0f;
   int count = 0;
 #pragma unroll
-  for (int i = 0; i < S::COUNT; ++i) {
-    if (S::col(i, tid, THREADS) >= a.d) break;
-    count += S::STEP;
+  for (int i = 0; i < C::COUNT; ++i) {
+    const At at(i, tid);
     if (a.residual) {
-      float v[S::STEP];
+      float v[8];
       res.get(i, v);
 #pragma unroll
-      for (int k = 0; k < S::STEP; ++k) h[i][k] += v[k];
+      for (int k = 0; k < 8; ++k) h[i][k] += v[k];
     }
 #pragma unroll
-    for (int k = 0; k < S::STEP; ++k) sum += h[i][k];
+    for (int k = 0; k < 8; ++k) sum += h[i][k];
+    count += at.count(a.d);
   }
   Part part;
   part.n = static_cast<float>(__reduce_add_sync(0xffffffffu, count));
   part.mean = part.n > 0.0f ? warp_sum(sum) / part.n : 0.0f;
   part.squares = 0.0f;
 #pragma unroll
-  for (int i = 0; i < S::COUNT; ++i) {
-    if (S::col(i, tid, THREADS) >= a.d) break;
+  for (int i = 0; i < C::COUNT; ++i) {
+    const At at(i, tid);
+    if (at.whole(a.d)) {
 #pragma unroll
-    for (int k = 0; k < S::STEP; ++k) {
-      const float c = h[i][k] - part.mean;
-      part.squares = fmaf(c, c, part.squares);
+      for (int k = 0; k < 8; ++k) {
+        const float c = h[i][k] - part.mean;
+        part.squares = fmaf(c, c, part.squares);
+      }
+    } else if (!ALIGNED) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float c = at.live(k, a.d) ? h[i][k] - part.mean : 0.0f;
+        part.squares = fmaf(c, c, part.squares);
+      }
     }
   }
+  __syncwarp();
   part.squares = warp_sum(part.squares);
   // Read while the row's statistics meet.
-  Held<W, E, VEC> w, b;
-  if (a.weight) w.load(weight, 0, a.d, tid, THREADS);
-  if (a.bias) b.load(bias, 0, a.d, tid, THREADS);
+  Chunks<W, E, ALIGNED, THREADS> w, b;
+  if (a.weight) w.load(weight, 0, a.d, tid);
+  if (a.bias) b.load(bias, 0, a.d, tid);
   part = join<THREADS>(part, a.d);
   const Stats s = stats_of(part.mean, part.squares, a.d, a.eps);
   if (tid == 0) {
@@ -139,26 +146,26 @@ __global__ void __launch_bounds__(THREADS* rows_per_cta(THREADS))
     if (a.rstd) o.rstd.store(row, 0, s.rstd);
   }
 #pragma unroll
-  for (int i = 0; i < S::COUNT; ++i) {
-    const int c = S::col(i, tid, THREADS);
-    if (c >= a.d) break;
-    if (a.h) store_step<T, VEC>(o.h, row, c, h[i]);
-    float vw[S::STEP], vb[S::STEP];
+  for (int i = 0; i < C::COUNT; ++i) {
+    const At at(i, tid);
+    if (!at.any(a.d)) break;
+    if (a.h) at.store(o.h, row, a.d, h[i]);
+    float vw[8], vb[8];
     if (a.weight) w.get(i, vw);
     if (a.bias) b.get(i, vb);
 #pragma unroll
-    for (int k = 0; k < S::STEP; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const float v = (h[i][k] - s.mean) * s.rstd;
       h[i][k] = a.bias ? fmaf(v, a.weight ? vw[k] : 1.0f, vb[k]) : a.weight ? v * vw[k] : v;
     }
-    store_step<T, VEC>(o.y, row, c, h[i]);
+    at.store(o.y, row, a.d, h[i]);
   }
 }
 
 // A row too wide for registers, on one CTA: one sweep for the mean, one for
 // the squares about it, one for the outputs, which read x and the residual
 // again (from L2).  Each element is read and then written by the same thread,
-// in the last sweep only, so h may be x or residual.
+// in the last sweep only, so h may be x or residual and y may be x.
 constexpr int kWideThreads = 512;
 
 __device__ __forceinline__ float wide_sum(float v, float (&part)[kWideThreads / 32]) {
@@ -168,50 +175,69 @@ __device__ __forceinline__ float wide_sum(float v, float (&part)[kWideThreads / 
   return warp_sum(threadIdx.x % 32 < kWideThreads / 32 ? part[threadIdx.x % 32] : 0.0f);
 }
 
-template <class T, class W, bool DROP>
+template <class T, class W, bool DROP, bool ALIGNED>
 __global__ void __launch_bounds__(kWideThreads)
     layer_norm_wide_kernel(const LayerNormArgs a, const Operands<T> o,
                            const Matrix<const W> weight, const Matrix<const W> bias) {
+  using At = Chunk<ALIGNED, kWideThreads>;
   __shared__ float sums[kWideThreads / 32], squares[kWideThreads / 32];
   grid_launch_dependents();
   grid_wait();
   const int64_t row = blockIdx.x;
   Dropout drop{};
-  if (DROP) drop.init(a.dropout);
-  // Calls f(column, h) for this thread's columns.  A warp's lanes go together
-  // as long as one of them has a column: they share their random words.
+  Dropout::Row of_row{};
+  if (DROP) {
+    drop.init(a.dropout);
+    of_row = drop.row(static_cast<uint32_t>(row));
+  }
+  // Calls f(chunk, h) for this thread's chunks, all warps as many times.
   auto sweep = [&](auto&& f) {
-    constexpr int N = 4;
-    for (int c0 = threadIdx.x; c0 - static_cast<int>(threadIdx.x % 32) < a.d;
-         c0 += N * kWideThreads) {
-      uint32_t words[N];
-      if (DROP) drop.words_of_columns(static_cast<uint32_t>(row), c0, kWideThreads, words);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = c0 + i * kWideThreads;
-        if (c >= a.d) break;
-        float h = o.x.load(row, c);
-        if (DROP) h = drop.apply(h, words[i]);
-        f(c, h + (a.residual ? o.residual.load(row, c) : 0.0f));
-      }
+    for (int i = 0; i * 8 * kWideThreads < a.d; ++i) {
+      const At at(i, threadIdx.x);
+      const auto x = at.load(o.x, row, a.d);
+      Eight<T, ALIGNED> r{};
+      if (a.residual) r = at.load(o.residual, row, a.d);
+      float h[8], v[8];
+      x.get(h);
+      r.get(v);
       __syncwarp();
+      if (DROP) at.drop(drop, of_row, at.words(drop), h);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] += v[k];
+      f(at, h);
     }
   };
   float t = 0.0f;
-  sweep([&](int, float h) { t += h; });
+  sweep([&](const At&, const float(&h)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t += h[k];
+  });
   const float mean = wide_sum(t, sums) / static_cast<float>(a.d);
   t = 0.0f;
-  sweep([&](int, float h) { t = fmaf(h - mean, h - mean, t); });
+  sweep([&](const At& at, const float(&h)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float v = at.live(k, a.d) ? h[k] - mean : 0.0f;
+      t = fmaf(v, v, t);
+    }
+  });
   const Stats s = stats_of(mean, wide_sum(t, squares), a.d, a.eps);
   if (threadIdx.x == 0) {
     if (a.mean) o.mean.store(row, 0, s.mean);
     if (a.rstd) o.rstd.store(row, 0, s.rstd);
   }
-  sweep([&](int c, float h) {
-    if (a.h) o.h.store(row, c, h);
-    const float v = (h - s.mean) * s.rstd;
-    o.y.store(row, c, fmaf(v, a.weight ? weight.load(0, c) : 1.0f,
-                           a.bias ? bias.load(0, c) : 0.0f));
+  sweep([&](const At& at, float(&h)[8]) {
+    if (a.h) at.store(o.h, row, a.d, h);
+    Eight<W, ALIGNED> w{}, b{};
+    if (a.weight) w = at.load(weight, 0, a.d);
+    if (a.bias) b = at.load(bias, 0, a.d);
+    float vw[8], vb[8];
+    w.get(vw);
+    b.get(vb);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      h[k] = fmaf((h[k] - s.mean) * s.rstd, a.weight ? vw[k] : 1.0f, vb[k]);
+    at.store(o.y, row, a.d, h);
   });
 }
 
@@ -228,7 +254,7 @@ cudaError_t launch(const LayerNormArgs& a, cudaStream_t stream) {
   const Matrix<const W> weight{static_cast<const W*>(a.weight), 0, a.d, a.bounds};
   const Matrix<const W> bias{static_cast<const W*>(a.bias), 0, a.d, a.bounds};
   const int e = sizeof(T);
-  const bool vec = a.d % 8 == 0 && rows_aligned(a.x, a.ldx, e) &&
+  const bool aligned = a.d % 8 == 0 && rows_aligned(a.x, a.ldx, e) &&
                    rows_aligned(a.residual, a.residual ? a.ldr : 0, e) &&
                    rows_aligned(a.h, a.h ? a.ldh : 0, e) && rows_aligned(a.y, a.ldy, e) &&
                    rows_aligned(a.weight, 0, sizeof(W)) && rows_aligned(a.bias, 0, sizeof(W));
@@ -236,14 +262,15 @@ cudaError_t launch(const LayerNormArgs& a, cudaStream_t stream) {
   const bool held = row_layout<16>(a.d, [&](auto threads, auto values) {
     constexpr int THREADS = decltype(threads)::value, E = decltype(values)::value;
     constexpr int ROWS = rows_per_cta(THREADS);
-    err = launch_dependent(vec ? layer_norm_kernel<T, W, DROP, THREADS, E, true>
-                               : layer_norm_kernel<T, W, DROP, THREADS, E, false>,
+    err = launch_dependent(aligned ? layer_norm_kernel<T, W, DROP, THREADS, E, true>
+                                   : layer_norm_kernel<T, W, DROP, THREADS, E, false>,
                            static_cast<unsigned>((n + ROWS - 1) / ROWS), THREADS * ROWS, stream,
                            a, o, weight, bias);
   });
   if (!held)
-    err = launch_dependent(layer_norm_wide_kernel<T, W, DROP>, static_cast<unsigned>(n),
-                           kWideThreads, stream, a, o, weight, bias);
+    err = launch_dependent(aligned ? layer_norm_wide_kernel<T, W, DROP, true>
+                                   : layer_norm_wide_kernel<T, W, DROP, false>,
+                           static_cast<unsigned>(n), kWideThreads, stream, a, o, weight, bias);
   return err;
 }
 

@@ -17,8 +17,8 @@ namespace {
 using namespace mt::host;
 
 // Longest row of a norm or of dropout: the kernels step a 32-bit column by up
-// to 2048 past the row's last one.
-constexpr int64_t kMaxWidth = INT32_MAX - 4095;
+// to 4096 past the row's last strip of 256.
+constexpr int64_t kMaxWidth = INT32_MAX - 8191;
 
 bool float_type(int t) { return half_type(t) || t == MT_DTYPE_F32; }
 bool sizes_ok(int64_t rows, int64_t d) {

@@ -4,11 +4,13 @@
 // key and counter alone, so the mask of any element is computed where it is
 // needed, forwards and backwards, and is never stored.
 //
-// Cost: 20 wide products, 40 three-input logic operations and the key's
-// additions (the same for every thread) for four words.  Beside 4 to 10 bytes
-// an element of memory traffic that is the smaller part of a pass as long as
-// every word is used, so threads that hold single columns share the blocks
-// (words_of_columns).
+// Cost: the wide products, which the multiplier takes at a quarter of an
+// addition's rate, 20 for four words.  Of the first three rounds' six, two
+// depend on the seed and the sequence, or on the row, alone and three on the
+// block of columns alone, so a thread that keeps its columns from row to row
+// (Columns) computes 15.  With the logic operations, comparisons and
+// conversions eight values are some 140 instructions: less than 4 bytes an
+// element take to move, so what surrounds them decides.
 #pragma once
 
 #include <cstdint>
@@ -28,8 +30,13 @@ struct DropoutArgs {
 namespace row {
 
 struct Dropout {
+  static constexpr int LATE = 7;  // rounds after the third
   uint32_t k0, k1, s0, s1, border;
   float scale;
+  uint32_t a_[LATE], b_[LATE];  // their keys
+
+  static constexpr uint32_t M0 = 0xD2511F53u, M1 = 0xCD9E8D57u;
+  static constexpr uint32_t W0 = 0x9E3779B9u, W1 = 0xBB67AE85u;
 
   __device__ __forceinline__ void init(const DropoutArgs& a) {
     const uint64_t key = static_cast<uint64_t>(*a.seed);
@@ -39,21 +46,59 @@ struct Dropout {
     s1 = a.sequence_hi;
     border = a.border;
     scale = a.scale;
+#pragma unroll
+    for (uint32_t i = 0; i < LATE; ++i) {
+      a_[i] = k0 + (i + 3) * W0;
+      b_[i] = k1 + (i + 3) * W1;
+      // Opaque, so that they stay in registers: the compiler would rather add
+      // them up again for every block, 14 of 137 instructions for eight words.
+      asm("" : "+r"(a_[i]), "+r"(b_[i]));
+    }
   }
 
-  // The four words of columns 4 * block .. 4 * block + 3 of a row.
-  __device__ __forceinline__ void words(uint32_t row, uint32_t block, uint32_t (&w)[4]) const {
-    uint32_t c0 = block, c1 = row, c2 = s0, c3 = s1, a = k0, b = k1;
+  static __device__ __forceinline__ uint32_t hi(uint64_t v) {
+    return static_cast<uint32_t>(v >> 32);
+  }
+  static __device__ __forceinline__ uint32_t lo(uint64_t v) { return static_cast<uint32_t>(v); }
+  static __device__ __forceinline__ uint64_t wide(uint32_t m, uint32_t v) {
+    return static_cast<uint64_t>(m) * v;
+  }
+
+  // A round takes (c0, c1, c2, c3) to (hi(M1 c2) ^ c1 ^ a, lo(M1 c2), hi(M0 c0) ^
+  // c3 ^ b, lo(M0 c0)), a and b the round's keys.  From (block, row, s0, s1):
+  //   after one    (hi(M1 s0) ^ row ^ a0, lo(M1 s0), hi(M0 block) ^ s1 ^ b0, lo(M0 block)):
+  //                the first of the row alone, the last two of the block alone;
+  //   after two    (of the block, of the block, hi of the row ^ of the block, of the row),
+  // and the third round's M0 product is of the block alone again.
+
+  // What a row adds: the words of its product of the second round.
+  struct Row {
+    uint32_t h, l;
+  };
+  __device__ __forceinline__ Row row(uint32_t row) const {
+    const uint64_t p = wide(M0, hi(wide(M1, s0)) ^ row ^ k0);
+    return Row{hi(p), lo(p)};
+  }
+  // What a block of four columns adds.
+  struct Columns {
+    uint32_t c1, c2, h, l;
+  };
+  __device__ __forceinline__ Columns columns(uint32_t block) const {
+    const uint64_t p0 = wide(M0, block), p1 = wide(M1, hi(p0) ^ s1 ^ k1);
+    const uint64_t q = wide(M0, hi(p1) ^ lo(wide(M1, s0)) ^ (k0 + W0));
+    return Columns{lo(p1) ^ (k0 + 2 * W0), lo(p0) ^ (k1 + W1), hi(q) ^ (k1 + 2 * W1), lo(q)};
+  }
+  // The block's four words in the row: the rest of round three, and seven more.
+  __device__ __forceinline__ void words(const Row& r, const Columns& c, uint32_t (&w)[4]) const {
+    const uint64_t p = wide(M1, r.h ^ c.c2);
+    uint32_t c0 = hi(p) ^ c.c1, c1 = lo(p), c2 = c.h ^ r.l, c3 = c.l;
 #pragma unroll
-    for (int i = 0; i < 10; ++i) {
-      const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
-      const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
-      c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ a;
-      c1 = static_cast<uint32_t>(p1);
-      c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ b;
-      c3 = static_cast<uint32_t>(p0);
-      a += 0x9E3779B9u;
-      b += 0xBB67AE85u;
+    for (int i = 0; i < LATE; ++i) {
+      const uint64_t p0 = wide(M0, c0), p1 = wide(M1, c2);
+      c0 = hi(p1) ^ c1 ^ a_[i];
+      c1 = lo(p1);
+      c2 = hi(p0) ^ c3 ^ b_[i];
+      c3 = lo(p0);
     }
     w[0] = c0;
     w[1] = c1;
@@ -65,43 +110,30 @@ struct Dropout {
     return word >= border ? v * scale : 0.0f;
   }
 
-  // D() of columns c .. c + 7 of a row, c a multiple of 8.
-  __device__ __forceinline__ void apply8(uint32_t row, int c, float (&v)[8]) const {
+  // D() of a block's four columns.
+  __device__ __forceinline__ void apply4(const Row& r, const Columns& c, float* v) const {
+    uint32_t w[4];
+    words(r, c, w);
 #pragma unroll
-    for (int k = 0; k < 8; k += 4) {
-      uint32_t w[4];
-      words(row, static_cast<uint32_t>(c + k) / 4, w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[k + i] = apply(v[k + i], w[i]);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = apply(v[i], w[i]);
   }
-
-  // The words of the N columns c0 + i * step (N and step multiples of 4) of a
-  // lane whose warp's lanes hold neighbouring columns, c0 % 4 == lane % 4: lane
-  // l of a quad computes the block of the quad's columns for every fourth step,
-  // from step l on, and the quad transposes its 4 x 4 words.  All 32 lanes call
-  // it together.
-  template <int N>
-  __device__ __forceinline__ void words_of_columns(uint32_t row, int c0, int step,
-                                                   uint32_t (&out)[N]) const {
-    static_assert(N % 4 == 0, "whole quads");
-    const int at = threadIdx.x & 3;
-    const bool odd = at & 1, upper = at & 2;
+  // D() of four values of four neighbouring lanes each, value i of the lanes
+  // being block i's columns in order; lane l gives the block of value l.  The
+  // quad transposes its 4 x 4 words.  All 32 lanes call it together.
+  __device__ __forceinline__ void apply_quad(const Row& r, const Columns& c, float* v) const {
+    const bool odd = threadIdx.x & 1, upper = threadIdx.x & 2;
+    uint32_t w[4];
+    words(r, c, w);
+    uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1);
+    uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+    if (odd) w[0] = x, w[2] = y;
+    else w[1] = x, w[3] = y;
+    x = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[2], 2);
+    y = __shfl_xor_sync(0xffffffffu, upper ? w[1] : w[3], 2);
+    if (upper) w[0] = x, w[1] = y;
+    else w[2] = x, w[3] = y;
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      uint32_t w[4];
-      words(row, static_cast<uint32_t>(c0 + (i + at) * step) / 4, w);
-      uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1);
-      uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
-      if (odd) w[0] = x, w[2] = y;
-      else w[1] = x, w[3] = y;
-      x = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[2], 2);
-      y = __shfl_xor_sync(0xffffffffu, upper ? w[1] : w[3], 2);
-      if (upper) w[0] = x, w[1] = y;
-      else w[2] = x, w[3] = y;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) out[i + s] = w[s];
-    }
+    for (int i = 0; i < 4; ++i) v[i] = apply(v[i], w[i]);
   }
 };
 

@@ -1,6 +1,6 @@
-// Native marshalling of the feed-forward operators for torch tensors: the
-// checks, output allocations and argument structures of layers.py without the
-// interpreter, for calls whose time is the host's (a few tokens).  Every
+// Native marshalling of the operators of mt_layers.h and mt_model.h for torch
+// tensors: the checks, output allocations and argument structures of layers.py
+// and model.py without the interpreter, for calls whose time is the host's (a few tokens).  Every
 // function returns None for anything it does not take (another type, layout,
 // device or device context, a tensor subclass), and the caller goes on in
 // Python, which takes it or says what is wrong; an integer is the status of a
@@ -14,7 +14,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "mt_layers.h"
+#include "mt_model.h"
 
 namespace {
 
@@ -25,6 +25,12 @@ mt_status (*g_rms_norm)(const mt_rms_norm_args*, cudaStream_t);
 mt_status (*g_rms_norm_backward)(const mt_rms_norm_backward_args*, cudaStream_t);
 mt_status (*g_linear)(const mt_linear_args*, cudaStream_t);
 mt_status (*g_linear_backward)(const mt_linear_backward_args*, cudaStream_t);
+// use_model_library
+mt_status (*g_layer_norm)(const mt_layer_norm_args*, cudaStream_t);
+mt_status (*g_layer_norm_backward)(const mt_layer_norm_backward_args*, cudaStream_t);
+mt_status (*g_dropout)(const mt_dropout_args*, cudaStream_t);
+mt_status (*g_loss)(const mt_linear_cross_entropy_args*, cudaStream_t);
+mt_status (*g_loss_backward)(const mt_linear_cross_entropy_backward_args*, cudaStream_t);
 
 int code_of(ScalarType t) {
   switch (t) {
@@ -374,6 +380,335 @@ PyObject* linear_backward(PyObject*, PyObject* const* o, Py_ssize_t n) {
   });
 }
 
+// Dropout's probability, seed and sequence.
+struct Drop {
+  double p = 0.0;
+  const int64_t* seed = nullptr;
+  uint64_t sequence = 0;
+  bool read(PyObject* probability, PyObject* seed_, PyObject* sequence_, c10::Device dev) {
+    Operand s;
+    if (!PyFloat_Check(probability) || !PyLong_Check(sequence_) || !s.read(seed_, true))
+      return false;
+    p = PyFloat_AS_DOUBLE(probability);
+    if (!(p >= 0.0 && p < 1.0) || (p > 0.0 && !s.t)) return false;
+    if (s.t) {
+      if (s.t->scalar_type() != ScalarType::Long || s.t->device() != dev || s.t->numel() != 1)
+        return false;
+      seed = static_cast<const int64_t*>(s.t->data_ptr());
+    }
+    sequence = PyLong_AsUnsignedLongLong(sequence_);
+    if (PyErr_Occurred()) {  // out of range
+      PyErr_Clear();
+      return false;
+    }
+    return true;
+  }
+};
+
+// layer_norm(x, weight, bias, residual, eps, dropout, seed, sequence)
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Operand x, w, b, r;
+    if (n != 8 || !x.read(a[0], false) || !w.read(a[1], true) || !b.read(a[2], true) ||
+        !r.read(a[3], true) || !PyFloat_Check(a[4]) || !lead(*x.t))
+      return none();
+    const ScalarType type = x.t->scalar_type();
+    if (!is_half(type) && type != ScalarType::Float) return none();
+    const c10::Device dev = x.t->device();
+    Drop drop;
+    if (!drop.read(a[5], a[6], a[7], dev)) return none();
+    mt_layer_norm_args g{};
+    g.rows = x.t->size(0);
+    g.d = x.t->size(1);
+    Matrix m;
+    if (!m.read(*x.t, g.rows, g.d, type, dev)) return none();
+    g.x = m.p;
+    g.ldx = m.ld;
+    if (w.t && b.t && w.t->scalar_type() != b.t->scalar_type()) return none();
+    for (const at::Tensor* v : {w.t, b.t}) {
+      if (!v) continue;
+      if (!vector(*v, g.d, type, ScalarType::Float, dev)) return none();
+      g.weight_dtype = code_of(v->scalar_type());
+    }
+    if (w.t) g.weight = w.t->data_ptr();
+    if (b.t) g.bias = b.t->data_ptr();
+    if (r.t) {
+      if (!m.read(*r.t, g.rows, g.d, type, dev)) return none();
+      g.residual = m.p;
+      g.ldr = m.ld;
+    }
+    g.eps = static_cast<float>(PyFloat_AS_DOUBLE(a[4]));
+    g.dtype = code_of(type);
+    g.seed = drop.seed;
+    g.sequence = drop.sequence;
+    g.dropout = drop.p;
+    at::Tensor h, y, mean, rstd;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      if (r.t || drop.p > 0.0) {
+        h = make({g.rows, g.d}, type, *x.t);
+        g.h = h.data_ptr();
+        g.ldh = g.d > 0 ? g.d : 1;
+      }
+      y = make({g.rows, g.d}, type, *x.t);
+      g.y = y.data_ptr();
+      g.ldy = g.d > 0 ? g.d : 1;
+      mean = make({g.rows}, ScalarType::Float, *x.t);
+      rstd = make({g.rows}, ScalarType::Float, *x.t);
+      g.mean = static_cast<float*>(mean.data_ptr());
+      g.rstd = static_cast<float*>(rstd.data_ptr());
+      st = g_layer_norm(&g, stream_of(*x.t));
+    }
+    if (st != MT_OK) return refused(st);
+    PyObject* hp = a[0];
+    if (h.defined()) hp = wrap(h);
+    else Py_INCREF(hp);
+    return tuple(wrap(y), hp, wrap(mean), wrap(rstd));
+  });
+}
+
+// layer_norm_backward(dy, h, weight, mean, rstd, dh, dropout, seed, sequence,
+//                     need_weight, need_bias)
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Operand dy, h, w, mean, rstd, dh;
+    if (n != 11 || !dy.read(a[0], false) || !h.read(a[1], false) || !w.read(a[2], true) ||
+        !mean.read(a[3], false) || !rstd.read(a[4], false) || !dh.read(a[5], true) ||
+        !lead(*dy.t))
+      return none();
+    const ScalarType type = dy.t->scalar_type(), f32 = ScalarType::Float;
+    if (!is_half(type) && type != f32) return none();
+    const c10::Device dev = dy.t->device();
+    Drop drop;
+    if (!drop.read(a[6], a[7], a[8], dev)) return none();
+    mt_layer_norm_backward_args g{};
+    g.rows = dy.t->size(0);
+    g.d = dy.t->size(1);
+    Matrix m;
+    if (!m.read(*dy.t, g.rows, g.d, type, dev)) return none();
+    g.dy = m.p;
+    g.lddy = m.ld;
+    if (!m.read(*h.t, g.rows, g.d, type, dev)) return none();
+    g.h = m.p;
+    g.ldh = m.ld;
+    if (w.t) {
+      if (!vector(*w.t, g.d, type, f32, dev)) return none();
+      g.weight = w.t->data_ptr();
+      g.weight_dtype = code_of(w.t->scalar_type());
+    }
+    if (!vector(*mean.t, g.rows, f32, f32, dev) || !vector(*rstd.t, g.rows, f32, f32, dev))
+      return none();
+    g.mean = static_cast<const float*>(mean.t->data_ptr());
+    g.rstd = static_cast<const float*>(rstd.t->data_ptr());
+    if (dh.t) {
+      if (!m.read(*dh.t, g.rows, g.d, type, dev)) return none();
+      g.dh = m.p;
+      g.lddh = m.ld;
+    }
+    g.dtype = code_of(type);
+    g.seed = drop.seed;
+    g.sequence = drop.sequence;
+    g.dropout = drop.p;
+    const bool need_weight = flag(a[9]), need_bias = flag(a[10]);
+    at::Tensor dx, dres, dw, db;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      dx = make({g.rows, g.d}, type, *dy.t);
+      g.dx = dx.data_ptr();
+      g.lddx = g.lddres = g.d > 0 ? g.d : 1;
+      if (drop.p > 0.0) {
+        dres = make({g.rows, g.d}, type, *dy.t);
+        g.dresidual = dres.data_ptr();
+      }
+      if (need_weight) {
+        dw = make({g.d}, f32, *dy.t);
+        g.dweight = static_cast<float*>(dw.data_ptr());
+      }
+      if (need_bias) {
+        db = make({g.d}, f32, *dy.t);
+        g.dbias = static_cast<float*>(db.data_ptr());
+      }
+      st = g_layer_norm_backward(&g, stream_of(*dy.t));
+    }
+    if (st != MT_OK) return refused(st);
+    PyObject* dxp = wrap(dx);
+    PyObject* dresp = dxp;
+    if (dres.defined()) dresp = wrap(dres);
+    else Py_INCREF(dxp);
+    return tuple(dxp, dresp, wrap(dw), wrap(db));
+  });
+}
+
+// dropout(x, p, seed, sequence, residual)
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Operand x, r;
+    if (n != 5 || !x.read(a[0], false) || !r.read(a[4], true) || !lead(*x.t)) return none();
+    const ScalarType type = x.t->scalar_type();
+    if (!is_half(type) && type != ScalarType::Float) return none();
+    const c10::Device dev = x.t->device();
+    Drop drop;
+    if (!drop.read(a[1], a[2], a[3], dev) || !drop.seed) return none();
+    mt_dropout_args g{};
+    g.rows = x.t->size(0);
+    g.d = x.t->size(1);
+    Matrix m;
+    if (!m.read(*x.t, g.rows, g.d, type, dev)) return none();
+    g.x = m.p;
+    g.ldx = m.ld;
+    if (r.t) {
+      if (!m.read(*r.t, g.rows, g.d, type, dev)) return none();
+      g.residual = m.p;
+      g.ldr = m.ld;
+    }
+    g.seed = drop.seed;
+    g.sequence = drop.sequence;
+    g.p = drop.p;
+    g.dtype = code_of(type);
+    at::Tensor y;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      y = make({g.rows, g.d}, type, *x.t);
+      g.y = y.data_ptr();
+      g.ldy = g.d > 0 ? g.d : 1;
+      st = g_dropout(&g, stream_of(*x.t));
+    }
+    if (st != MT_OK) return refused(st);
+    return wrap(y);
+  });
+}
+
+// What the loss and its gradient share: a, b, target and the options.
+struct Head {
+  ScalarType type;
+  c10::Device dev{c10::DeviceType::CPU};
+  int64_t T = 0, K = 0, V = 0, ignore_index = 0;
+  Matrix a, b;
+  const int64_t* target = nullptr;
+  float smoothing = 0.0f, z_loss = 0.0f;
+  bool trans = false;
+  bool read(const Operand& at_, const Operand& bt, const Operand& tt, PyObject* trans_,
+            PyObject* ignore, PyObject* s, PyObject* c) {
+    if (!lead(*at_.t) || bt.t->dim() != 2 || !PyLong_Check(ignore) || !PyFloat_Check(s) ||
+        !PyFloat_Check(c))
+      return false;
+    type = at_.t->scalar_type();
+    dev = at_.t->device();
+    if (!is_half(type)) return false;
+    trans = flag(trans_);
+    T = at_.t->size(0);
+    K = at_.t->size(1);
+    V = bt.t->size(trans ? 0 : 1);
+    if (!a.read(*at_.t, T, K, type, dev) ||
+        !b.read(*bt.t, trans ? V : K, trans ? K : V, type, dev) ||
+        !vector(*tt.t, T, ScalarType::Long, ScalarType::Long, dev) || (T > 0 && V == 0))
+      return false;
+    target = static_cast<const int64_t*>(tt.t->data_ptr());
+    const double sd = PyFloat_AS_DOUBLE(s), cd = PyFloat_AS_DOUBLE(c);
+    if (!(sd >= 0.0 && sd <= 1.0) || !(cd >= 0.0 && cd <= 3.4e38)) return false;
+    smoothing = static_cast<float>(sd);
+    z_loss = static_cast<float>(cd);
+    ignore_index = PyLong_AsLongLong(ignore);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      return false;
+    }
+    return true;
+  }
+  template <class G>
+  void fill(G* g) const {
+    g->T = T;
+    g->K = K;
+    g->V = V;
+    g->A = a.p;
+    g->lda = a.ld;
+    g->B = b.p;
+    g->ldb = b.ld;
+    g->target = target;
+    g->ignore_index = ignore_index;
+    g->label_smoothing = smoothing;
+    g->z_loss = z_loss;
+    g->trans_b = trans;
+    g->dtype = code_of(type);
+  }
+};
+
+// linear_cross_entropy(a, b, target, trans_b, ignore_index, label_smoothing,
+//                      z_loss)
+PyObject* linear_cross_entropy(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Operand a, b, target;
+    Head head;
+    if (n != 7 || !a.read(o[0], false) || !b.read(o[1], false) || !target.read(o[2], false) ||
+        !head.read(a, b, target, o[3], o[4], o[5], o[6]))
+      return none();
+    mt_linear_cross_entropy_args g{};
+    head.fill(&g);
+    at::Tensor loss, lse;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      loss = make({head.T}, ScalarType::Float, *a.t);
+      lse = make({head.T}, ScalarType::Float, *a.t);
+      g.loss = static_cast<float*>(loss.data_ptr());
+      g.lse = static_cast<float*>(lse.data_ptr());
+      st = g_loss(&g, stream_of(*a.t));
+    }
+    if (st != MT_OK) return refused(st);
+    return tuple(wrap(loss), wrap(lse));
+  });
+}
+
+// linear_cross_entropy_backward(dloss, a, b, target, lse, trans_b,
+//     ignore_index, label_smoothing, z_loss, need_a, need_b, db_dtype)
+PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Operand dloss, a, b, target, lse;
+    Head head;
+    if (n != 12 || !dloss.read(o[0], false) || !a.read(o[1], false) || !b.read(o[2], false) ||
+        !target.read(o[3], false) || !lse.read(o[4], false) ||
+        !head.read(a, b, target, o[5], o[6], o[7], o[8]))
+      return none();
+    const ScalarType f32 = ScalarType::Float;
+    ScalarType db_type = head.type;
+    if (o[11] != Py_None) {
+      if (!THPDtype_Check(o[11])) return none();
+      db_type = reinterpret_cast<THPDtype*>(o[11])->scalar_type;
+    }
+    if ((db_type != head.type && db_type != f32) || !vector(*dloss.t, head.T, f32, f32, head.dev) ||
+        !vector(*lse.t, head.T, f32, f32, head.dev))
+      return none();
+    mt_linear_cross_entropy_backward_args g{};
+    head.fill(&g);
+    g.dloss = static_cast<const float*>(dloss.t->data_ptr());
+    g.lse = static_cast<const float*>(lse.t->data_ptr());
+    g.db_dtype = code_of(db_type);
+    const bool need_a = flag(o[9]), need_b = flag(o[10]);
+    const int64_t rows = head.trans ? head.V : head.K, cols = head.trans ? head.K : head.V;
+    at::Tensor da, db;
+    mt_status st;
+    {
+      Unlocked unlocked;
+      if (need_a) {
+        da = make({head.T, head.K}, head.type, *a.t);
+        g.dA = da.data_ptr();
+        g.ldda = head.K > 0 ? head.K : 1;
+      }
+      if (need_b) {
+        db = make({rows, cols}, db_type, *a.t);
+        g.dB = db.data_ptr();
+        g.lddb = cols > 0 ? cols : 1;
+      }
+      st = g_loss_backward(&g, stream_of(*a.t));
+    }
+    if (st != MT_OK) return refused(st);
+    return tuple(wrap(da), wrap(db));
+  });
+}
+
 // use_library(mt_rms_norm, mt_rms_norm_backward, mt_linear,
 //             mt_linear_backward): the entry points' addresses.
 PyObject* use_library(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -393,6 +728,26 @@ PyObject* use_library(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// use_model_library(mt_layer_norm, mt_layer_norm_backward, mt_dropout,
+//     mt_linear_cross_entropy, mt_linear_cross_entropy_backward)
+PyObject* use_model_library(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 5) {
+    PyErr_SetString(PyExc_TypeError, "use_model_library takes five addresses");
+    return nullptr;
+  }
+  void* p[5];
+  for (int i = 0; i < 5; ++i) {
+    p[i] = PyLong_AsVoidPtr(a[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  g_layer_norm = reinterpret_cast<decltype(g_layer_norm)>(p[0]);
+  g_layer_norm_backward = reinterpret_cast<decltype(g_layer_norm_backward)>(p[1]);
+  g_dropout = reinterpret_cast<decltype(g_dropout)>(p[2]);
+  g_loss = reinterpret_cast<decltype(g_loss)>(p[3]);
+  g_loss_backward = reinterpret_cast<decltype(g_loss_backward)>(p[4]);
+  Py_RETURN_NONE;
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return PyMethodDef{name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(F)),
@@ -404,6 +759,12 @@ PyMethodDef g_methods[] = {method<rms_norm>("rms_norm"),
                            method<linear>("linear"),
                            method<linear_backward>("linear_backward"),
                            method<use_library>("use_library"),
+                           method<layer_norm>("layer_norm"),
+                           method<layer_norm_backward>("layer_norm_backward"),
+                           method<dropout>("dropout"),
+                           method<linear_cross_entropy>("linear_cross_entropy"),
+                           method<linear_cross_entropy_backward>("linear_cross_entropy_backward"),
+                           method<use_model_library>("use_model_library"),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "mt_torch_binding", nullptr, -1, g_methods};

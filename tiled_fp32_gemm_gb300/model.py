@@ -3,7 +3,8 @@
 
 ``layer_norm``, ``dropout``, ``linear_cross_entropy`` and their gradients on
 torch CUDA tensors, and the C entry points under their own names taking a
-filled argument structure.  Marshalling only, as in ``layers``; ``stream`` (a
+filled argument structure.  Marshalling only, as in ``layers`` (natively where
+a call allocates its outputs); ``stream`` (a
 handle; None: the current stream) runs a call elsewhere, its outputs in that
 stream's memory; operands have to stay until its work is done.
 """
@@ -108,7 +109,15 @@ def _setup():
     handle = lib()
     for name in SIGNATURES:
         layers._functions.setdefault(name, getattr(handle, name))
+    _point_native()
     _torch = layers._torch
+
+
+def _point_native():
+    """Points the native marshalling at the library the binding calls."""
+    if layers._native is not None:
+        layers._native.use_model_library(
+            *(ctypes.cast(layers._functions[n], _P).value for n in SIGNATURES))
 
 
 def _dropped(p, seed, sequence, device):
@@ -148,6 +157,11 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, dropout=0.0, 
     if stream is not None:
         return elsewhere(layer_norm, stream, x, weight, bias, residual, eps, dropout, seed,
                          sequence, out, h_out)
+    if layers._native is not None and out is None and h_out is None:
+        r = layers._native.layer_norm(x, weight, bias, residual, float(eps), dropout, seed,
+                                      sequence)
+        if r is not None:
+            return layers._done(r, "mt_layer_norm")
     rows, d, dt, dev, xp, ldx = layers._first(x, "x", layers._FLOATS)
     p, sp, sequence = _dropped(dropout, seed, sequence, dev)
     rp = ldr = hp = ldh = wp = bp = wcode = 0
@@ -189,6 +203,11 @@ def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, dropout=0.0, seed=No
     if stream is not None:
         return elsewhere(layer_norm_backward, stream, dy, h, weight, mean, rstd, dh, dropout,
                          seed, sequence, need_weight, need_bias, out)
+    if layers._native is not None and out is None:
+        r = layers._native.layer_norm_backward(dy, h, weight, mean, rstd, dh, dropout, seed,
+                                               sequence, bool(need_weight), bool(need_bias))
+        if r is not None:
+            return layers._done(r, "mt_layer_norm_backward")
     rows, d, dt, dev, dyp, lddy = layers._first(dy, "dy", layers._FLOATS)
     p, sp, sequence = _dropped(dropout, seed, sequence, dev)
     f32 = _torch.float32
@@ -232,6 +251,10 @@ def dropout(x, p, seed, sequence=0, residual=None, out=None, stream=None):
         _setup()
     if stream is not None:
         return elsewhere(dropout, stream, x, p, seed, sequence, residual, out)
+    if layers._native is not None and out is None:
+        r = layers._native.dropout(x, p, seed, sequence, residual)
+        if r is not None:
+            return layers._done(r, "mt_dropout")
     rows, d, dt, dev, xp, ldx = layers._first(x, "x", layers._FLOATS)
     if seed is None:
         raise TypeError("seed must be an int64 CUDA tensor of one value")
@@ -291,6 +314,11 @@ def linear_cross_entropy(a, b, target, trans_b=False, ignore_index=-100, label_s
     if stream is not None:
         return elsewhere(linear_cross_entropy, stream, a, b, target, trans_b, ignore_index,
                          label_smoothing, z_loss)
+    if layers._native is not None:
+        r = layers._native.linear_cross_entropy(a, b, target, bool(trans_b), ignore_index,
+                                                label_smoothing, z_loss)
+        if r is not None:
+            return layers._done(r, "mt_linear_cross_entropy")
     T, K, V, dt, dev, ap, lda, bp, ldb, tp = _head(a, b, target, trans_b)
     s, c = _loss_options(label_smoothing, z_loss)
     loss = layers._empty(T, dtype=_torch.float32, device=dev)
@@ -317,6 +345,12 @@ def linear_cross_entropy_backward(dloss, a, b, target, lse, trans_b=False, ignor
     if stream is not None:
         return elsewhere(linear_cross_entropy_backward, stream, dloss, a, b, target, lse, trans_b,
                          ignore_index, label_smoothing, z_loss, need_a, need_b, db_dtype)
+    if layers._native is not None:
+        r = layers._native.linear_cross_entropy_backward(
+            dloss, a, b, target, lse, bool(trans_b), ignore_index, label_smoothing, z_loss,
+            bool(need_a), bool(need_b), db_dtype)
+        if r is not None:
+            return layers._done(r, "mt_linear_cross_entropy_backward")
     T, K, V, dt, dev, ap, lda, bp, ldb, tp = _head(a, b, target, trans_b)
     s, c = _loss_options(label_smoothing, z_loss)
     f32 = _torch.float32
