@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // K slice's partial tile.
 struct CUpdate {
   static constexpr bool DEPENDENT_LAUNCH = false;
-  static constexpr int WARPS = 4;
+  static constexpr int WARPS = 4, STORE_BYTES = 0;
   Epilogue ep;
   __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int /*half*/,
                                              int lane, const Sched& sched, float* square,

@@ -108,6 +108,8 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int j) {
 // square, rank) takes the 32 x 256 accumulator of warp q's lanes at TMEM
 // address t_row (rows q * 32 .. of CTA `rank`'s half) to memory; with
 // Drain::WARPS = 8 two warps share it (half 0 and 1).
+// Drain::STORE_BYTES: shared memory that the drain stages its stores in, each
+// warp's last bulk group waited for before the CTA leaves (0: none).
 // Drain::DEPENDENT_LAUNCH: the kernel is launched as a programmatic dependent
 // and lets its own dependents launch early.
 // ACC_BUFS accumulators of 256 columns each (1 or 2) sit in TMEM.
@@ -127,6 +129,22 @@ struct PairGeometry {
                                    EPI_STAGE_BYTES;
 };
 
+// A drain warp's part of the staging that Drain::STORE_BYTES asks for: past the
+// barriers, from a 1024-byte boundary on, as swizzled boxes want it.  `square`:
+// the warp's pointer that the pair kernel gives the drain.
+template <class Drain>
+__device__ __forceinline__ uint8_t* store_staging(float* square, int q, int half) {
+  const uintptr_t base = reinterpret_cast<uintptr_t>(square - q * EPI_WARP_FLOATS);
+  return reinterpret_cast<uint8_t*>((base + 1023) & ~static_cast<uintptr_t>(1023)) +
+         (half * 4 + q) * (Drain::STORE_BYTES / Drain::WARPS);
+}
+// Dynamic shared memory of the pair kernel.
+template <class Drain, int ACC_BUFS>
+constexpr int pair_smem() {
+  return PairGeometry<ACC_BUFS>::SMEM_BYTES - EPI_STAGE_BYTES +
+         (Drain::STORE_BYTES > 0 ? 1024 - 256 + Drain::STORE_BYTES : 0);
+}
+
 // Threads of the pair kernel: the copy warp, the MMA warp, the drain's warps.
 template <class Drain>
 constexpr int pair_threads() {
@@ -136,7 +154,8 @@ constexpr int pair_threads() {
 template <class E, bool A_MN, bool B_MN, int ACC_BUFS, class Drain>
 __global__ void __launch_bounds__(pair_threads<Drain>(), 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                const __grid_constant__ CUtensorMap tmap_b, uint32_t idesc, Drain drain, int Kt,
+                const __grid_constant__ CUtensorMap tmap_b, uint32_t idesc,
+                const __grid_constant__ Drain drain, int Kt,
                 int tiles_m, int tiles_n, int group_m, Sched sched, int fault_inject) {
   static_assert(E::BYTES == 2 || (!A_MN && !B_MN), "8-bit operands are K-major");
   using G = PairGeometry<ACC_BUFS>;
@@ -285,6 +304,7 @@ __global__ void __launch_bounds__(pair_threads<Drain>(), 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty_even + 8u * static_cast<uint32_t>(b));
     }
+    if (Drain::STORE_BYTES > 0 && lane == 0) bulk_wait();
   }
 
   tc_fence_before();

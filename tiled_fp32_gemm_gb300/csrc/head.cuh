@@ -88,26 +88,55 @@ struct HeadStats {
 
 // A token's factors of D: D = exp2(z * log2(e) - x) * p - all - (its target: hit).
 struct __align__(16) HeadRow {
+  static constexpr int DEAD = -2;  // no target: a row of zeros
+
   float x, p, all, hit;
+  int target;  // column of the vocabulary; -1: outside it, and the factors are NaN
+};
+
+// What they are made of.
+struct HeadSource {
+  const float* dloss;
+  const float* lse;
+  const int64_t* target;
+  int64_t ignore_index;
+  float smoothing, z_loss;
+  int V;
+
+  __device__ __forceinline__ HeadRow row(int64_t t, float scale) const {
+    const int64_t column = target[t];
+    HeadRow r{0.0f, 0.0f, 0.0f, 0.0f, HeadRow::DEAD};
+    if (column != ignore_index) {
+      const bool inside = column >= 0 && column < V;
+      const float l = lse[t], g = inside ? dloss[t] * scale : NAN;
+      r.x = l * LOG2E;
+      r.p = g * (1.0f + 2.0f * z_loss * l);
+      r.all = g * (smoothing / static_cast<float>(V));
+      r.hit = g * (1.0f - smoothing);
+      r.target = inside ? static_cast<int>(column) : -1;
+    }
+    return r;
+  }
 };
 
 // D of columns first .. first + C - 1 of the vocabulary, to a T x C matrix of
-// rows of ldd 16-bit values (a multiple of 64, on 16 bytes): whole groups of
-// eight columns may be written past C.
+// rows of ldd 16-bit values, or to boxes of 64 columns x 32 rows of its map.
 struct HeadGrad {
+  CUtensorMap map;
   int T, C;
-  const HeadRow* rows;
-  const int* target;  // column of the vocabulary; DEAD: a row of zeros
+  const HeadRow* rows;  // with fp16's scale; null: from the source
+  HeadSource source;
   int first;
   void* D;
   int64_t ldd;
   int dtype;
   BoundsRecord* bounds;
 
-  static constexpr int DEAD = -2;
-
-  __device__ __forceinline__ bool row_ok(int t) const {
-    return bounds_ok(bounds, SITE_ROWS, t, 1, T);
+  // Token t's factors, those of no target where there is no such token.
+  __device__ __forceinline__ HeadRow row(int t, int end) const {
+    if (t >= end || !bounds_ok(bounds, SITE_ROWS, t, 1, T))
+      return HeadRow{0.0f, 0.0f, 0.0f, 0.0f, HeadRow::DEAD};
+    return rows ? rows[t] : source.row(t, 1.0f);
   }
 };
 
@@ -184,28 +213,32 @@ __device__ __forceinline__ void finish(const HeadStats& e, int c, int t_begin, i
   }
 }
 
+// The tokens' factors are read 16 rows ahead, a row a lane, and handed round.
 template <class T, class Sums>
 __device__ __forceinline__ void finish_typed(const HeadGrad& e, int c, int t_begin, int t_end,
                                              Sums&& logits) {
   T* const D = static_cast<T*>(e.D);
-  const int column = e.first + c;
+  const int lane = threadIdx.x % 32, column = e.first + c;
+  auto load = [&](int t) { return e.row(t + lane, lane < FINISH_ROWS ? t_end : 0); };
+  HeadRow next = load(t_begin);
 #pragma unroll 1
   for (int t = t_begin; t < t_end; t += FINISH_ROWS) {
+    const HeadRow now = next;
+    if (t + FINISH_ROWS < t_end) next = load(t + FINISH_ROWS);
     Rows v;
     __syncwarp();
     logits(t, v);
-    if (c >= e.C) continue;
+    T* to = D + t * e.ldd + c;
 #pragma unroll
-    for (int i = 0; i < FINISH_ROWS; ++i) {
-      const int row = t + i;
-      if (row >= t_end || !e.row_ok(row)) break;
-      const HeadRow r = e.rows[row];  // the same address in every lane
-      const int target = e.target[row];
-      const float p = exp2_approx(fmaf(v[i], LOG2E, -r.x));
-      const float d = fmaf(p, r.p, -r.all) - (target == column ? r.hit : 0.0f);
-      const int64_t at = row * e.ldd + c;
-      if (bounds_ok(e.bounds, SITE_C_STORE, at, 1, e.T * e.ldd))
-        D[at] = row::from_f32<T>(target == HeadGrad::DEAD ? 0.0f : d);
+    for (int i = 0; i < FINISH_ROWS; ++i, to += e.ldd) {
+      auto of = [&](float f) { return __shfl_sync(0xffffffffu, f, i); };
+      const int target = __shfl_sync(0xffffffffu, now.target, i);
+      const float p = exp2_approx(fmaf(v[i], LOG2E, -of(now.x)));
+      const float hit = of(now.hit);
+      const float d = fmaf(p, of(now.p), -of(now.all)) - (target == column ? hit : 0.0f);
+      if (c < e.C && t + i < t_end &&
+          bounds_ok(e.bounds, SITE_C_STORE, (t + i) * e.ldd + c, 1, e.T * e.ldd))
+        *to = row::from_f32<T>(target == HeadRow::DEAD ? 0.0f : d);
     }
   }
 }
@@ -229,8 +262,8 @@ cudaError_t launch_head(const LinearArgs& a, const LinearPlan& p, void* workspac
 cudaError_t head_prepare();
 template <class Ep>
 cudaError_t launch_head_pair(const CUtensorMap& map_x, const CUtensorMap& map_w, uint32_t idesc,
-                             const Ep& ep, bool w_mn, int smem, int kt, int clusters,
-                             int fault_inject, cudaStream_t stream);
+                             const Ep& ep, bool w_mn, int kt, int clusters, int fault_inject,
+                             cudaStream_t stream);
 template <class Ep>
 linear::LinearKernel head_split_kernel_for(int bt);
 cudaError_t head_pair_read_and_clear_status(unsigned int* status);

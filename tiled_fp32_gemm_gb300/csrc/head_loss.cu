@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -27,7 +28,7 @@ int64_t up256(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
 
 // --- forwards -----------------------------------------------------------------
 
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 256;
 
 struct JoinArgs {
   int64_t T, V, slots;
@@ -43,7 +44,7 @@ struct JoinArgs {
 };
 
 // Joins the entries of `across` tokens (a power of two up to 32) a CTA: a
-// thread takes every (1024 / across)th of a token's, and the threads' meet in
+// thread takes every (256 / across)th of a token's, and the threads' meet in
 // a fixed tree.  Logarithm and difference in fp64: one a token, and lse is some
 // 12 while the loss may be a thousandth of it.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a, int across) {
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a, in
   Softmax s{-INFINITY, 0.0f};
   float sum = 0.0f;
   if (t < a.T) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t i = me; i < a.slots; i += lanes) {
       const int64_t at = i * a.T + t;
       if (!bounds_ok(a.bounds, SITE_PARTIAL, at, 1, a.slots * a.T)) continue;
@@ -94,16 +95,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a, in
   a.loss[t] = loss;
 }
 
-// The product whose logits either pass takes, columns first .. first + n - 1.
-LinearArgs logits_of(const HeadLossArgs& a, int64_t first, int64_t n) {
+// A piece of the weight: columns `first` .. first + n - 1 of the vocabulary, as
+// they are stored at p.
+struct Piece {
+  const void* p;
+  int64_t ld, first, n;
+};
+Piece piece_of(const HeadLossArgs& a, int64_t first, int64_t n) {
+  return Piece{static_cast<const char*>(a.W) + 2 * (a.w_mn ? first : first * a.ldw), a.ldw, first,
+               n};
+}
+
+// The product whose logits either pass takes.
+LinearArgs logits_of(const HeadLossArgs& a, const Piece& w) {
   LinearArgs l{};
   l.T = a.T;
-  l.C = n;
+  l.C = w.n;
   l.K = a.K;
   l.X = a.X;
   l.ldx = a.ldx;
-  l.W = static_cast<const char*>(a.W) + 2 * (a.w_mn ? first : first * a.ldw);
-  l.ldw = a.ldw;
+  l.W = w.p;
+  l.ldw = w.ld;
   l.w_mn = a.w_mn;
   l.dtype = l.out_dtype = a.dtype;
   l.act = ACT_NONE;
@@ -111,11 +123,22 @@ LinearArgs logits_of(const HeadLossArgs& a, int64_t first, int64_t n) {
   return l;
 }
 
+// Pairs pay from half as many tiles on as for the linear layer, whose epilogue
+// costs the split kernel less: there 16 tokens' statistics meet over a warp's
+// lanes, here a thread walks over one token's.  Past 2048 values of K few tiles
+// want the split kernel's slices.  Measured (bf16, loss, us for the split kernel
+// against pairs): 256 x 1024 x 8192 (32 pairs) 20.0 / 14.9, 300 x 512 x 5000 (40)
+// 17.7 / 12.3, 512 x 1024 x 2048 (16) 17.2 / 14.0, 200 x 256 x 1024 (4) 13.6 /
+// 10.4, 1024 x 2048 x 1024 (16) 18.9 / 18.8, but 256 x 4096 x 4096 (16) 23.0 / 27.5.
+LinearPlan plan_logits(const LinearArgs& l, int sms) {
+  return plan_linear(l, sms, l.K <= 2048 ? 7 : sms);
+}
+
 }  // namespace
 
 HeadLossPlan plan_head_loss(const HeadLossArgs& a, int sms) {
   HeadLossPlan p{};
-  p.product = plan_linear(logits_of(a, 0, a.V), sms);
+  p.product = plan_logits(logits_of(a, piece_of(a, 0, a.V)), sms);
   p.slots = p.product.pair ? ceil_div(a.V, 2 * PAIR_SLOT) * 2
                            : ceil_div(a.V, linear::LINEAR_BC) * (linear::LINEAR_BC / LANE_SLOT);
   p.parts_bytes = up256(p.slots * a.T * 8);
@@ -135,7 +158,7 @@ cudaError_t launch_head_loss(const HeadLossArgs& a, const HeadLossPlan& p, float
   const HeadStats stats{static_cast<int>(a.T), static_cast<int>(a.V), a.target, parts, sums,
                         target_logit, p.slots, a.bounds};
   const cudaError_t e =
-      launch_head(logits_of(a, 0, a.V), p.product,
+      launch_head(logits_of(a, piece_of(a, 0, a.V)), p.product,
                   ws + p.parts_bytes + p.sums_bytes + p.target_bytes, stats, stream, fault_inject);
   if (e != cudaSuccess) return e;
   // As many tokens side by side as leave a CTA for every SM.
@@ -151,18 +174,14 @@ cudaError_t launch_head_loss(const HeadLossArgs& a, const HeadLossPlan& p, float
 
 namespace {
 
+// fp16: the tokens' factors, with D's scale in them, are made beforehand.
 struct RowArgs {
-  int64_t T, V;
-  const float* dloss;
-  const float* lse;
-  const int64_t* target;
-  int64_t ignore_index;
-  float smoothing, z_loss;
+  int64_t T;
+  HeadSource source;
   HeadRow* rows;
-  int* column;
-  // fp16 only (null otherwise): per-CTA maxima of |dloss| (amax), and what the
-  // products' results are multiplied with to undo D's scale: n factors for
-  // their rows, n ones for their columns.
+  // Per-CTA maxima of a token's largest factor (amax), and what the products'
+  // results are multiplied with to undo D's scale: n factors for their rows, n
+  // ones for their columns.
   float* amax;
   float* undo;
   float* ones;
@@ -176,8 +195,9 @@ constexpr int kMaxCtas = 256;  // CTAs that leave a maximum
 // The largest factor of a token's D: |dloss| (1 + 2 c |lse|); 0 for what does
 // not count (no target, not finite).
 __device__ __forceinline__ float size_of(const RowArgs& a, int64_t t) {
-  if (a.target[t] == a.ignore_index) return 0.0f;
-  const float v = fabsf(a.dloss[t]) * (1.0f + 2.0f * a.z_loss * fabsf(a.lse[t]));
+  const HeadSource& s = a.source;
+  if (s.target[t] == s.ignore_index) return 0.0f;
+  const float v = fabsf(s.dloss[t]) * (1.0f + 2.0f * s.z_loss * fabsf(s.lse[t]));
   return v < INFINITY ? v : 0.0f;
 }
 
@@ -201,18 +221,14 @@ __global__ void __launch_bounds__(kRowThreads) size_kernel(const RowArgs a) {
   if (threadIdx.x == 0) a.amax[blockIdx.x] = v;
 }
 
-// The tokens' factors of D; with `ctas` maxima, D's scale is the power of two
+// The tokens' factors of D.  From `ctas` maxima: D's scale is the power of two
 // that brings the largest to [2^13, 2^14): fp16 then keeps ten digits of a
 // probability down to 2^-27 of the largest factor, and 65504 is not reached.
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowArgs a, int ctas) {
   grid_launch_dependents();
   grid_wait();
-  float scale = 1.0f;
-  if (a.amax) {
-    const float top = cta_max(static_cast<int>(threadIdx.x) < ctas ? a.amax[threadIdx.x] : 0.0f);
-    const int e = top > 0.0f ? max(-126, min(126, 13 - ilogbf(top))) : 0;
-    scale = ldexpf(1.0f, e);
-  }
+  const float top = cta_max(static_cast<int>(threadIdx.x) < ctas ? a.amax[threadIdx.x] : 0.0f);
+  const float scale = ldexpf(1.0f, top > 0.0f ? max(-126, min(126, 13 - ilogbf(top))) : 0);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
        i < max(a.T, a.n); i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
     if (i < a.n) {
@@ -220,31 +236,38 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowArgs a, int 
       a.ones[i] = 1.0f;
     }
     if (i >= a.T || !bounds_ok(a.bounds, SITE_ROWS, i, 1, a.T)) continue;
-    const int64_t target = a.target[i];
-    HeadRow r{0.0f, 0.0f, 0.0f, 0.0f};
-    int column = HeadGrad::DEAD;
-    if (target != a.ignore_index) {
-      const bool inside = target >= 0 && target < a.V;
-      const float lse = a.lse[i], g = inside ? a.dloss[i] * scale : NAN;
-      r.x = lse * LOG2E;
-      r.p = g * (1.0f + 2.0f * a.z_loss * lse);
-      r.all = g * (a.smoothing / static_cast<float>(a.V));
-      r.hit = g * (1.0f - a.smoothing);
-      column = inside ? static_cast<int>(target) : -1;
-    }
-    a.rows[i] = r;
-    a.column[i] = column;
+    a.rows[i] = a.source.row(i, scale);
   }
 }
 
-// dX in its type from its sums over the pieces of the vocabulary.
+// dX in its type from its planes of sums, added in order.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads)
-    round_rows_kernel(const Matrix<const float> acc, const Matrix<T> to, int64_t rows, int cols) {
+    round_planes_kernel(const float* sums, int planes, int64_t plane, int64_t pitch,
+                        int64_t extent, const Matrix<T> to, int64_t rows, int cols) {
   grid_launch_dependents();
   grid_wait();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < cols; c += kRowThreads) to.store(r, c, acc.load(r, c));
+  const int64_t per_row = pitch / 4, total = rows * per_row;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
+    const int64_t r = i / per_row;
+    const int c = static_cast<int>(i % per_row) * 4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int p = 0; p < planes; ++p) {
+      const int64_t at = p * plane + r * pitch + c;
+      if (!bounds_ok(to.rec, SITE_PARTIAL, at, 4, extent)) continue;
+      const float4 v = *reinterpret_cast<const float4*>(sums + at);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + k < cols) to.store(r, c + k, v[k]);
+  }
 }
 
 // A piece of D: large enough that its products fill the GPU for several rounds
@@ -252,11 +275,11 @@ __global__ void __launch_bounds__(kRowThreads)
 // it and the two that read it.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 
-// The two products of a piece of n columns from `first` on.
+// The two products of a piece of the vocabulary.
 struct Products {
   LinearArgs x, w;
 };
-Products products_of(const HeadGradArgs& a, const void* d, int64_t ldd, int64_t first, int64_t n) {
+Products products_of(const HeadGradArgs& a, const void* d, int64_t ldd, const Piece& w) {
   const HeadLossArgs& l = a.loss;
   Products p{};
   p.x.dtype = p.w.dtype = l.dtype;
@@ -265,19 +288,19 @@ Products products_of(const HeadGradArgs& a, const void* d, int64_t ldd, int64_t 
   // dX = D * W^T: contracted over the piece.
   p.x.T = l.T;
   p.x.C = l.K;
-  p.x.K = n;
+  p.x.K = w.n;
   p.x.X = d;
   p.x.ldx = ldd;
-  p.x.W = static_cast<const char*>(l.W) + 2 * (l.w_mn ? first : first * l.ldw);
-  p.x.ldw = l.ldw;
+  p.x.W = w.p;
+  p.x.ldw = w.ld;
   p.x.w_mn = !l.w_mn;
   p.x.out_dtype = l.dtype;
   p.x.Y = a.dX;
   p.x.ldy = a.lddx;
   // dW as W is stored, contracted over the tokens.
   const int64_t elem = dtype_bytes(a.dw_dtype);
-  p.w.T = l.w_mn ? l.K : n;
-  p.w.C = l.w_mn ? n : l.K;
+  p.w.T = l.w_mn ? l.K : w.n;
+  p.w.C = l.w_mn ? w.n : l.K;
   p.w.K = l.T;
   p.w.X = l.w_mn ? l.X : d;
   p.w.ldx = l.w_mn ? l.ldx : ldd;
@@ -285,27 +308,39 @@ Products products_of(const HeadGradArgs& a, const void* d, int64_t ldd, int64_t 
   p.w.ldw = l.w_mn ? ldd : l.ldx;
   p.w.x_mn = p.w.w_mn = 1;
   p.w.out_dtype = a.dw_dtype;
-  p.w.Y = a.dW ? static_cast<char*>(a.dW) + elem * (l.w_mn ? first : first * a.lddw) : nullptr;
+  p.w.Y = a.dW ? static_cast<char*>(a.dW) + elem * (l.w_mn ? w.first : w.first * a.lddw) : nullptr;
   p.w.ldy = a.lddw;
   return p;
 }
 
-// Plans of a piece's launches.
+// Plans of a piece's launches.  Their operands are in a form that TMA reads:
+// the three products share the copies of those that are not.
 struct PiecePlan {
   LinearPlan logits, x, w;
-  int64_t bytes(const HeadGradArgs& a) const {
-    return std::max(up256(logits.workspace_bytes),
-                    (a.dX ? up256(x.workspace_bytes) : 0) + (a.dW ? up256(w.workspace_bytes) : 0));
-  }
+  bool planes;  // dX's sums are kept in planes of fp32
 };
-PiecePlan plan_piece(const HeadGradArgs& a, int64_t ldd, int64_t first, int64_t n, int sms) {
+PiecePlan plan_piece(const HeadGradArgs& a, const Piece& piece, int64_t pieces, int64_t ldd,
+                     int sms) {
   PiecePlan p{};
-  const Products m = products_of(a, nullptr, ldd, first, n);
-  p.logits = plan_linear(logits_of(a.loss, first, n), sms);
+  const Products m = products_of(a, nullptr, ldd, piece);
+  p.logits = plan_logits(logits_of(a.loss, piece), sms);
   // Planned as if both were wanted: a gradient's bits do not depend on which
   // others are asked for.
   plan_linear_two(m.x, m.w, sms, &p.x, &p.w);
+  // dX's sums are kept over several pieces of the vocabulary, and where few
+  // tiles of dX leave a long contraction to be cut into slices of pairs.  Measured
+  // (bf16, the whole gradient, us without and with slices): 1 x 1024 x 32768 68.4
+  // / 60.9, 100 x 1024 x 32768 79.1 / 66.0, 1024 x 2048 x 32000 288 / 265, but 300 x
+  // 256 x 10000 31.1 / 34.3, 48 x 512 x 5000 20.3 / 28.6.
+  p.planes = pieces > 1 || (!p.x.pair && piece.n >= 16384);
+  if (p.planes) p.w = plan_linear(m.w, sms);
   return p;
+}
+
+PaddedCopy copy_of_x(const HeadLossArgs& l) { return PaddedCopy{l.X, l.T, l.K, l.ldx, nullptr}; }
+PaddedCopy copy_of_w(const HeadLossArgs& l, const Piece& w) {
+  return l.w_mn ? PaddedCopy{w.p, l.K, w.n, w.ld, nullptr}
+                : PaddedCopy{w.p, w.n, l.K, w.ld, nullptr};
 }
 
 }  // namespace
@@ -314,8 +349,8 @@ HeadGradPlan plan_head_grad(const HeadGradArgs& a, int sms) {
   const HeadLossArgs& l = a.loss;
   HeadGradPlan p{};
   if (l.T == 0) {  // one launch that writes zeros
-    p.too_large = plan_linear(products_of(a, nullptr, ceil_div(l.V, 64) * 64, 0, l.V).w, sms).grid >
-                  INT32_MAX;
+    const Products m = products_of(a, nullptr, ceil_div(l.V, 64) * 64, piece_of(l, 0, l.V));
+    p.too_large = plan_linear(m.w, sms).grid > INT32_MAX;
     return p;
   }
   const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * l.T) / 256 * 256);
@@ -326,89 +361,103 @@ HeadGradPlan plan_head_grad(const HeadGradArgs& a, int sms) {
   const int64_t widest = std::min(l.V, p.piece);
   p.ldd = ceil_div(widest, 64) * 64;
   p.d_bytes = up256(l.T * p.ldd * 2);
-  p.rows_bytes = up256(l.T * static_cast<int64_t>(sizeof(HeadRow))) + up256(l.T * 4);
-  p.acc_bytes = a.dX && p.pieces > 1 ? up256(l.T * l.K * 4) : 0;
-  if (l.dtype == DT_F16)
+  if (l.dtype == DT_F16) {
+    p.rows_bytes = up256(l.T * static_cast<int64_t>(sizeof(HeadRow)));
     p.scale_bytes = kMaxCtas * 4 + 2 * up256(4 * std::max({l.T, l.K, widest}));
-  // The last piece is narrower, and may take other kernels.
-  for (int64_t first : {int64_t(0), (p.pieces - 1) * p.piece}) {
-    const PiecePlan q = plan_piece(a, p.ldd, first, std::min(p.piece, l.V - first), sms);
-    p.product_bytes = std::max(p.product_bytes, q.bytes(a));
-    p.too_large |= q.logits.grid > INT32_MAX || q.x.grid > INT32_MAX || q.w.grid > INT32_MAX;
   }
-  p.workspace_bytes = p.d_bytes + p.rows_bytes + p.acc_bytes + p.scale_bytes + p.product_bytes;
+  const Piece first = piece_of(l, 0, widest);
+  p.x_bytes = up256(padded_bytes(copy_of_x(l), 2));
+  p.w_bytes = up256(padded_bytes(copy_of_w(l, first), 2));
+  const PiecePlan q = plan_piece(a, first, p.pieces, p.ldd, sms);
+  if (q.planes && a.dX) {
+    p.dx = plan_planes(products_of(a, nullptr, p.ldd, first).x, sms);
+    p.acc_bytes = up256(p.dx.bytes);
+  }
+  p.too_large =
+      q.logits.grid > INT32_MAX || q.x.grid > INT32_MAX || q.w.grid > INT32_MAX;
+  p.workspace_bytes =
+      p.d_bytes + p.rows_bytes + p.acc_bytes + p.scale_bytes + p.x_bytes + p.w_bytes;
   return p;
 }
 
-cudaError_t launch_head_grad(const HeadGradArgs& a, const HeadGradPlan& p, void* workspace,
+cudaError_t launch_head_grad(const HeadGradArgs& args, const HeadGradPlan& p, void* workspace,
                              int sms, cudaStream_t stream) {
-  const HeadLossArgs& l = a.loss;
+  HeadGradArgs a = args;
+  HeadLossArgs& l = a.loss;
   if (l.T == 0) {
-    const Products m = products_of(a, nullptr, ceil_div(l.V, 64) * 64, 0, l.V);
+    const Products m = products_of(a, nullptr, ceil_div(l.V, 64) * 64, piece_of(l, 0, l.V));
     return launch_linear(m.w, plan_linear(m.w, sms), nullptr, stream);  // a sum of nothing
   }
   char* ws = static_cast<char*>(workspace);
   void* const D = ws;
-  HeadRow* const rows = reinterpret_cast<HeadRow*>(ws + p.d_bytes);
-  int* const column = reinterpret_cast<int*>(
-      ws + p.d_bytes + up256(l.T * static_cast<int64_t>(sizeof(HeadRow))));
+  HeadRow* const rows = p.rows_bytes ? reinterpret_cast<HeadRow*>(ws + p.d_bytes) : nullptr;
   float* const acc = reinterpret_cast<float*>(ws + p.d_bytes + p.rows_bytes);
   char* const scales = ws + p.d_bytes + p.rows_bytes + p.acc_bytes;
-  char* const products = scales + p.scale_bytes;
-  RowArgs r{l.T, l.V, a.dloss, a.lse, l.target, l.ignore_index, l.smoothing, l.z_loss, rows,
-            column, nullptr, nullptr, nullptr, 0, l.bounds};
-  int ctas = 0;
+  char* const x_copy = scales + p.scale_bytes;
+  char* const w_copy = x_copy + p.x_bytes;
+  const HeadSource source{a.dloss, a.lse, l.target, l.ignore_index, l.smoothing, l.z_loss,
+                          static_cast<int>(l.V)};
+  RowArgs r{l.T, source, rows, nullptr, nullptr, nullptr, 0, l.bounds};
   cudaError_t e = cudaSuccess;
   if (p.scale_bytes) {
     r.n = std::max({l.T, l.K, std::min(l.V, p.piece)});
     r.amax = reinterpret_cast<float*>(scales);
     r.undo = reinterpret_cast<float*>(scales + kMaxCtas * 4);
     r.ones = r.undo + up256(4 * r.n) / 4;
-    ctas = static_cast<int>(std::min<int64_t>(kMaxCtas, ceil_div(l.T, kRowThreads)));
+    const int ctas = static_cast<int>(std::min<int64_t>(kMaxCtas, ceil_div(l.T, kRowThreads)));
     e = launch_dependent(size_kernel, static_cast<unsigned>(ctas), kRowThreads, stream, r);
+    const int64_t most = 8 * static_cast<int64_t>(sms);
+    if (e == cudaSuccess)
+      e = launch_dependent(
+          rows_kernel,
+          static_cast<unsigned>(std::min(most, ceil_div(std::max(l.T, r.n), kRowThreads))),
+          kRowThreads, stream, r, ctas);
   }
-  if (e == cudaSuccess)
-    e = launch_dependent(
-        rows_kernel,
-        static_cast<unsigned>(std::min<int64_t>(8 * static_cast<int64_t>(sms),
-                                                ceil_div(std::max(l.T, r.n), kRowThreads))),
-        kRowThreads, stream, r, ctas);
   for (int64_t i = 0; i < p.pieces && e == cudaSuccess; ++i) {
-    const int64_t first = i * p.piece, n = std::min(p.piece, l.V - first);
-    const PiecePlan q = plan_piece(a, p.ldd, first, n, sms);
-    const HeadGrad grad{static_cast<int>(l.T), static_cast<int>(n), rows, column,
-                        static_cast<int>(first), D, p.ldd, l.dtype, l.bounds};
-    e = launch_head(logits_of(l, first, n), q.logits, products, grad, stream);
+    Piece piece = piece_of(l, i * p.piece, std::min(p.piece, l.V - i * p.piece));
+    PaddedCopy cx = copy_of_x(l), cw = copy_of_w(l, piece);
+    cx.dst = i == 0 && p.x_bytes ? x_copy : nullptr;
+    cw.dst = p.w_bytes ? w_copy : nullptr;
+    e = launch_padded_copies({&cx, &cw}, 2, l.bounds, stream);
     if (e != cudaSuccess) break;
-    Products m = products_of(a, D, p.ldd, first, n);
-    m.x.row_scale = m.w.row_scale = r.undo;
+    l.X = cx.p;
+    l.ldx = cx.ld;
+    piece.p = cw.p;
+    piece.ld = cw.ld;
+    const PiecePlan q = plan_piece(a, piece, p.pieces, p.ldd, sms);
+    const HeadGrad grad{{}, static_cast<int>(l.T), static_cast<int>(piece.n), rows, source,
+                        static_cast<int>(piece.first), D, p.ldd, l.dtype, l.bounds};
+    e = launch_head(logits_of(l, piece), q.logits, nullptr, grad, stream);
+    if (e != cudaSuccess) break;
+    Products m = products_of(a, D, p.ldd, piece);
+    m.x.row_scale = m.w.row_scale = m.x.scale = m.w.scale = r.undo;
     m.x.col_scale = m.w.col_scale = r.ones;
-    if (p.acc_bytes) {
-      m.x.out_dtype = DT_F32;
-      m.x.Y = acc;
-      m.x.ldy = l.K;
-      m.x.residual = i > 0 ? acc : nullptr;
-      m.x.ldr = l.K;
+    m.x.plain = m.w.plain = 1;
+    if (a.dX && q.planes) {
+      e = launch_linear_planes(m.x, p.dx, acc, i > 0, sms, stream);
+      if (e == cudaSuccess && a.dW) e = launch_linear(m.w, q.w, nullptr, stream);
+    } else if (a.dX && a.dW) {
+      e = launch_linear_two(m.x, q.x, nullptr, m.w, q.w, nullptr, stream);
+    } else {
+      e = a.dX ? launch_linear(m.x, q.x, nullptr, stream)
+               : launch_linear(m.w, q.w, nullptr, stream);
     }
-    char* const wx = products;
-    char* const ww = products + (a.dX ? up256(q.x.workspace_bytes) : 0);
-    if (a.dX && a.dW) e = launch_linear_two(m.x, q.x, wx, m.w, q.w, ww, stream);
-    else if (a.dX) e = launch_linear(m.x, q.x, wx, stream);
-    else e = launch_linear(m.w, q.w, ww, stream);
   }
-  if (e != cudaSuccess || !p.acc_bytes) return e;
-  const Matrix<const float> from{acc, l.K, l.T * l.K, l.bounds};
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(l.T, 16 * sms));
+  if (e != cudaSuccess || !a.dX || !p.acc_bytes) return e;
+  const int64_t plane = p.dx.rows * p.dx.pitch, all = p.dx.planes * plane;
+  const unsigned grid = static_cast<unsigned>(
+      std::min<int64_t>(16 * static_cast<int64_t>(sms), ceil_div(l.T * p.dx.pitch / 4, kRowThreads)));
   const int64_t extent = view_extent(l.T, l.K, a.lddx);
   const int cols = static_cast<int>(l.K);
-  if (l.dtype == DT_F16)
-    return launch_dependent(
-        round_rows_kernel<__half>, grid, kRowThreads, stream, from,
-        Matrix<__half>{static_cast<__half*>(a.dX), a.lddx, extent, l.bounds}, l.T, cols);
-  return launch_dependent(
-      round_rows_kernel<__nv_bfloat16>, grid, kRowThreads, stream, from,
-      Matrix<__nv_bfloat16>{static_cast<__nv_bfloat16*>(a.dX), a.lddx, extent, l.bounds}, l.T,
-      cols);
+  auto go = [&](auto* kernel, auto* to) {
+    using V = std::remove_pointer_t<decltype(to)>;
+    return launch_dependent(kernel, grid, kRowThreads, stream, static_cast<const float*>(acc),
+                            p.dx.planes, plane, p.dx.pitch, all,
+                            Matrix<V>{to, a.lddx, extent, l.bounds}, l.T, cols);
+  };
+  return l.dtype == DT_F16 ? go(round_planes_kernel<__half>, static_cast<__half*>(a.dX))
+                           : go(round_planes_kernel<__nv_bfloat16>,
+                                static_cast<__nv_bfloat16*>(a.dX));
 }
 
 }  // namespace mt

@@ -9,6 +9,7 @@
 
 #include "gemm_f16.cuh"
 #include "head.cuh"
+#include "store_box.cuh"
 
 namespace mt {
 namespace head {
@@ -26,7 +27,7 @@ __device__ __forceinline__ uint32_t hot_of(int at) {
 
 struct StatsDrain {
   static constexpr bool DEPENDENT_LAUNCH = true;
-  static constexpr int WARPS = 8;
+  static constexpr int WARPS = 8, STORE_BYTES = 0;
   HeadStats ep;
 
   __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int half,
@@ -74,54 +75,47 @@ struct StatsDrain {
 
 struct GradDrain {
   static constexpr bool DEPENDENT_LAUNCH = true;
-  static constexpr int WARPS = 8;
+  static constexpr int WARPS = 8, STORE_BYTES = WARPS * STORE_BOX_BYTES;
   HeadGrad ep;
 
   template <class T>
   __device__ __forceinline__ void typed(uint32_t t_row, const Unit& w, int q, int half, int lane,
-                                        int rank) const {
-    const int t = w.tm * PAIR_TILE + rank * PAIR_HALF + q * 32 + lane;
+                                        uint8_t* box, int rank) const {
+    const int t0 = w.tm * PAIR_TILE + rank * PAIR_HALF + q * 32, t = t0 + lane;
     const int c0 = w.tn * PAIR_TILE + half * PAIR_SLOT;
-    const bool live = t < ep.T && ep.row_ok(t);
-    const HeadRow r = live ? ep.rows[t] : HeadRow{0.0f, 0.0f, 0.0f, 0.0f};
-    const int hit = live ? ep.target[t] : HeadGrad::DEAD;
-    const int target = hit - ep.first - c0;
-    T* const to = static_cast<T*>(ep.D) + t * ep.ldd + c0;
+    const HeadRow r = ep.row(t, ep.T);
+    const int hit = r.target;
+    const int target = hit - ep.first - c0;  // negative without one
+    constexpr int PER = 64 / CHUNK;          // chunks of a box
 #pragma unroll 1
-    for (int ch = 0; ch < CHUNKS; ++ch) {
-      const int c = ch * CHUNK;
-      float v[CHUNK];
-      __syncwarp();
-      tmem_ld32(t_row + half * PAIR_SLOT + c, v);
-      if (!live) continue;
+    for (int c = 0; c < PAIR_SLOT; c += 64) {
+      store_begin(lane);
 #pragma unroll
-      for (int i = 0; i < CHUNK; ++i)
-        v[i] = hit == HeadGrad::DEAD
-                   ? 0.0f
-                   : fmaf(exp2_approx(fmaf(v[i], LOG2E, -r.x)), r.p, -r.all);
-      if (const uint32_t hot = hot_of(target - c)) {
+      for (int i = 0; i < PER; ++i) {
+        float v[CHUNK];
+        __syncwarp();
+        tmem_ld32(t_row + half * PAIR_SLOT + c + i * CHUNK, v);
 #pragma unroll
-        for (int i = 0; i < CHUNK; ++i) v[i] -= hot >> i & 1u ? r.hit : 0.0f;
+        for (int k = 0; k < CHUNK; ++k)
+          v[k] = hit == HeadRow::DEAD
+                     ? 0.0f
+                     : fmaf(exp2_approx(fmaf(v[k], LOG2E, -r.x)), r.p, -r.all);
+        if (const uint32_t hot = hot_of(target - c - i * CHUNK)) {
+#pragma unroll
+          for (int k = 0; k < CHUNK; ++k) v[k] -= hot >> k & 1u ? r.hit : 0.0f;
+        }
+        store_fill<T>(box, lane, i * CHUNK, v);
       }
-#pragma unroll
-      for (int g = 0; g < CHUNK; g += 8) {
-        if (c0 + c + g >= ep.C ||
-            !bounds_ok(ep.bounds, SITE_C_STORE, t * ep.ldd + c0 + c + g, 8, ep.T * ep.ldd))
-          continue;
-        float part[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) part[i] = v[g + i];
-        row::Pack8<T> o;
-        o.set(part);
-        *reinterpret_cast<row::Pack8<T>*>(to + c + g) = o;
-      }
+      store_end(&ep.map, box, lane, c0 + c, t0, c0 + c < ep.C && t0 < ep.T, false);
     }
   }
 
   __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int half,
-                                             int lane, const Sched&, float*, int rank) const {
-    if (ep.dtype == DT_F16) typed<__half>(t_row, w, q, half, lane, rank);
-    else typed<__nv_bfloat16>(t_row, w, q, half, lane, rank);
+                                             int lane, const Sched&, float* square,
+                                             int rank) const {
+    uint8_t* const box = store_staging<GradDrain>(square, q, half);
+    if (ep.dtype == DT_F16) typed<__half>(t_row, w, q, half, lane, box, rank);
+    else typed<__nv_bfloat16>(t_row, w, q, half, lane, box, rank);
   }
 };
 
@@ -130,7 +124,6 @@ using DrainOf = typename std::conditional<std::is_same<Ep, HeadStats>::value, St
                                           GradDrain>::type;
 
 constexpr int ACC_BUFS = 2;
-using Geometry = PairGeometry<ACC_BUFS>;
 
 template <class Drain>
 const void* kernel_for(bool w_mn) {
@@ -144,7 +137,7 @@ using namespace head;
 
 template <class Ep>
 cudaError_t launch_head_pair(const CUtensorMap& map_x, const CUtensorMap& map_w, uint32_t idesc,
-                             const Ep& ep, bool w_mn, int smem, int kt, int clusters,
+                             const Ep& ep, bool w_mn, int kt, int clusters,
                              int fault_inject, cudaStream_t stream) {
   using Drain = DrainOf<Ep>;
   Drain drain{ep};
@@ -155,12 +148,12 @@ cudaError_t launch_head_pair(const CUtensorMap& map_x, const CUtensorMap& map_w,
   void* args[] = {&x,       &w,       &idesc, &drain, &kt,
                   &tiles_t, &tiles_c, &group, &sched, &fault_inject};
   return launch_dependent(kernel_for<Drain>(w_mn), dim3(2 * static_cast<unsigned>(clusters)),
-                          pair_threads<Drain>(), smem, 2, stream, args);
+                          pair_threads<Drain>(), pair_smem<Drain, ACC_BUFS>(), 2, stream, args);
 }
 template cudaError_t launch_head_pair(const CUtensorMap&, const CUtensorMap&, uint32_t,
-                                      const HeadStats&, bool, int, int, int, int, cudaStream_t);
+                                      const HeadStats&, bool, int, int, int, cudaStream_t);
 template cudaError_t launch_head_pair(const CUtensorMap&, const CUtensorMap&, uint32_t,
-                                      const HeadGrad&, bool, int, int, int, int, cudaStream_t);
+                                      const HeadGrad&, bool, int, int, int, cudaStream_t);
 
 cudaError_t head_prepare() {
   cudaError_t r = cudaSuccess;
@@ -172,8 +165,8 @@ cudaError_t head_prepare() {
                                cudaSharedmemCarveoutMaxShared);
   };
   for (bool w_mn : {false, true}) {
-    prepare(kernel_for<StatsDrain>(w_mn), Geometry::SMEM_BYTES - EPI_STAGE_BYTES);
-    prepare(kernel_for<GradDrain>(w_mn), Geometry::SMEM_BYTES - EPI_STAGE_BYTES);
+    prepare(kernel_for<StatsDrain>(w_mn), pair_smem<StatsDrain, ACC_BUFS>());
+    prepare(kernel_for<GradDrain>(w_mn), pair_smem<GradDrain, ACC_BUFS>());
   }
   for (int bt : {16, 32, 64, 128}) {
     const linear::LinearKernel s = head_split_kernel_for<HeadStats>(bt);

@@ -113,7 +113,22 @@ struct LinearArgs {
   int out_dtype;  // Y, Z, residual: DT_F16, DT_BF16 or DT_F32
   int act;
   BoundsRecord* bounds;
+  // A product of 16-bit operands and no more: Y = scale * X * W (scale: one value
+  // on the device, null: 1).  No bias, activation, scales, residual or Z.
+  int plain = 0;
+  const float* scale = nullptr;
 };
+
+// A plain product whose contraction is cut into slices, each with a plane of
+// sums of its own: plane s, rows s * rows .. of `sums` (fp32, pitch a multiple of
+// 4, `rows` T rounded up to whole tiles), is written, or with `add` added to.
+struct PlanesPlan {
+  int planes, kt_per_slice;
+  int64_t rows, pitch, bytes;
+};
+PlanesPlan plan_planes(const LinearArgs& a, int sms);
+cudaError_t launch_linear_planes(const LinearArgs& a, const PlanesPlan& p, float* sums, bool add,
+                                 int sms, cudaStream_t stream);
 
 // What a product launches.  pair: CTA pairs on tiles of 256 columns x 256
 // rows of Y (linear_pair.cu); else CTA tiles of bc = 128 columns x bt rows,
@@ -129,6 +144,8 @@ struct LinearPlan {
 };
 
 LinearPlan plan_linear(const LinearArgs& a, int sms);
+// The same with pairs from `sevenths` sevenths of a pair on.
+LinearPlan plan_linear(const LinearArgs& a, int sms, int sevenths);
 // Two products that do not depend on one another: planned for one launch when
 // both take the split kernel.
 void plan_linear_two(const LinearArgs& a, const LinearArgs& b, int sms, LinearPlan* pa,
@@ -145,6 +162,19 @@ cudaError_t linear_read_and_clear_status(unsigned int* status);
 // Whether TMA reads a matrix of `elem`-byte values in place: 16-byte aligned
 // base, row pitch a multiple of 16 bytes.
 bool tma_readable(const void* p, int64_t ld, int elem);
+
+// A stored matrix of `elem`-byte values and where its padded copy goes (dst null:
+// nowhere), for operands that several products read: TMA reads the copy in
+// place.  padded_bytes: the copy's size, 0 where TMA reads the matrix itself.
+struct PaddedCopy {
+  const void* p;
+  int64_t rows, cols, ld;
+  void* dst;
+};
+int64_t padded_bytes(const PaddedCopy& c, int elem);
+// Copies up to two (null: none) in one launch; p and ld become the copies'.
+cudaError_t launch_padded_copies(PaddedCopy* const (&copies)[2], int elem, BoundsRecord* bounds,
+                                 cudaStream_t stream);
 
 // linear_grad.cu: dz = dY * act'(Z) rounded to `dtype` (dZ null: not written;
 // else 16-byte aligned rows of lddz >= N values, lddz a multiple of 8, whose

@@ -2,6 +2,7 @@
 // read in place, the choice of kernel and its launch.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -175,7 +176,9 @@ bool tma_readable(const void* p, int64_t ld, int elem) {
          ld * elem < (int64_t(1) << 39);
 }
 
-LinearPlan plan_linear(const LinearArgs& a, int sms) {
+LinearPlan plan_linear(const LinearArgs& a, int sms) { return plan_linear(a, sms, 2 * sms); }
+
+LinearPlan plan_linear(const LinearArgs& a, int sms, int sevenths) {
   LinearPlan p{};
   const int elem = dtype_bytes(a.dtype);
   const int64_t pairs = ceil_div(a.C, kPair) * ceil_div(a.T, kPair);
@@ -185,7 +188,7 @@ LinearPlan plan_linear(const LinearArgs& a, int sms) {
   // split kernel): 512 tokens (32 pairs) 32.0 / 28.0, 768 (48) 33.1 / 38.5,
   // 1024 (64) 33.2 / 39.0, 2048 (128) 55.1 / 74.7; e4m3 512 tokens 23.9 / 21.5,
   // 768 25.2 / 27.1, 2048 38.8 / 52.4.
-  p.pair = a.K > 0 && sms >= 2 && 7 * pairs >= 2 * sms && a.T > 128 &&
+  p.pair = a.K > 0 && sms >= 2 && 7 * pairs >= sevenths && a.T > 128 &&
            pairs <= INT32_MAX / 8;
   if (p.pair) {
     const LinearKernel k = linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn);
@@ -260,6 +263,7 @@ cudaError_t linear_prepare() {
     for (int mn = 0; mn < 4; ++mn)
       if (r == cudaSuccess) r = prepare(linear_pair_kernel_for(dtype, mn & 1, mn >> 1));
   }
+  if (r == cudaSuccess) r = linear_rows_prepare();
   return r == cudaSuccess ? head_prepare() : r;
 }
 
@@ -327,6 +331,51 @@ cudaError_t launch_split(const LinearPlan& p, const LinearKernel& k, int64_t gri
 
 }  // namespace
 
+namespace {
+
+// The map of a result that is written by boxes of 32 rows x 128 bytes; false
+// where TMA cannot write it.
+bool encode_boxes(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t cols,
+                  int64_t ld) {
+  const CUtensorMapDataType t = dtype == DT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : dtype == DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int elem = dtype_bytes(dtype);
+  return tma_readable(p, ld, elem) &&
+         encode_tensor_map_2d(map, t, elem, p, rows, cols, ld, 128 / elem, 32,
+                              CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool encode_result(CUtensorMap* map, const LinearArgs& a) {
+  return encode_boxes(map, a.out_dtype, a.Y, a.T, a.C, a.ldy);
+}
+
+// The MMA of pairs whose M side are the rows.
+uint32_t pair_rows_idesc(const LinearArgs& a) {
+  const uint32_t fmt = a.dtype == DT_BF16 ? 1u : 0u;
+  return tc::instr_desc(kPair, kPair, fmt, fmt, a.x_mn ? 1u : 0u, a.w_mn ? 1u : 0u);
+}
+
+}  // namespace
+
+int64_t padded_bytes(const PaddedCopy& c, int elem) {
+  return copy_bytes(Stored{c.p, c.rows, c.cols, c.ld}, elem);
+}
+
+cudaError_t launch_padded_copies(PaddedCopy* const (&copies)[2], int elem, BoundsRecord* bounds,
+                                 cudaStream_t stream) {
+  CopyJobs jobs{};
+  jobs.rec = bounds;
+  for (PaddedCopy* c : copies) {
+    if (!c || !c->dst) continue;
+    Stored m{c->p, c->rows, c->cols, c->ld};
+    jobs.job[jobs.count] = copy_job(&m, elem, c->dst, jobs.blocks);
+    jobs.blocks += jobs.job[jobs.count++].blocks;
+    c->p = m.p;
+    c->ld = m.ld;
+  }
+  return launch_copies(&jobs, stream);
+}
+
 cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* workspace,
                           cudaStream_t stream, int fault_inject) {
   Ready r{};
@@ -334,6 +383,11 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* worksp
   cudaError_t e = make_ready(a, p, workspace, &jobs, &r);
   if (e == cudaSuccess) e = launch_copies(&jobs, stream);
   if (e != cudaSuccess) return e;
+  CUtensorMap map_y;
+  if (p.pair && a.plain && encode_result(&map_y, a))
+    return launch_linear_rows(a, r.map_x, r.map_w, map_y, pair_rows_idesc(a),
+                              static_cast<int>(ktiles_of(a)), nullptr, false,
+                              static_cast<int>(p.grid / 2), stream);
   if (p.pair)
     return launch_linear_pair(linear_pair_kernel_for(a.dtype, a.w_mn, a.x_mn), r.map_w, r.map_x,
                               r.idesc, r.ep, static_cast<int>(ktiles_of(a)),
@@ -345,6 +399,39 @@ cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& p, void* worksp
                       stream);
 }
 
+// Slices of at least eight K tiles, as many as find pairs of SMs beside each
+// other.
+PlanesPlan plan_planes(const LinearArgs& a, int sms) {
+  PlanesPlan p{};
+  const int64_t tiles = ceil_div(a.T, kPair) * ceil_div(a.C, kPair), kt = ktiles_of(a);
+  const int64_t want = std::min<int64_t>(sms / 2 / std::max<int64_t>(1, tiles), kt / 8);
+  p.planes = static_cast<int>(std::max<int64_t>(1, want));
+  p.kt_per_slice = static_cast<int>(ceil_div(kt, p.planes));
+  p.planes = static_cast<int>(ceil_div(kt, p.kt_per_slice));
+  p.rows = ceil_div(a.T, kPair) * kPair;
+  p.pitch = ceil_div(a.C, 4) * 4;
+  p.bytes = p.planes * p.rows * p.pitch * 4;
+  return p;
+}
+
+cudaError_t launch_linear_planes(const LinearArgs& a, const PlanesPlan& p, float* sums, bool add,
+                                 int sms, cudaStream_t stream) {
+  Ready r{};
+  CopyJobs jobs{};
+  LinearPlan pairs{};
+  pairs.pair = 1;
+  CUtensorMap map_y;
+  cudaError_t e = make_ready(a, pairs, nullptr, &jobs, &r);
+  if (e == cudaSuccess &&
+      !encode_boxes(&map_y, DT_F32, sums, p.planes * p.rows, a.C, p.pitch))
+    e = cudaErrorInvalidValue;
+  if (e != cudaSuccess) return e;
+  const int64_t units = ceil_div(a.T, kPair) * ceil_div(a.C, kPair) * p.planes;
+  return launch_linear_rows(a, r.map_x, r.map_w, map_y, pair_rows_idesc(a),
+                            static_cast<int>(ktiles_of(a)), &p, add,
+                            static_cast<int>(std::min<int64_t>(units, sms / 2)), stream);
+}
+
 template <class Ep>
 cudaError_t launch_head(const LinearArgs& a, const LinearPlan& p, void* workspace, const Ep& ep,
                         cudaStream_t stream, int fault_inject) {
@@ -354,12 +441,13 @@ cudaError_t launch_head(const LinearArgs& a, const LinearPlan& p, void* workspac
   if (e == cudaSuccess) e = launch_copies(&jobs, stream);
   if (e != cudaSuccess) return e;
   if (p.pair) {
-    // The tokens are the MMA's M side here.
-    const uint32_t fmt = a.dtype == DT_BF16 ? 1u : 0u;
-    const uint32_t idesc = tc::instr_desc(kPair, kPair, fmt, fmt, 0u, a.w_mn ? 1u : 0u);
-    return launch_head_pair(r.map_x, r.map_w, idesc, ep, a.w_mn != 0,
-                            static_cast<int>(p.smem_bytes), static_cast<int>(ktiles_of(a)),
-                            static_cast<int>(p.grid / 2), fault_inject, stream);
+    Ep with = ep;
+    if constexpr (std::is_same<Ep, head::HeadGrad>::value)
+      if (!encode_boxes(&with.map, ep.dtype, ep.D, ep.T, ep.C, ep.ldd))
+        return cudaErrorInvalidValue;
+    return launch_head_pair(r.map_x, r.map_w, pair_rows_idesc(a), with, a.w_mn != 0,
+                            static_cast<int>(ktiles_of(a)), static_cast<int>(p.grid / 2),
+                            fault_inject, stream);
   }
   SplitProblemsOf<Ep> problems{};
   problems.p[0] = problem_of(a, p, r, ep, 0);
@@ -401,12 +489,13 @@ cudaError_t launch_linear_two(const LinearArgs& a, const LinearPlan& pa, void* w
 }
 
 cudaError_t linear_read_and_clear_status(unsigned int* status) {
-  unsigned int split = 0, pair = 0, head_split = 0, head_pair = 0;
+  unsigned int split = 0, pair = 0, rows = 0, head_split = 0, head_pair = 0;
   cudaError_t e = linear_split_read_and_clear_status(&split);
   if (e == cudaSuccess) e = linear_pair_read_and_clear_status(&pair);
+  if (e == cudaSuccess) e = linear_rows_read_and_clear_status(&rows);
   if (e == cudaSuccess) e = head_split_read_and_clear_status(&head_split);
   if (e == cudaSuccess) e = head_pair_read_and_clear_status(&head_pair);
-  *status = split | pair | head_split | head_pair;
+  *status = split | pair | rows | head_split | head_pair;
   return e;
 }
 

@@ -307,5 +307,12 @@ cudaError_t launch_linear_pair(const linear::LinearKernel& k, const CUtensorMap&
                                const linear::LinearEpilogue& ep, int kt, int clusters,
                                int fault_inject, cudaStream_t stream);
 cudaError_t linear_pair_read_and_clear_status(unsigned int* status);
+// linear_rows.cu: plain products whose Y TMA writes, on pairs.
+cudaError_t linear_rows_prepare();
+cudaError_t launch_linear_rows(const LinearArgs& a, const CUtensorMap& map_x,
+                               const CUtensorMap& map_w, const CUtensorMap& map_y,
+                               uint32_t idesc, int kt, const PlanesPlan* planes, bool add,
+                               int clusters, cudaStream_t stream);
+cudaError_t linear_rows_read_and_clear_status(unsigned int* status);
 
 }  // namespace mt

@@ -21,7 +21,7 @@ using namespace f16tc;
 // a column block.
 struct PairDrain {
   static constexpr bool DEPENDENT_LAUNCH = true;
-  static constexpr int WARPS = 8;
+  static constexpr int WARPS = 8, STORE_BYTES = 0;
   LinearEpilogue ep;
   __device__ __forceinline__ void operator()(uint32_t t_row, const Unit& w, int q, int half,
                                              int lane, const Sched&, float*, int rank) const {

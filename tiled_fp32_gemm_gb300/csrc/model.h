@@ -127,7 +127,8 @@ struct HeadGradPlan {
   int64_t piece;   // columns of the vocabulary at a time, a multiple of 256
   int64_t pieces;
   int64_t ldd;     // row pitch of a piece of D
-  int64_t d_bytes, rows_bytes, acc_bytes, scale_bytes, product_bytes, workspace_bytes;
+  int64_t d_bytes, rows_bytes, acc_bytes, scale_bytes, x_bytes, w_bytes, workspace_bytes;
+  PlanesPlan dx;   // dX's sums, where they are kept (acc_bytes)
   bool too_large;  // a grid past 2^31 - 1
 };
 HeadGradPlan plan_head_grad(const HeadGradArgs& a, int sms);
