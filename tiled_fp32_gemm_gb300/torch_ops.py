@@ -1,15 +1,17 @@
-"""Torch operator registrations for the library's products and the
-feed-forward operators.
+"""Torch operator registrations for the library's products, the feed-forward
+operators, the residual joins and the vocabulary's loss.
 
 Importing this module registers ``torch.ops.mt.sgemm(a, b)``,
-``torch.ops.mt.gemm_bias(a, b, bias)``, ``torch.ops.mt.linear`` and
-``torch.ops.mt.rms_norm`` as torch custom operators: the same C-ABI calls as
-``sgemm``, ``gemm(..., bias=...)``, ``linear`` and ``rms_norm``, visible to
-torch's dispatcher, graph capture and tracing (each has a shape-only fake
-implementation, so tracing needs no GPU).  ``linear`` and ``rms_norm`` are
-differentiable, once: their gradients are ``linear_backward`` and
-``rms_norm_backward``, which have none themselves, so a second derivative
-raises.  Marshalling only: the work runs in the library's
+``torch.ops.mt.gemm_bias(a, b, bias)``, ``torch.ops.mt.linear``,
+``torch.ops.mt.rms_norm``, ``torch.ops.mt.layer_norm``, ``torch.ops.mt.dropout``
+and ``torch.ops.mt.linear_cross_entropy`` as torch custom operators: the same
+C-ABI calls as the functions of those names (``gemm(..., bias=...)``), visible
+to torch's dispatcher, graph capture and tracing (each has a shape-only fake
+implementation, so tracing needs no GPU).  All but the first two are
+differentiable, once: their gradients are the ``*_backward`` functions (for
+dropout, dropout itself), which have none themselves, so a second derivative
+raises.  A seed that is advanced in place between an operator and its gradient
+raises too: torch notices it.  Marshalling only: the work runs in the library's
 kernels.
 """
 from __future__ import annotations
@@ -19,7 +21,9 @@ from typing import Optional, Tuple
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import gemm, linear, linear_backward, rms_norm, rms_norm_backward, sgemm
+from . import (dropout, gemm, layer_norm, layer_norm_backward, linear, linear_backward,
+               linear_cross_entropy, linear_cross_entropy_backward, rms_norm, rms_norm_backward,
+               sgemm)
 
 
 @torch.library.custom_op("mt::sgemm", mutates_args=())
@@ -133,3 +137,126 @@ def _rms_norm_grad(ctx, dy, dh, _):
 
 
 rms_norm_op.register_autograd(_rms_norm_grad, setup_context=_rms_norm_setup)
+
+
+@torch.library.custom_op("mt::layer_norm", mutates_args=())
+def layer_norm_op(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor,
+                  residual: Optional[torch.Tensor], eps: float, dropout: float,
+                  seed: Optional[torch.Tensor], sequence: int
+                  ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(y, h, mean, rstd) of the layer norm of h = drop(x) + residual through
+    mt_layer_norm; where nothing is dropped or added h is empty (it is x)."""
+    y, h, mean, rstd = layer_norm(x, weight, bias, residual=residual, eps=eps, dropout=dropout,
+                                  seed=seed, sequence=sequence)
+    return y, x.new_empty((0,)) if h is x else h, mean, rstd
+
+
+@layer_norm_op.register_fake
+def _layer_norm_fake(x, weight, bias, residual, eps, dropout, seed, sequence):
+    torch._check(x.dim() == 2 and weight.dim() == 1 and weight.shape[0] == x.shape[1]
+                 and bias.shape == weight.shape,
+                 lambda: "mt::layer_norm needs rows x d, a weight and a bias of d values")
+    joined = residual is not None or dropout > 0.0
+    stats = [x.new_empty((x.shape[0],), dtype=torch.float32) for _ in range(2)]
+    return (x.new_empty(tuple(x.shape)),
+            x.new_empty(tuple(x.shape)) if joined else x.new_empty((0,)), *stats)
+
+
+def _layer_norm_setup(ctx, inputs, output):
+    x, weight, _, residual, _, p, seed, sequence = inputs
+    _, h, mean, rstd = output
+    ctx.joined = residual is not None or p > 0.0
+    ctx.save_for_backward(h if ctx.joined else x, weight, mean, rstd, seed if p > 0.0 else None)
+    ctx.options = p, sequence
+    ctx.has_residual = residual is not None
+    ctx.mark_non_differentiable(mean, rstd)
+
+
+@once_differentiable
+def _layer_norm_grad(ctx, dy, dh, *_):
+    h, weight, mean, rstd, seed = ctx.saved_tensors
+    p, sequence = ctx.options
+    dx, dres, dweight, dbias = layer_norm_backward(
+        dy.contiguous(), h, weight, mean, rstd,
+        dh=dh.contiguous() if ctx.joined and dh is not None else None, dropout=p, seed=seed,
+        sequence=sequence, need_weight=ctx.needs_input_grad[1], need_bias=ctx.needs_input_grad[2])
+    if dweight is not None:
+        dweight = dweight.to(weight.dtype)
+    if dbias is not None:
+        dbias = dbias.to(weight.dtype)
+    return dx, dweight, dbias, dres if ctx.has_residual else None, None, None, None, None
+
+
+layer_norm_op.register_autograd(_layer_norm_grad, setup_context=_layer_norm_setup)
+
+
+@torch.library.custom_op("mt::dropout", mutates_args=())
+def dropout_op(x: torch.Tensor, p: float, seed: torch.Tensor, sequence: int,
+               residual: Optional[torch.Tensor]) -> torch.Tensor:
+    """drop(x) + residual through mt_dropout."""
+    return dropout(x, p, seed, sequence=sequence, residual=residual)
+
+
+@dropout_op.register_fake
+def _dropout_fake(x, p, seed, sequence, residual):
+    torch._check(x.dim() == 2, lambda: "mt::dropout needs rows x d")
+    return x.new_empty(tuple(x.shape))
+
+
+def _dropout_setup(ctx, inputs, output):
+    _, p, seed, sequence, residual = inputs
+    ctx.save_for_backward(seed)
+    ctx.options = p, sequence
+    ctx.has_residual = residual is not None
+
+
+@once_differentiable
+def _dropout_grad(ctx, dy):
+    seed, = ctx.saved_tensors
+    p, sequence = ctx.options
+    dx = dropout(dy.contiguous(), p, seed, sequence=sequence) if ctx.needs_input_grad[0] else None
+    return dx, None, None, None, dy if ctx.has_residual else None
+
+
+dropout_op.register_autograd(_dropout_grad, setup_context=_dropout_setup)
+
+
+@torch.library.custom_op("mt::linear_cross_entropy", mutates_args=())
+def linear_cross_entropy_op(a: torch.Tensor, b: torch.Tensor, target: torch.Tensor,
+                            trans_b: bool, ignore_index: int, label_smoothing: float,
+                            z_loss: float) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(loss, lse) per token through mt_linear_cross_entropy; lse is not
+    differentiable."""
+    return linear_cross_entropy(a, b, target, trans_b=trans_b, ignore_index=ignore_index,
+                                label_smoothing=label_smoothing, z_loss=z_loss)
+
+
+@linear_cross_entropy_op.register_fake
+def _linear_cross_entropy_fake(a, b, target, trans_b, ignore_index, label_smoothing, z_loss):
+    k = b.shape[1] if trans_b else b.shape[0]
+    torch._check(a.dim() == 2 and b.dim() == 2 and a.shape[1] == k
+                 and target.shape == (a.shape[0],),
+                 lambda: "mt::linear_cross_entropy needs (T, K), a weight of K x V (V x K with "
+                         "trans_b) and T targets")
+    return tuple(a.new_empty((a.shape[0],), dtype=torch.float32) for _ in range(2))
+
+
+def _linear_cross_entropy_setup(ctx, inputs, output):
+    a, b, target, trans_b, ignore_index, label_smoothing, z_loss = inputs
+    ctx.save_for_backward(a, b, target, output[1])
+    ctx.options = dict(trans_b=trans_b, ignore_index=ignore_index,
+                       label_smoothing=label_smoothing, z_loss=z_loss)
+    ctx.mark_non_differentiable(output[1])
+
+
+@once_differentiable
+def _linear_cross_entropy_grad(ctx, dloss, _):
+    a, b, target, lse = ctx.saved_tensors
+    da, db = linear_cross_entropy_backward(dloss.contiguous(), a, b, target, lse,
+                                           need_a=ctx.needs_input_grad[0],
+                                           need_b=ctx.needs_input_grad[1], **ctx.options)
+    return da, db, None, None, None, None, None
+
+
+linear_cross_entropy_op.register_autograd(_linear_cross_entropy_grad,
+                                          setup_context=_linear_cross_entropy_setup)
