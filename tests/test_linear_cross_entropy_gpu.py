@@ -272,7 +272,8 @@ def test_one_gradient_alone_has_the_same_bits(T, K, V, need):
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("trans", [True, False])
-@pytest.mark.parametrize("T,K,V", [(4096, 40, 40000), (8192, 64, 33001)])
+@pytest.mark.parametrize("T,K,V", [(4096, 40, 40000), (8192, 64, 33001), (16384, 40, 40000),
+                                   (20000, 66, 33001)])
 def test_several_pieces_of_the_vocabulary(T, K, V, trans, dtype):
     a, b, target, dloss = operands(T, K, V, DTYPES[dtype], trans)
     check_grad(a, b, target, dloss, trans, smooth=0.1)

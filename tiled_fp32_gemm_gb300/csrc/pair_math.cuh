@@ -34,6 +34,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "l"(bits_of(a)), "l"(bits_of(b)), "l"(bits_of(c)));
   return pair_of(r);
 }
+__device__ __forceinline__ float2 get2(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ void put2(float* v, float2 p) {
+  v[0] = p.x;
+  v[1] = p.y;
+}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 }  // namespace row

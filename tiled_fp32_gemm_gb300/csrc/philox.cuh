@@ -106,16 +106,17 @@ struct Dropout {
     w[3] = c3;
   }
 
-  __device__ __forceinline__ float apply(float v, uint32_t word) const {
-    return word >= border ? v * scale : 0.0f;
+  // Four values by their words.
+  __device__ __forceinline__ void apply(float* v, const uint32_t (&w)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = w[i] >= border ? v[i] * scale : 0.0f;
   }
 
   // D() of a block's four columns.
   __device__ __forceinline__ void apply4(const Row& r, const Columns& c, float* v) const {
     uint32_t w[4];
     words(r, c, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = apply(v[i], w[i]);
+    apply(v, w);
   }
   // D() of four values of four neighbouring lanes each, value i of the lanes
   // being block i's columns in order; lane l gives the block of value l.  The
@@ -132,8 +133,7 @@ struct Dropout {
     y = __shfl_xor_sync(0xffffffffu, upper ? w[1] : w[3], 2);
     if (upper) w[0] = x, w[1] = y;
     else w[2] = x, w[3] = y;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = apply(v[i], w[i]);
+    apply(v, w);
   }
 };
 
