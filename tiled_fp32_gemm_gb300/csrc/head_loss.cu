@@ -31,7 +31,7 @@ int64_t up256(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
 
 // --- forwards -----------------------------------------------------------------
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 8;  // entries a thread has in flight
 
 struct JoinArgs {
   int64_t T, V, slots;
@@ -47,31 +47,41 @@ struct JoinArgs {
 };
 
 // Joins the entries of `across` tokens (a power of two up to 32) a CTA: a
-// thread takes every (256 / across)th of a token's, and the threads' meet in
+// thread takes every (THREADS / across)th of a token's, and the threads' meet in
 // a fixed tree.  Logarithm and difference in fp64: one a token, and lse is some
 // 12 while the loss may be a thousandth of it.
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a, int across) {
-  __shared__ Softmax soft[kJoinThreads];
-  __shared__ float plain[kJoinThreads];
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) join_kernel(const JoinArgs a, int across) {
+  __shared__ Softmax soft[THREADS];
+  __shared__ float plain[THREADS];
   grid_launch_dependents();
   grid_wait();
-  const int lanes = kJoinThreads / across, me = threadIdx.x / across;
+  const int lanes = THREADS / across, me = threadIdx.x / across;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * across + threadIdx.x % across;
   Softmax s{-INFINITY, 0.0f};
   float sum = 0.0f;
   if (t < a.T) {
-#pragma unroll 8
-    for (int64_t i = me; i < a.slots; i += lanes) {
-      const int64_t at = i * a.T + t;
-      if (!bounds_ok(a.bounds, SITE_PARTIAL, at, 1, a.slots * a.T)) continue;
-      const float2 p = a.parts[at];
-      s.join(Softmax{p.x, p.y});
-      if (a.sums) sum += a.sums[at];
+    for (int64_t i0 = me; i0 < a.slots; i0 += kJoinBatch * lanes) {
+      float2 part[kJoinBatch];
+      float add[kJoinBatch];
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const int64_t i = i0 + k * lanes, at = i * a.T + t;
+        const bool there =
+            i < a.slots && bounds_ok(a.bounds, SITE_PARTIAL, at, 1, a.slots * a.T);
+        part[k] = there ? a.parts[at] : make_float2(-INFINITY, 0.0f);
+        add[k] = there && a.sums ? a.sums[at] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        s.join(Softmax{part[k].x, part[k].y});
+        sum += add[k];
+      }
     }
   }
   soft[threadIdx.x] = s;
   plain[threadIdx.x] = sum;
-  for (int n = kJoinThreads / 2; n >= across; n /= 2) {
+  for (int n = THREADS / 2; n >= across; n /= 2) {
     __syncthreads();
     if (threadIdx.x < n) {
       soft[threadIdx.x].join(soft[threadIdx.x + n]);
@@ -169,8 +179,10 @@ cudaError_t launch_head_loss(const HeadLossArgs& a, const HeadLossPlan& p, float
   while (across < 32 && a.T >= 2 * across * static_cast<int64_t>(sms)) across *= 2;
   const JoinArgs j{a.T, a.V, p.slots, parts, sums, target_logit, a.target, a.ignore_index,
                    a.smoothing, a.z_loss, loss, lse, a.bounds};
-  return launch_dependent(join_kernel, static_cast<unsigned>(ceil_div(a.T, across)), kJoinThreads,
-                          stream, j, across);
+  // Few tokens: the threads that a CTA for every SM would have.
+  const unsigned ctas = static_cast<unsigned>(ceil_div(a.T, across));
+  return a.T < sms ? launch_dependent(join_kernel<1024>, ctas, 1024, stream, j, across)
+                   : launch_dependent(join_kernel<256>, ctas, 256, stream, j, across);
 }
 
 // --- backwards ----------------------------------------------------------------
@@ -243,33 +255,47 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowArgs a, int 
   }
 }
 
-// dX in its type from its planes of sums, added in order.
+// dX in its type from its planes of sums.  A CTA takes 32 groups of four values;
+// its warps take every eighth plane each, and the warps' sums are added in order.
+constexpr int kPlaneWarps = kRowThreads / 32;
+
 template <class T>
 __global__ void __launch_bounds__(kRowThreads)
     round_planes_kernel(const float* sums, int planes, int64_t plane, int64_t pitch,
                         int64_t extent, const Matrix<T> to, int64_t rows, int cols) {
+  __shared__ float4 part[kPlaneWarps][32];
   grid_launch_dependents();
   grid_wait();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t per_row = pitch / 4, total = rows * per_row;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
-    const int64_t r = i / per_row;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * 32; i0 < total;
+       i0 += static_cast<int64_t>(gridDim.x) * 32) {
+    const int64_t i = i0 + lane, r = i / per_row;
     const int c = static_cast<int>(i % per_row) * 4;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < total) {
 #pragma unroll 4
-    for (int p = 0; p < planes; ++p) {
-      const int64_t at = p * plane + r * pitch + c;
-      if (!bounds_ok(to.rec, SITE_PARTIAL, at, 4, extent)) continue;
-      const float4 v = *reinterpret_cast<const float4*>(sums + at);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+      for (int p = warp; p < planes; p += kPlaneWarps) {
+        const int64_t at = p * plane + r * pitch + c;
+        if (!bounds_ok(to.rec, SITE_PARTIAL, at, 4, extent)) continue;
+        const float4 v = *reinterpret_cast<const float4*>(sums + at);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
     }
-    const float v[4] = {s.x, s.y, s.z, s.w};
+    part[warp][lane] = s;
+    __syncthreads();
+    // Warp w finishes value w of the groups (four of the warps).
+    if (warp < 4 && i < total && c + warp < cols) {
+      float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (c + k < cols) to.store(r, c + k, v[k]);
+      for (int w = 0; w < kPlaneWarps; ++w)
+        t += reinterpret_cast<const float*>(&part[w][lane])[warp];
+      to.store(r, c + warp, t);
+    }
+    __syncthreads();
   }
 }
 
@@ -335,9 +361,10 @@ PiecePlan plan_piece(const HeadGradArgs& a, const Piece& piece, int64_t pieces, 
   // dX's sums are kept over several pieces of the vocabulary, and where few
   // tiles of dX leave a long contraction to be cut into slices of pairs.  Measured
   // (bf16, the whole gradient, us without and with slices): 1 x 1024 x 32768 68.4
-  // / 60.9, 100 x 1024 x 32768 79.1 / 66.0, 1024 x 2048 x 32000 288 / 265, but 300 x
-  // 256 x 10000 31.1 / 34.3, 48 x 512 x 5000 20.3 / 28.6.
-  p.planes = pieces > 1 || (!p.x.pair && piece.n >= 16384);
+  // / 60.9, 1024 x 2048 x 32000 288 / 265, 1809 x 169 x 9889 73.8 / 64.0, 16 x 1024 x 9000
+  // 32.5 / 30.4, but 300 x 256 x 10000 31.0 / 32.5, 500 x 1024 x 5000 34.0 / 40.3, 48 x 512
+  // x 5000 21.1 / 28.4.
+    p.planes = pieces > 1 || (!p.x.pair && piece.n >= 8192);
   if (p.planes) p.w = plan_linear(m.w, sms);
   return p;
 }
@@ -451,7 +478,7 @@ cudaError_t launch_head_grad(const HeadGradArgs& args, const HeadGradPlan& p, vo
   if (e != cudaSuccess || !a.dX || !p.acc_bytes) return e;
   const int64_t plane = p.dx.rows * p.dx.pitch, all = p.dx.planes * plane;
   const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>(16 * static_cast<int64_t>(sms), ceil_div(l.T * p.dx.pitch / 4, kRowThreads)));
+      std::min<int64_t>(32 * static_cast<int64_t>(sms), ceil_div(l.T * p.dx.pitch / 4, 32)));
   const int64_t extent = view_extent(l.T, l.K, a.lddx);
   const int cols = static_cast<int>(l.K);
   auto go = [&](auto* kernel, auto* to) {

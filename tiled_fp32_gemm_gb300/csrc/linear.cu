@@ -41,7 +41,7 @@ struct CopyJobs {
   int count, blocks;
 };
 
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 256, kBatch = 4;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyJobs jobs) {
   grid_launch_dependents();
@@ -49,33 +49,62 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyJobs 
   const CopyJob& j = jobs.job[static_cast<int>(blockIdx.x) >= jobs.job[1].first_block ? 1 : 0];
   const int x0 = threadIdx.x % j.row_threads, row_step = kCopyThreads / j.row_threads;
   const int chunks = static_cast<int>(j.pitch / 16);
-  for (int64_t r = static_cast<int64_t>(blockIdx.x - j.first_block) * row_step +
-                   threadIdx.x / j.row_threads;
-       r < j.rows; r += static_cast<int64_t>(j.blocks) * row_step) {
-    for (int x = x0; x < chunks; x += j.row_threads) {
-      const int64_t c0 = 16 * static_cast<int64_t>(x), at = r * j.pitch_src + c0;
+  const int64_t first = static_cast<int64_t>(blockIdx.x - j.first_block) * row_step +
+                        threadIdx.x / j.row_threads;
+  const int64_t step = static_cast<int64_t>(j.blocks) * row_step;
+  // kBatch words, `down` rows and `right` words apart; the loads of all of them
+  // are in flight before the first is stored.
+  auto batch = [&](int64_t r0, int xw, int64_t down, int right) {
+    uint4 lo[kBatch], hi[kBatch];
+    int shift[kBatch];  // -1: byte by byte
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t r = r0 + k * down, c0 = 16 * static_cast<int64_t>(xw + k * right);
+      const int64_t at = r * j.pitch_src + c0;
+      shift[k] = -1;
+      if (r >= j.rows || c0 >= j.bytes) continue;
+      const int s = static_cast<int>(reinterpret_cast<uintptr_t>(j.src + at) & 15u);
+      if (at < s || at - s + 32 > j.extent) continue;
+      const uint4* p = reinterpret_cast<const uint4*>(j.src + (at - s));
+      lo[k] = p[0];
+      hi[k] = p[1];
+      shift[k] = s;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t r = r0 + k * down, c0 = 16 * static_cast<int64_t>(xw + k * right);
+      const int64_t at = r * j.pitch_src + c0, to = r * j.pitch + c0;
       const int left = static_cast<int>(min(int64_t(16), j.bytes - c0));  // of the row, or < 0
+      if (r >= j.rows || c0 >= j.pitch) break;
       uint32_t o[4] = {0u, 0u, 0u, 0u};
-      const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(j.src + at) & 15u);
-      if (left > 0 && at >= shift && at - shift + 32 <= j.extent) {
-        const uint4* p = reinterpret_cast<const uint4*>(j.src + (at - shift));
-        const uint4 u = row::shifted(p[0], p[1], shift);
+      if (shift[k] >= 0) {
+        const uint4 u = row::shifted(lo[k], hi[k], shift[k]);
         o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int keep = left - 4 * i;  // bytes of this word inside the row
           if (keep < 4) o[i] = keep <= 0 ? 0u : o[i] & ((1u << (8 * keep)) - 1u);
         }
-      } else {
+      } else if (left > 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (i < left && bounds_ok(jobs.rec, SITE_PREP_SRC, at + i, 1, j.extent))
             o[i / 4] |= static_cast<uint32_t>(j.src[at + i]) << (8 * (i % 4));
       }
-      const int64_t to = r * j.pitch + c0;
       if (bounds_ok(jobs.rec, SITE_PREP_DST, to, 16, j.rows * j.pitch))
         *reinterpret_cast<uint4*>(j.dst + to) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+  };
+  // Rows past 16 KB one after the other, along each; others from row to row, a
+  // column of words at a time.  Measured (us for a loss with the copy, along / from
+  // row to row): 2160 rows of 60 KB 84 / 114, 7499 of 6.5 KB 42 / 35, 110304 of 0.7 KB
+  // 79 / 59.
+  if (chunks > 1024) {
+    for (int64_t r = first; r < j.rows; r += step)
+      for (int x = x0; x < chunks; x += kBatch * j.row_threads) batch(r, x, 0, j.row_threads);
+  } else {
+    for (int x = x0; x < chunks; x += j.row_threads)
+      for (int64_t r = first; r < j.rows; r += kBatch * step) batch(r, x, step, 0);
   }
 }
 
