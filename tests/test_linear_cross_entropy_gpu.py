@@ -271,6 +271,17 @@ def test_one_gradient_alone_has_the_same_bits(T, K, V, need):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("db_dtype", [None, torch.float32])
+@pytest.mark.parametrize("T,K,V,trans", [(200, 1024, 9000, True), (30, 520, 20000, True),
+                                         (300, 1040, 9008, False), (2000, 2048, 9100, True)])
+def test_weight_gradients_on_pairs(T, K, V, trans, db_dtype, dtype):
+    """Results that leave by boxes, 16- and 32-bit, with and without D's scale,
+    ragged in rows and columns."""
+    a, b, target, dloss = operands(T, K, V, DTYPES[dtype], trans)
+    check_grad(a, b, target, dloss, trans, db_dtype=db_dtype)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("trans", [True, False])
 @pytest.mark.parametrize("T,K,V", [(4096, 40, 40000), (8192, 64, 33001), (16384, 40, 40000),
                                    (20000, 66, 33001)])

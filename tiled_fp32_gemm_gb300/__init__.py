@@ -19,7 +19,10 @@ by ``tiled_fp32_gemm_gb300.build``).  This module only marshals arguments:
   (torch supplies device memory and the current stream; nothing else);
   ``gemm`` for the general form and ``gemm_mixed`` for 16-bit inputs;
 * the feed-forward operators of ``layers`` (include/mt_layers.h):
-  ``rms_norm``, ``linear`` and their gradients.
+  ``rms_norm``, ``linear`` and their gradients;
+* the residual joins and the vocabulary's loss of ``model``
+  (include/mt_model.h): ``layer_norm``, ``dropout``, ``linear_cross_entropy``
+  and their gradients.
 
 There is no CPU fallback: if the library is missing, every call raises.
 """

@@ -14,6 +14,8 @@
 // 0.79, with dropout 141 us, 0.70; 16384 x 8192 194 us, 0.81; 4096 x 16384 200 us, 0.40
 // (32 values a thread spill 150 bytes); fp32 8192 x 8192 206 us, 0.77; unaligned
 // 16384 x 4095 127 us, 0.62; 4096 x 20000, read twice, 220 us, 0.44.
+#pragma once
+
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -773,28 +775,18 @@ cudaError_t launch_weight(const LayerNormGradArgs& a, float* partial, int sms,
 
 }  // namespace
 
-int64_t layer_norm_grad_workspace(const LayerNormGradArgs& a, int sms) {
-  Staging g{};
-  int parts = 0;
-  path_of(a, sms, &g, &parts);
-  return static_cast<int64_t>(parts) * a.d * 4 * ((a.dweight != nullptr) + (a.dbias != nullptr));
-}
-
-cudaError_t layer_norm_grad_read_and_clear_status(unsigned int* status) {
-  cudaError_t e = cudaMemcpyFromSymbol(status, g_status, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));
-}
-
-cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& a, void* workspace, int sms,
-                                   cudaStream_t stream) {
-  float* partial = static_cast<float*>(workspace);
-  switch (a.dtype) {
-    case DT_F16: return launch_weight<__half>(a, partial, sms, stream);
-    case DT_BF16: return launch_weight<__nv_bfloat16>(a, partial, sms, stream);
-    default: return launch_weight<float>(a, partial, sms, stream);
+// One storage type's part (layer_norm_grad_<type>.cu): the call, and its status
+// word read and cleared.
+#define MT_LAYER_NORM_GRAD_TYPE(NAME, T)                                                     \
+  cudaError_t launch_layer_norm_grad_##NAME(const LayerNormGradArgs& a, float* partial,      \
+                                            int sms, cudaStream_t stream) {                  \
+    return launch_weight<T>(a, partial, sms, stream);                                        \
+  }                                                                                          \
+  cudaError_t layer_norm_grad_##NAME##_read_and_clear_status(unsigned int* status) {         \
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_status, sizeof(unsigned int));            \
+    if (e != cudaSuccess) return e;                                                          \
+    const unsigned int zero = 0;                                                             \
+    return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));                        \
   }
-}
 
 }  // namespace mt

@@ -37,7 +37,7 @@ struct LayerNormArgs {
 
 cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t stream);
 
-// layer_norm_grad.cu.  See mt_layer_norm_backward_args for the operator.
+// layer_norm_grad.cuh.  See mt_layer_norm_backward_args for the operator.
 struct LayerNormGradArgs {
   int64_t rows;
   int d;
@@ -68,6 +68,16 @@ int64_t layer_norm_grad_workspace(const LayerNormGradArgs& a, int sms);
 cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& a, void* workspace, int sms,
                                    cudaStream_t stream);
 cudaError_t layer_norm_grad_read_and_clear_status(unsigned int* status);
+// Its parts by storage type.
+cudaError_t launch_layer_norm_grad_f16(const LayerNormGradArgs& a, float* partial, int sms,
+                                       cudaStream_t stream);
+cudaError_t launch_layer_norm_grad_bf16(const LayerNormGradArgs& a, float* partial, int sms,
+                                        cudaStream_t stream);
+cudaError_t launch_layer_norm_grad_f32(const LayerNormGradArgs& a, float* partial, int sms,
+                                       cudaStream_t stream);
+cudaError_t layer_norm_grad_f16_read_and_clear_status(unsigned int* status);
+cudaError_t layer_norm_grad_bf16_read_and_clear_status(unsigned int* status);
+cudaError_t layer_norm_grad_f32_read_and_clear_status(unsigned int* status);
 
 // dropout.cu.  See mt_dropout_args for the operator.
 struct DropoutCall {
