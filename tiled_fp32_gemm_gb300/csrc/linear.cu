@@ -41,8 +41,9 @@ struct CopyJobs {
   int count, blocks;
 };
 
-constexpr int kCopyThreads = 256, kBatch = 4;
+constexpr int kCopyThreads = 256;
 
+template <int BATCH>
 __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyJobs jobs) {
   grid_launch_dependents();
   grid_wait();
@@ -52,13 +53,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyJobs 
   const int64_t first = static_cast<int64_t>(blockIdx.x - j.first_block) * row_step +
                         threadIdx.x / j.row_threads;
   const int64_t step = static_cast<int64_t>(j.blocks) * row_step;
-  // kBatch words, `down` rows and `right` words apart; the loads of all of them
+  // BATCH words, `down` rows and `right` words apart; the loads of all of them
   // are in flight before the first is stored.
   auto batch = [&](int64_t r0, int xw, int64_t down, int right) {
-    uint4 lo[kBatch], hi[kBatch];
-    int shift[kBatch];  // -1: byte by byte
+    uint4 lo[BATCH], hi[BATCH];
+    int shift[BATCH];  // -1: byte by byte
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
+    for (int k = 0; k < BATCH; ++k) {
       const int64_t r = r0 + k * down, c0 = 16 * static_cast<int64_t>(xw + k * right);
       const int64_t at = r * j.pitch_src + c0;
       shift[k] = -1;
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyJobs 
       shift[k] = s;
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
+    for (int k = 0; k < BATCH; ++k) {
       const int64_t r = r0 + k * down, c0 = 16 * static_cast<int64_t>(xw + k * right);
       const int64_t at = r * j.pitch_src + c0, to = r * j.pitch + c0;
       const int left = static_cast<int>(min(int64_t(16), j.bytes - c0));  // of the row, or < 0
@@ -95,16 +96,15 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyJobs 
         *reinterpret_cast<uint4*>(j.dst + to) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   };
-  // Rows past 16 KB one after the other, along each; others from row to row, a
-  // column of words at a time.  Measured (us for a loss with the copy, along / from
-  // row to row): 2160 rows of 60 KB 84 / 114, 7499 of 6.5 KB 42 / 35, 110304 of 0.7 KB
-  // 79 / 59.
-  if (chunks > 1024) {
+  // A batch goes along a row past 16 KB and from row to row in others, a column of
+  // words at a time.  Measured (us for a loss with the copy, along / from row to row):
+  // 2160 rows of 60 KB 84 / 114, 110304 of 0.7 KB 79 / 59.
+  if (BATCH == 1 || chunks > 1024) {
     for (int64_t r = first; r < j.rows; r += step)
-      for (int x = x0; x < chunks; x += kBatch * j.row_threads) batch(r, x, 0, j.row_threads);
+      for (int x = x0; x < chunks; x += BATCH * j.row_threads) batch(r, x, 0, j.row_threads);
   } else {
     for (int x = x0; x < chunks; x += j.row_threads)
-      for (int64_t r = first; r < j.rows; r += kBatch * step) batch(r, x, step, 0);
+      for (int64_t r = first; r < j.rows; r += BATCH * step) batch(r, x, step, 0);
   }
 }
 
@@ -337,8 +337,16 @@ cudaError_t make_ready(const LinearArgs& a, const LinearPlan& p, void* workspace
 cudaError_t launch_copies(CopyJobs* jobs, cudaStream_t stream) {
   if (jobs->count == 0) return cudaSuccess;
   if (jobs->count == 1) jobs->job[1].first_block = INT32_MAX;
-  return launch_dependent(copy_rows_kernel, dim3(static_cast<unsigned>(jobs->blocks)),
-                          kCopyThreads, stream, *jobs);
+  // Eight words a thread and more are loaded four at a time, fewer one by one: the
+  // batch's 80 registers let three blocks share an SM, the single word's 38 six.  Measured
+  // (us with the product or loss that follows, batched / single): 2 words a thread 73.5 / 64.5
+  // (4097 and 2053 fp16 rows of 3001), 5 words 36.0 / 33.6, 8.5 words 59.8 / 65.0, 49 words
+  // 240 / 260.
+  int64_t words = 0;
+  for (int i = 0; i < jobs->count; ++i) words += jobs->job[i].rows * (jobs->job[i].pitch / 16);
+  const bool batched = words >= 8 * static_cast<int64_t>(jobs->blocks) * kCopyThreads;
+  return launch_dependent(batched ? copy_rows_kernel<4> : copy_rows_kernel<1>,
+                          dim3(static_cast<unsigned>(jobs->blocks)), kCopyThreads, stream, *jobs);
 }
 
 template <class Ep>
