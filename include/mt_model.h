@@ -46,9 +46,9 @@ extern "C" {
  * weight NULL: ones; bias NULL: zeros.  h enters the norm unrounded.  Written:
  * h in x's type (NULL: not written), m and r to `mean` and `rstd` (rows floats;
  * NULL: not written; the gradient reads both) and y.  The variance is that of
- * the differences from the mean, so a common offset costs it nothing.  A NaN or
- * an infinity in a row makes its m, r and y NaN; a variance past fp32's range
- * (differences past 1.8e19) makes r 0 and y the bias.
+ * the differences from the mean, so a common offset costs it nothing.  A NaN in a
+ * row makes its m, r and y NaN, an infinity r and y (and m infinite or NaN); a
+ * variance past fp32's range (differences past 1.8e19) makes r 0 and y the bias.
  */
 typedef struct {
     int64_t rows, d;
@@ -165,7 +165,10 @@ MT_API mt_status mt_dropout(const mt_dropout_args *args, cudaStream_t stream);
  * s = label_smoothing, c = z_loss.  A is T x K, B is K x V, or V x K with
  * trans_b.  A row whose target is ignore_index has loss 0 (its lse is
  * computed); a target outside [0, V) that is not ignore_index makes the row's
- * loss NaN.  A NaN or infinite logit makes its row's lse NaN.
+ * loss NaN.  A logit that is NaN or +infinity makes its row's lse NaN.  The
+ * products' sums are the tensor cores', which truncate as they accumulate: within
+ * 5e-5 of the sum of absolute values, as mt_linear's (lse to some 1e-6 for 4096
+ * values of K).
  */
 typedef struct {
     int64_t T, K, V;
@@ -189,8 +192,9 @@ typedef struct {
 /*
  * T == 0 does nothing; V == 0 with rows is MT_ERR_INVALID_ARG; K == 0 gives the
  * loss of zero logits.  Outputs overlap nothing (MT_ERR_ALIAS).  Scratch: two
- * or three floats for every token and 128 columns of the vocabulary (32, up to
- * 128 tokens), and copies of operands TMA cannot read in place (see mt_linear).
+ * floats (three with smoothing) for every token and 128 columns of the vocabulary
+ * (32 for few tokens), and copies of operands TMA cannot read in place (see
+ * mt_linear).
  * Other errors as mt_linear.
  */
 MT_API mt_status mt_linear_cross_entropy(const mt_linear_cross_entropy_args *args,
@@ -205,10 +209,12 @@ MT_API mt_status mt_linear_cross_entropy(const mt_linear_cross_entropy_args *arg
  *     dB = A^T * D, stored as B is         K x V (V x K with trans_b), db_dtype
  *
  * D is rounded to dtype for the two products and held for one piece of the
- * vocabulary at a time; in fp16 it is held times a power of two that brings the
- * largest |dloss| near 2^13, so that small probabilities keep their digits.  A
- * row whose target is ignore_index has a D of zeros whatever its logits are; its row of A
- * still enters dB's sums, times zero, and has to be finite.  Any other target
+ * vocabulary at a time (up to 1 GiB); in fp16 it is held times a power of two that
+ * brings the largest |dloss| (1 + 2 c |lse|) of the call to 2^13 or more, so that
+ * small probabilities keep their digits (p is at most 1 with the forward call's lse;
+ * with another D may overflow).  A row whose target is ignore_index has a D of zeros
+ * whatever its logits, dloss and lse are; its row of A still enters dB's sums, times
+ * zero, and has to be finite.  Any other target
  * outside [0, V) makes the row's D NaN.  dA or dB may be NULL: not computed.
  * The gradient is that of loss: nothing reaches A or B through lse on its own.
  */
@@ -234,9 +240,11 @@ typedef struct {
     int32_t reserved;       /* 0 */
 } mt_linear_cross_entropy_backward_args;
 
-/* T == 0 writes zeros to dB.  Outputs overlap nothing (MT_ERR_ALIAS).  Scratch:
- * a piece of D, dA in fp32 where the vocabulary takes several pieces, and
- * copies of operands TMA cannot read in place.  Other errors as
+/* T == 0 writes zeros to dB.  Outputs overlap nothing (MT_ERR_ALIAS).  Results do
+ * not depend on which of dA and dB are asked for, and are the same bits each time.
+ * Scratch: a piece of D, dA's sums in fp32 (once for several pieces of the
+ * vocabulary, or for each of up to sms / 2 slices of a long one), and copies of
+ * operands TMA cannot read in place.  Other errors as
  * mt_linear_cross_entropy. */
 MT_API mt_status mt_linear_cross_entropy_backward(
     const mt_linear_cross_entropy_backward_args *args, cudaStream_t stream);
