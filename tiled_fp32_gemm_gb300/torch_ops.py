@@ -11,8 +11,8 @@ implementation, so tracing needs no GPU).  All but the first two are
 differentiable, once: their gradients are the ``*_backward`` functions (for
 dropout, dropout itself), which have none themselves, so a second derivative
 raises.  A seed that is advanced in place between an operator and its gradient
-raises too: torch notices it.  Marshalling only: the work runs in the library's
-kernels.
+raises too: torch notices it.  No gradient of zeros is made for an output that
+nothing reads.  Marshalling only: the work runs in the library's kernels.
 """
 from __future__ import annotations
 
@@ -82,11 +82,14 @@ def _linear_setup(ctx, inputs, output):
     a, b, bias, residual, activation, trans_b = inputs
     ctx.save_for_backward(a, b, output[1])
     ctx.options = activation, trans_b
+    ctx.set_materialize_grads(False)
     ctx.mark_non_differentiable(output[1])
 
 
 @once_differentiable
 def _linear_grad(ctx, dy, _):
+    if dy is None:
+        return (None,) * 6
     a, b, z = ctx.saved_tensors
     activation, trans_b = ctx.options
     need_a, need_b, need_bias, need_residual = ctx.needs_input_grad[:4]
@@ -122,15 +125,24 @@ def _rms_norm_setup(ctx, inputs, output):
     _, h, rstd = output
     ctx.save_for_backward(x if residual is None else h, weight, rstd)
     ctx.has_residual = residual is not None
+    ctx.set_materialize_grads(False)
     ctx.mark_non_differentiable(rstd)
+
+
+def _both(dy, dh, h):
+    """The gradients of a norm's y and h as its gradient takes them: h's is None
+    where nothing reads it, y's is needed."""
+    dy = torch.zeros_like(h, memory_format=torch.contiguous_format) if dy is None \
+        else dy.contiguous()
+    return dy, None if dh is None else dh.contiguous()
 
 
 @once_differentiable
 def _rms_norm_grad(ctx, dy, dh, _):
     h, weight, rstd = ctx.saved_tensors
-    dx, dweight = rms_norm_backward(
-        dy.contiguous(), h, weight, rstd, need_weight=ctx.needs_input_grad[1],
-        dh=dh.contiguous() if ctx.has_residual and dh is not None else None)
+    dy, dh = _both(dy, dh if ctx.has_residual else None, h)
+    dx, dweight = rms_norm_backward(dy, h, weight, rstd, dh=dh,
+                                    need_weight=ctx.needs_input_grad[1])
     if dweight is not None:
         dweight = dweight.to(weight.dtype)
     return dx, dweight, dx if ctx.has_residual else None, None
@@ -169,6 +181,7 @@ def _layer_norm_setup(ctx, inputs, output):
     ctx.save_for_backward(h if ctx.joined else x, weight, mean, rstd, seed if p > 0.0 else None)
     ctx.options = p, sequence
     ctx.has_residual = residual is not None
+    ctx.set_materialize_grads(False)
     ctx.mark_non_differentiable(mean, rstd)
 
 
@@ -176,10 +189,10 @@ def _layer_norm_setup(ctx, inputs, output):
 def _layer_norm_grad(ctx, dy, dh, *_):
     h, weight, mean, rstd, seed = ctx.saved_tensors
     p, sequence = ctx.options
+    dy, dh = _both(dy, dh if ctx.joined else None, h)
     dx, dres, dweight, dbias = layer_norm_backward(
-        dy.contiguous(), h, weight, mean, rstd,
-        dh=dh.contiguous() if ctx.joined and dh is not None else None, dropout=p, seed=seed,
-        sequence=sequence, need_weight=ctx.needs_input_grad[1], need_bias=ctx.needs_input_grad[2])
+        dy, h, weight, mean, rstd, dh=dh, dropout=p, seed=seed, sequence=sequence,
+        need_weight=ctx.needs_input_grad[1], need_bias=ctx.needs_input_grad[2])
     if dweight is not None:
         dweight = dweight.to(weight.dtype)
     if dbias is not None:
@@ -208,10 +221,13 @@ def _dropout_setup(ctx, inputs, output):
     ctx.save_for_backward(seed)
     ctx.options = p, sequence
     ctx.has_residual = residual is not None
+    ctx.set_materialize_grads(False)
 
 
 @once_differentiable
 def _dropout_grad(ctx, dy):
+    if dy is None:
+        return (None,) * 5
     seed, = ctx.saved_tensors
     p, sequence = ctx.options
     dx = dropout(dy.contiguous(), p, seed, sequence=sequence) if ctx.needs_input_grad[0] else None
@@ -246,11 +262,14 @@ def _linear_cross_entropy_setup(ctx, inputs, output):
     ctx.save_for_backward(a, b, target, output[1])
     ctx.options = dict(trans_b=trans_b, ignore_index=ignore_index,
                        label_smoothing=label_smoothing, z_loss=z_loss)
+    ctx.set_materialize_grads(False)
     ctx.mark_non_differentiable(output[1])
 
 
 @once_differentiable
 def _linear_cross_entropy_grad(ctx, dloss, _):
+    if dloss is None:
+        return (None,) * 7
     a, b, target, lse = ctx.saved_tensors
     da, db = linear_cross_entropy_backward(dloss.contiguous(), a, b, target, lse,
                                            need_a=ctx.needs_input_grad[0],
