@@ -152,12 +152,13 @@ rms_norm_op.register_autograd(_rms_norm_grad, setup_context=_rms_norm_setup)
 
 
 @torch.library.custom_op("mt::layer_norm", mutates_args=())
-def layer_norm_op(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor,
-                  residual: Optional[torch.Tensor], eps: float, dropout: float,
-                  seed: Optional[torch.Tensor], sequence: int
+def layer_norm_op(x: torch.Tensor, weight: Optional[torch.Tensor],
+                  bias: Optional[torch.Tensor], residual: Optional[torch.Tensor], eps: float,
+                  dropout: float, seed: Optional[torch.Tensor], sequence: int
                   ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """(y, h, mean, rstd) of the layer norm of h = drop(x) + residual through
-    mt_layer_norm; where nothing is dropped or added h is empty (it is x)."""
+    mt_layer_norm (no weight: ones, no bias: zeros); where nothing is dropped or
+    added h is empty (it is x)."""
     y, h, mean, rstd = layer_norm(x, weight, bias, residual=residual, eps=eps, dropout=dropout,
                                   seed=seed, sequence=sequence)
     return y, x.new_empty((0,)) if h is x else h, mean, rstd
@@ -165,9 +166,9 @@ def layer_norm_op(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor,
 
 @layer_norm_op.register_fake
 def _layer_norm_fake(x, weight, bias, residual, eps, dropout, seed, sequence):
-    torch._check(x.dim() == 2 and weight.dim() == 1 and weight.shape[0] == x.shape[1]
-                 and bias.shape == weight.shape,
-                 lambda: "mt::layer_norm needs rows x d, a weight and a bias of d values")
+    torch._check(x.dim() == 2 and all(v is None or v.dim() == 1 and v.shape[0] == x.shape[1]
+                                      for v in (weight, bias)),
+                 lambda: "mt::layer_norm needs rows x d, a weight and a bias of d values or none")
     joined = residual is not None or dropout > 0.0
     stats = [x.new_empty((x.shape[0],), dtype=torch.float32) for _ in range(2)]
     return (x.new_empty(tuple(x.shape)),
@@ -175,11 +176,12 @@ def _layer_norm_fake(x, weight, bias, residual, eps, dropout, seed, sequence):
 
 
 def _layer_norm_setup(ctx, inputs, output):
-    x, weight, _, residual, _, p, seed, sequence = inputs
+    x, weight, bias, residual, _, p, seed, sequence = inputs
     _, h, mean, rstd = output
     ctx.joined = residual is not None or p > 0.0
     ctx.save_for_backward(h if ctx.joined else x, weight, mean, rstd, seed if p > 0.0 else None)
     ctx.options = p, sequence
+    ctx.vector_dtype = next((v.dtype for v in (weight, bias) if v is not None), None)
     ctx.has_residual = residual is not None
     ctx.set_materialize_grads(False)
     ctx.mark_non_differentiable(mean, rstd)
@@ -194,9 +196,9 @@ def _layer_norm_grad(ctx, dy, dh, *_):
         dy, h, weight, mean, rstd, dh=dh, dropout=p, seed=seed, sequence=sequence,
         need_weight=ctx.needs_input_grad[1], need_bias=ctx.needs_input_grad[2])
     if dweight is not None:
-        dweight = dweight.to(weight.dtype)
+        dweight = dweight.to(ctx.vector_dtype)
     if dbias is not None:
-        dbias = dbias.to(weight.dtype)
+        dbias = dbias.to(ctx.vector_dtype)
     return dx, dweight, dbias, dres if ctx.has_residual else None, None, None, None, None
 
 
