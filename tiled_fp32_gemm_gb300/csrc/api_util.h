@@ -2,8 +2,10 @@
 // operators and the fused products (layers_api.cu, model_api.cu).
 #pragma once
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include <cuda_runtime.h>
 
@@ -76,7 +78,25 @@ struct Scratch {
 
 inline bool half_type(int t) { return t == MT_DTYPE_F16 || t == MT_DTYPE_BF16; }
 
-// The fused products' kernel attributes, set once per device.
+// What a group of kernels needs before its first launch on a device (their
+// shared-memory limits).
+struct OncePerDevice {
+  std::mutex mutex;
+  std::atomic<uint8_t> ready[kMaxDevices];
+
+  mt_status run(int dev, cudaError_t (*prepare)()) {
+    if (ready[dev].load(std::memory_order_acquire)) return MT_OK;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (prepare() != cudaSuccess) {
+      cudaGetLastError();
+      return MT_ERR_LAUNCH;
+    }
+    ready[dev].store(1, std::memory_order_release);
+    return MT_OK;
+  }
+};
+
+// The fused products' kernels made ready.
 mt_status prepare_linear(int dev);
 
 }  // namespace host

@@ -259,7 +259,6 @@ cudaError_t launch_head(const LinearArgs& a, const LinearPlan& p, void* workspac
                         cudaStream_t stream, int fault_inject = 0);
 
 // The kernels with these epilogues (head_pair.cu, head_split.cu).
-cudaError_t head_prepare();
 template <class Ep>
 cudaError_t launch_head_pair(const CUtensorMap& map_x, const CUtensorMap& map_w, uint32_t idesc,
                              const Ep& ep, bool w_mn, int kt, int clusters, int fault_inject,

@@ -9,6 +9,7 @@
 
 #include "gemm_f16.cuh"
 #include "head.cuh"
+#include "model.h"
 #include "store_box.cuh"
 
 namespace mt {
@@ -174,7 +175,7 @@ cudaError_t head_prepare() {
     prepare(s.kernel, s.smem);
     prepare(g.kernel, g.smem);
   }
-  return r;
+  return r == cudaSuccess ? linear_rows_prepare() : r;
 }
 
 cudaError_t head_pair_read_and_clear_status(unsigned int* status) {

@@ -1,11 +1,9 @@
 // C entry points of the feed-forward operators (include/mt_layers.h):
 // argument checks, launch choices, scratch.
-#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
 #include <cuda_runtime.h>
 
@@ -61,9 +59,7 @@ bool linear_types_ok(const mt_linear_args& g) {
   return g.activation >= MT_ACT_NONE && g.activation <= MT_ACT_SILU;
 }
 
-// The product kernels' shared-memory limits, set once per device.
-std::mutex g_linear_mutex;
-std::atomic<uint8_t> g_linear_ready[kMaxDevices];
+OncePerDevice g_linear_ready;
 
 }  // namespace
 
@@ -72,14 +68,7 @@ namespace host {
 
 mt_status prepare_linear(int dev) {
   if (!mt::tensor_map_encoder_available()) return MT_ERR_CUDA;
-  if (g_linear_ready[dev].load(std::memory_order_acquire)) return MT_OK;
-  std::lock_guard<std::mutex> lock(g_linear_mutex);
-  if (mt::linear_prepare() != cudaSuccess) {
-    cudaGetLastError();
-    return MT_ERR_LAUNCH;
-  }
-  g_linear_ready[dev].store(1, std::memory_order_release);
-  return MT_OK;
+  return g_linear_ready.run(dev, mt::linear_prepare);
 }
 
 }  // namespace host

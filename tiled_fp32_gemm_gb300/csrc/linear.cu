@@ -292,8 +292,7 @@ cudaError_t linear_prepare() {
     for (int mn = 0; mn < 4; ++mn)
       if (r == cudaSuccess) r = prepare(linear_pair_kernel_for(dtype, mn & 1, mn >> 1));
   }
-  if (r == cudaSuccess) r = linear_rows_prepare();
-  return r == cudaSuccess ? head_prepare() : r;
+  return r;
 }
 
 namespace {

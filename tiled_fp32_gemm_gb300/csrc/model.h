@@ -112,6 +112,9 @@ struct HeadLossArgs {
   BoundsRecord* bounds;
 };
 
+// Attributes of the loss's kernels and of its plain products', once per device.
+cudaError_t head_prepare();
+
 // A forward pass: its scratch, and the launches.
 struct HeadLossPlan {
   LinearPlan product;

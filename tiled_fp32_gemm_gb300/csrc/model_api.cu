@@ -40,6 +40,14 @@ mt::DropoutArgs dropout_args(const int64_t* seed, uint64_t sequence, double p) {
                          static_cast<float>(1.0 / (1.0 - p))};
 }
 
+// The loss's kernels and those of the products it makes.
+OncePerDevice g_loss_ready;
+
+mt_status prepare_loss(int dev) {
+  const mt_status st = prepare_linear(dev);
+  return st == MT_OK ? g_loss_ready.run(dev, mt::head_prepare) : st;
+}
+
 mt_status launched(cudaError_t e) {
   if (e == cudaSuccess) return MT_OK;
   cudaGetLastError();
@@ -182,7 +190,7 @@ mt_status mt_linear_cross_entropy(const mt_linear_cross_entropy_args* g, cudaStr
   int dev = 0;
   DeviceInfo info;
   mt_status st = current_device(&dev, &info);
-  if (st == MT_OK) st = prepare_linear(dev);
+  if (st == MT_OK) st = prepare_loss(dev);
   if (st != MT_OK) return st;
   const mt::HeadLossArgs a{T, K, V, g->A, g->lda, g->B, g->ldb, g->trans_b ? 0 : 1, g->target,
                            g->ignore_index, g->label_smoothing, g->z_loss, g->dtype,
@@ -228,7 +236,7 @@ mt_status mt_linear_cross_entropy_backward(const mt_linear_cross_entropy_backwar
   int dev = 0;
   DeviceInfo info;
   mt_status st = current_device(&dev, &info);
-  if (st == MT_OK) st = prepare_linear(dev);
+  if (st == MT_OK) st = prepare_loss(dev);
   if (st != MT_OK) return st;
   const mt::HeadGradArgs a{
       {T, K, V, g->A, g->lda, g->B, g->ldb, g->trans_b ? 0 : 1, g->target, g->ignore_index,
