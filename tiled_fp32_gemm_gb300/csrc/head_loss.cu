@@ -136,15 +136,20 @@ LinearArgs logits_of(const HeadLossArgs& a, const Piece& w) {
   return l;
 }
 
-// Pairs pay from half as many tiles on as for the linear layer, whose epilogue
-// costs the split kernel less: there 16 tokens' statistics meet over a warp's
-// lanes, here a thread walks over one token's.  Past 2048 values of K few tiles
-// want the split kernel's slices.  Measured (bf16, loss, us for the split kernel
-// against pairs): 256 x 1024 x 8192 (32 pairs) 20.0 / 14.9, 300 x 512 x 5000 (40)
-// 17.7 / 12.3, 512 x 1024 x 2048 (16) 17.2 / 14.0, 200 x 256 x 1024 (4) 13.6 /
-// 10.4, 1024 x 2048 x 1024 (16) 18.9 / 18.8, but 256 x 4096 x 4096 (16) 23.0 / 27.5.
+// Pairs from one tile on (and more than 128 tokens) up to 1280 values of K, from
+// a seventh as many tiles as SMs on past that: half as many as for the linear
+// layer, whose epilogue costs the split kernel less (there 16 tokens' statistics
+// meet over a warp's lanes, here a thread walks over one token's).  Of a long K few
+// tiles want the split kernel's slices.  Measured (bf16, the loss after a flush of
+// L2, us for the split kernel against pairs, steps of 2 us, by tiles of 256 x 256):
+//   K     256: 4 tiles 22 / 18, 16 tiles 22 / 18, 32 tiles 22 / 18, 128 tiles 35 / 22
+//   K    1280: 4 tiles 22 / 22, 16 tiles 24 / 22, 32 tiles 28 / 24
+//   K    1536: 4 tiles 22 / 24, 16 tiles 25 / 24, 32 tiles 28 / 24
+//   K    2048: 4 tiles 23 / 26, 16 tiles 26 / 26, 32 tiles 32 / 28, 128 tiles 56 / 36
+//   K    4096: 4 tiles 26 / 35, 16 tiles 31 / 35, 32 tiles 43 / 39, 128 tiles 82 / 57
+//   K    8192: 4 tiles 32 / 51, 16 tiles 43 / 55, 32 tiles 61 / 61, 128 tiles 133 / 96
 LinearPlan plan_logits(const LinearArgs& l, int sms) {
-  return plan_linear(l, sms, l.K <= 2048 ? 7 : sms);
+  return plan_linear(l, sms, l.K <= 1280 ? 7 : sms);
 }
 
 }  // namespace
