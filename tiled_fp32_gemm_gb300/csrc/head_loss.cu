@@ -305,10 +305,20 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // A piece of D: large enough that its products fill the GPU for many rounds of
-// tiles and dX's sums seldom wait in memory, a few hundredths of this GPU's.
-// Measured (bf16, us by MiB 64 / 256 / 512 / 1024): 8192 x 2048 x 65536 4160 / 3761 /
-// 3804 / 3533, 8192 x 1024 x 32768 1170 / 1067 / 938 / 954, 4096 x 4096 x 131072 7379 /
-// 7042 / 7099 / 7004.
+// tiles and dX's sums seldom wait in memory, 0.4 % of this GPU's.  What counts is
+// one piece instead of two (mostly 3 to 5 %, up to 20); of several pieces 1 GiB ones
+// are as fast as 512 MiB ones or up to 4 % faster.  Measured (bf16, us for a gradient
+// by itself, by limits of 128 / 256 / 512 / 1024 / 2048 MiB, the same form again
+// within 2 %):
+//   D of  512 MiB   8192 x 1024 x 32768   1316 / 1249 / 1007 / 1003 / 1002
+//   D of 1024 MiB   8192 x 2048 x 65536   4593 / 4114 / 4159 / 3949 / 4016
+//                   4096 x 4096 x 131072  7834 / 7806 / 7934 / 7672 / 7834
+//   D of 1144 MiB   6000 x 2048 x 100000  4969 / 4540 / 4655 / 4501 / 4495
+//   D of 2048 MiB   8192 x 512 x 131072   3169 / 2461 / 2399 / 2293 / 2289
+//                   8192 x 1024 x 131072  4181 / 4211 / 4107 / 4102 / 3992
+//                   16384 x 2048 x 65536  8518 / 8354 / 8225 / 8233 / 7898
+//                   4096 x 1024 x 262144  4645 / 3971 / 4150 / 4162 / 4121
+//                   32768 x 1024 x 32768  5530 / 4333 / 4336 / 4407 / 3869
 constexpr int64_t kPieceBytes = int64_t(1) << 30;
 
 // The two products of a piece of the vocabulary.
@@ -363,13 +373,22 @@ PiecePlan plan_piece(const HeadGradArgs& a, const Piece& piece, int64_t pieces, 
   // Planned as if both were wanted: a gradient's bits do not depend on which
   // others are asked for.
   plan_linear_two(m.x, m.w, sms, &p.x, &p.w);
-  // dX's sums are kept over several pieces of the vocabulary, and where few
-  // tiles of dX leave a long contraction to be cut into slices of pairs.  Measured
-  // (bf16, the whole gradient, us without and with slices): 1 x 1024 x 32768 68.4
-  // / 60.9, 1024 x 2048 x 32000 288 / 265, 1809 x 169 x 9889 73.8 / 64.0, 16 x 1024 x 9000
-  // 32.5 / 30.4, but 300 x 256 x 10000 31.0 / 32.5, 500 x 1024 x 5000 34.0 / 40.3, 48 x 512
-  // x 5000 21.1 / 28.4.
-    p.planes = pieces > 1 || (!p.x.pair && piece.n >= 8192);
+  // dX's sums are kept over several pieces of the vocabulary, and where too few
+  // tiles of dX for pairs leave a contraction of 8192 columns or more to be cut into
+  // slices of pairs.  The planes and their rounding cost 5 to 10 us, which shorter
+  // contractions seldom give back; at 8192 it is about even, from 16384 on a gain
+  // but for a few percent past 2048 values of K.  Measured (bf16, the whole gradient
+  // after a flush of L2, us without / with slices, T x K by columns):
+  //                     4096          8192         16384         65536
+  //   16 x 256        24 / 34       29 / 36       42 / 32       83 / 51
+  //   16 x 1024       30 / 34       41 / 38       52 / 46      125 / 105
+  //   16 x 4096       50 / 48       65 / 66      103 / 105     306 / 308
+  //   256 x 256       27 / 40       34 / 41       45 / 38       99 / 64
+  //   256 x 1024      36 / 43       45 / 46       68 / 56      199 / 131
+  //   256 x 4096      60 / 66       83 / 91      126 / 130     398 / 380
+  //   1024 x 256      38 / 43       49 / 52       76 / 56      215 / 144
+  //   1024 x 1024     76 / 56      118 / 70      103 / 106     309 / 290
+  p.planes = pieces > 1 || (!p.x.pair && piece.n >= 8192);
   if (p.planes) p.w = plan_linear(m.w, sms);
   return p;
 }
