@@ -30,6 +30,12 @@ constexpr int SMEM_STAGE_BUDGET = 200 * 1024;
 
 // Per translation unit: each reads and clears its own.
 static __device__ unsigned int g_status;  // bit 0: a bounded wait expired
+static inline cudaError_t read_and_clear_status(unsigned int* status) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));
+}
 
 // Element types of the operands: 16-bit (fp16 or bf16, by the instruction
 // descriptor) and e4m3; both MMAs take 32 bytes of K per step.

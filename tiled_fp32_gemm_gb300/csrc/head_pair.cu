@@ -179,10 +179,7 @@ cudaError_t head_prepare() {
 }
 
 cudaError_t head_pair_read_and_clear_status(unsigned int* status) {
-  cudaError_t e = cudaMemcpyFromSymbol(status, f16tc::g_status, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(f16tc::g_status, &zero, sizeof(unsigned int));
+  return f16tc::read_and_clear_status(status);
 }
 
 }  // namespace mt

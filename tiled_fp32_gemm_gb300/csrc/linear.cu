@@ -365,10 +365,6 @@ cudaError_t launch_split(const LinearPlan& p, const LinearKernel& k, int64_t gri
                           p.cluster, stream, args);
 }
 
-}  // namespace
-
-namespace {
-
 // The map of a result that is written by boxes of 32 rows x 128 bytes; false
 // where TMA cannot write it.
 bool encode_boxes(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t cols,

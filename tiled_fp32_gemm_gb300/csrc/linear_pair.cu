@@ -71,10 +71,7 @@ cudaError_t launch_linear_pair(const LinearKernel& k, const CUtensorMap& map_w,
 }
 
 cudaError_t linear_pair_read_and_clear_status(unsigned int* status) {
-  cudaError_t e = cudaMemcpyFromSymbol(status, f16tc::g_status, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(f16tc::g_status, &zero, sizeof(unsigned int));
+  return f16tc::read_and_clear_status(status);
 }
 
 }  // namespace mt

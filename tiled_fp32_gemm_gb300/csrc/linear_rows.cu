@@ -117,10 +117,7 @@ cudaError_t launch_linear_rows(const LinearArgs& a, const CUtensorMap& map_x,
 }
 
 cudaError_t linear_rows_read_and_clear_status(unsigned int* status) {
-  cudaError_t e = cudaMemcpyFromSymbol(status, f16tc::g_status, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(f16tc::g_status, &zero, sizeof(unsigned int));
+  return f16tc::read_and_clear_status(status);
 }
 
 }  // namespace mt

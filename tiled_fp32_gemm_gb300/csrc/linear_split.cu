@@ -35,10 +35,7 @@ LinearKernel linear_split_kernel_for(int dtype, int bt) {
 }
 
 cudaError_t linear_split_read_and_clear_status(unsigned int* status) {
-  cudaError_t e = cudaMemcpyFromSymbol(status, f16tc::g_status, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(f16tc::g_status, &zero, sizeof(unsigned int));
+  return f16tc::read_and_clear_status(status);
 }
 
 }  // namespace mt
