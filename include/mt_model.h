@@ -49,6 +49,7 @@ extern "C" {
  * the differences from the mean, so a common offset costs it nothing.  A NaN in a
  * row makes its m, r and y NaN, an infinity r and y (and m infinite or NaN); a
  * variance past fp32's range (differences past 1.8e19) makes r 0 and y the bias.
+ * Differences below 1e-19 have subnormal squares: with eps (nearly) 0 r loses digits.
  */
 typedef struct {
     int64_t rows, d;
@@ -191,8 +192,8 @@ typedef struct {
 
 /*
  * T == 0 does nothing; V == 0 with rows is MT_ERR_INVALID_ARG; K == 0 gives the
- * loss of zero logits.  Outputs overlap nothing (MT_ERR_ALIAS).  Scratch: two
- * floats (three with smoothing) for every token and 128 columns of the vocabulary
+ * loss of zero logits.  Outputs overlap nothing (MT_ERR_ALIAS).  Scratch: a float a token,
+ * two floats (three with smoothing) for every token and 128 columns of the vocabulary
  * (32 for few tokens), and copies of operands TMA cannot read in place (see
  * mt_linear).
  * Other errors as mt_linear.
@@ -208,14 +209,16 @@ MT_API mt_status mt_linear_cross_entropy(const mt_linear_cross_entropy_args *arg
  *     dA = D * op(B)^T                     T x K, dtype
  *     dB = A^T * D, stored as B is         K x V (V x K with trans_b), db_dtype
  *
- * D is rounded to dtype for the two products and held for one piece of the
- * vocabulary at a time (up to 1 GiB); in fp16 it is held times a power of two that
- * brings the largest |dloss| (1 + 2 c |lse|) of the call to 2^13 or more, so that
- * small probabilities keep their digits (p is at most 1 with the forward call's lse;
- * with another D may overflow).  A row whose target is ignore_index has a D of zeros
- * whatever its logits, dloss and lse are; its row of A still enters dB's sums, times
- * zero, and has to be finite.  Any other target
- * outside [0, V) makes the row's D NaN.  dA or dB may be NULL: not computed.
+ * D is rounded to dtype for the two products, whatever db_dtype is, and held for one
+ * piece of the vocabulary at a time (up to 1 GiB, but at least 256 columns); in fp16 it is
+ * held times a power of two that brings the largest |dloss| (1 + 2 c |lse|) of the call to
+ * 2^13 or more, so that values down to 2^-27 of the largest factor keep all of their bits
+ * (p is at most 1 with the forward call's lse; with another D may overflow).  The
+ * rounding takes dloss's digits with it, alike for every token of the same dloss (bf16:
+ * up to 2^-8 of it), and nothing of a power of two.  A row whose target is ignore_index
+ * has a D of zeros whatever its logits, dloss and lse are; its row of A still enters dB's
+ * sums, times zero, and has to be finite.  Any other target outside [0, V) makes the row's
+ * D NaN.  dA or dB may be NULL: not computed.
  * The gradient is that of loss: nothing reaches A or B through lse on its own.
  */
 typedef struct {
@@ -242,10 +245,10 @@ typedef struct {
 
 /* T == 0 writes zeros to dB.  Outputs overlap nothing (MT_ERR_ALIAS).  Results do
  * not depend on which of dA and dB are asked for, and are the same bits each time.
- * Scratch: a piece of D, dA's sums in fp32 (once for several pieces of the
- * vocabulary, or for each of up to sms / 2 slices of a long one), and copies of
- * operands TMA cannot read in place.  Other errors as
- * mt_linear_cross_entropy. */
+ * Scratch: a piece of D; for several pieces of the vocabulary or a long one dA's sums in
+ * fp32, up to sms / 2 times (slices), T rounded up to whole 256 rows; in fp16 32 bytes a
+ * token and two vectors of max(T, K, the piece's columns) floats; and copies of operands
+ * TMA cannot read in place.  Other errors as mt_linear_cross_entropy. */
 MT_API mt_status mt_linear_cross_entropy_backward(
     const mt_linear_cross_entropy_backward_args *args, cudaStream_t stream);
 

@@ -3,11 +3,11 @@
 // the rounding of dX's sums.
 //
 // Bound by the tensor cores for batches (2 T K V operations forwards, 6 back,
-// of which a third computes the logits again): bf16, V x K weight, 8192 x 4096 x
-// 131072 forwards 5.0 ms, 1761 TFLOP/s, 4096 x 4096 x 131072 back 6.9 ms, 1903
-// TFLOP/s.  Few tokens are bound by the weight's stream: one token x 4096 x 131072
-// 162 us, 0.98 of the copy rate; back 566 us, the weight read twice and its gradient
-// written.
+// of which a third computes the logits again): bf16, V x K weight, calls back to back
+// for a second, 8192 x 4096 x 131072 forwards 4.9 to 5.0 ms, 1765 to 1782 TFLOP/s, 4096
+// x 4096 x 131072 back 7.8 ms, 1698 TFLOP/s.  Few tokens are bound by the weight's
+// stream: one token x 4096 x 131072 162 us, 0.98 of the copy rate; back 571 us, the
+// weight read twice and its gradient written.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(kRowThreads) size_kernel(const RowArgs a) {
 }
 
 // The tokens' factors of D.  From `ctas` maxima: D's scale is the power of two
-// that brings the largest to [2^13, 2^14): fp16 then keeps ten digits of a
-// probability down to 2^-27 of the largest factor, and 65504 is not reached.
+// that brings the largest to [2^13, 2^14): fp16 then keeps its eleven bits down to
+// 2^-27 (7.5e-9) of the largest factor and one fewer for each half of that (1e-9: eight
+// or nine), and 65504 is not reached.
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowArgs a, int ctas) {
   grid_launch_dependents();
   grid_wait();

@@ -7,13 +7,17 @@
 // and the CTAs' shares are added in a fixed order by a second kernel.  Rows
 // that start on 16 bytes stream through shared memory
 // (layer_norm_grad_staged_kernel), others through registers
-// (layer_norm_grad_kernel); rows too wide for either are read twice.  Arithmetic
-// in pairs of values, one instruction each.
+// (layer_norm_grad_kernel).  Of rows too wide for either dy and h pass three times, once
+// for the column sums where they are wanted (layer_norm_grad_columns_kernel) and twice
+// for dx (layer_norm_grad_wide_kernel, the second time mostly from L2).  Arithmetic in
+// pairs of values, one instruction each.
 //
-// Measured on GB300 (bf16 with dh, share of the copy rate): 16384 x 4096 100 us,
-// 0.79, with dropout 141 us, 0.70; 16384 x 8192 194 us, 0.81; 4096 x 16384 200 us, 0.40
+// Measured on GB300 (bf16 with dh, the required bytes' share of the copy rate): 16384 x
+// 4096 100 us, 0.79, with dropout 141 us, 0.70; 16384 x 8192 194 us, 0.81; 4096 x 16384 200 us, 0.40
 // (32 values a thread spill 150 bytes); fp32 8192 x 8192 206 us, 0.77; unaligned
-// 16384 x 4095 127 us, 0.62; 4096 x 20000, read twice, 220 us, 0.44.
+// 16384 x 4095 127 us, 0.62.  Too wide: 4096 x 20000 221 us, 0.44 (150 us, 0.64 without
+// column sums); 4096 x 20001 322 us, 0.30; unaligned past 8192, 4096 x 12001 206 us,
+// 0.28; fp32 2048 x 13000 139 us, 0.45, 2048 x 16384 155 us, 0.51.
 #pragma once
 
 #include <algorithm>

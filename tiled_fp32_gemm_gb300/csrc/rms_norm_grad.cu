@@ -4,7 +4,8 @@
 // share of dweight in registers from row to row, and the CTAs' shares are
 // added in a fixed order by a second kernel.  Rows that start on 16 bytes
 // stream through shared memory (rms_norm_grad_staged_kernel), others through
-// registers (rms_norm_grad_kernel), rows too wide for either are read twice.
+// registers (rms_norm_grad_kernel).  Of rows too wide for either dy and h pass three
+// times, once for dweight where it is wanted and twice for dx.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
