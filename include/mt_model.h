@@ -210,15 +210,16 @@ MT_API mt_status mt_linear_cross_entropy(const mt_linear_cross_entropy_args *arg
  *     dB = A^T * D, stored as B is         K x V (V x K with trans_b), db_dtype
  *
  * D is rounded to dtype for the two products, whatever db_dtype is, and held for one
- * piece of the vocabulary at a time (up to 1 GiB, but at least 256 columns); in fp16 it is
- * held times a power of two that brings the largest |dloss| (1 + 2 c |lse|) of the call to
- * 2^13 or more, so that values down to 2^-27 of the largest factor keep all of their bits
- * (p is at most 1 with the forward call's lse; with another D may overflow).  The
- * rounding takes dloss's digits with it, alike for every token of the same dloss (bf16:
- * up to 2^-8 of it), and nothing of a power of two.  A row whose target is ignore_index
- * has a D of zeros whatever its logits, dloss and lse are; its row of A still enters dB's
- * sums, times zero, and has to be finite.  Any other target outside [0, V) makes the row's
- * D NaN.  dA or dB may be NULL: not computed.
+ * piece of the vocabulary at a time (up to 1 GiB, but at least 256 columns).  In fp16,
+ * and in bf16 for (T + 256) K V of 2^36 and more, it is held times a scale that makes the
+ * largest |dloss| (1 - s) of the call a power of two, so that a dloss that all tokens
+ * have is not rounded with D, and brings the largest |dloss| (1 + 2 c |lse|) to 2^13 or
+ * more, so that fp16 keeps all bits of values down to 2^-27 of it (p is at most 1 with
+ * the forward call's lse; with another D may overflow).  Smaller bf16 calls round dloss
+ * with D, alike for every token that has it: by up to 2^-8, a power of two not at all.  A
+ * row whose target is ignore_index has a D of zeros whatever its logits, dloss and lse
+ * are; its row of A still enters dB's sums, times zero, and has to be finite.  Any other
+ * target outside [0, V) makes the row's D NaN.  dA or dB may be NULL: not computed.
  * The gradient is that of loss: nothing reaches A or B through lse on its own.
  */
 typedef struct {
@@ -246,9 +247,9 @@ typedef struct {
 /* T == 0 writes zeros to dB.  Outputs overlap nothing (MT_ERR_ALIAS).  Results do
  * not depend on which of dA and dB are asked for, and are the same bits each time.
  * Scratch: a piece of D; for several pieces of the vocabulary or a long one dA's sums in
- * fp32, up to sms / 2 times (slices), T rounded up to whole 256 rows; in fp16 32 bytes a
- * token and two vectors of max(T, K, the piece's columns) floats; and copies of operands
- * TMA cannot read in place.  Other errors as mt_linear_cross_entropy. */
+ * fp32, up to sms / 2 times (slices), T rounded up to whole 256 rows; where D is scaled
+ * 32 bytes a token and two vectors of max(T, K, the piece's columns) floats; and copies of
+ * operands TMA cannot read in place.  Other errors as mt_linear_cross_entropy. */
 MT_API mt_status mt_linear_cross_entropy_backward(
     const mt_linear_cross_entropy_backward_args *args, cudaStream_t stream);
 

@@ -194,14 +194,15 @@ cudaError_t launch_head_loss(const HeadLossArgs& a, const HeadLossPlan& p, float
 
 namespace {
 
-// fp16: the tokens' factors, with D's scale in them, are made beforehand.
+// Where D is held times a scale, the tokens' factors with the scale in them are made
+// beforehand.
 struct RowArgs {
   int64_t T;
   HeadSource source;
   HeadRow* rows;
-  // Per-CTA maxima of a token's largest factor (amax), and what the products'
-  // results are multiplied with to undo D's scale: n factors for their rows, n
-  // ones for their columns.
+  // Per-CTA maxima (amax, kMaxCtas of a token's largest factor and as many of
+  // |dloss|), and what the products' results are multiplied with to undo D's scale: n
+  // factors for their rows, n ones for their columns.
   float* amax;
   float* undo;
   float* ones;
@@ -210,54 +211,75 @@ struct RowArgs {
 };
 
 constexpr int kRowThreads = 256;
-constexpr int kMaxCtas = 256;  // CTAs that leave a maximum
+constexpr int kMaxCtas = 256;  // CTAs that leave maxima
 
-// The largest factor of a token's D: |dloss| (1 + 2 c |lse|); 0 for what does
-// not count (no target, not finite).
-__device__ __forceinline__ float size_of(const RowArgs& a, int64_t t) {
-  const HeadSource& s = a.source;
-  if (s.target[t] == s.ignore_index) return 0.0f;
-  const float v = fabsf(s.dloss[t]) * (1.0f + 2.0f * s.z_loss * fabsf(s.lse[t]));
-  return v < INFINITY ? v : 0.0f;
-}
+// What counts of a value's size: 0 unless it is finite.
+__device__ __forceinline__ float finite(float v) { return v < INFINITY ? v : 0.0f; }
 
-// Maximum over the CTA, in thread 0's warp.
-__device__ __forceinline__ float cta_max(float v) {
-  __shared__ float part[kRowThreads / 32];
-  v = warp_max(v);
+// Maxima over the CTA, in every warp.
+__device__ __forceinline__ float2 cta_max(float2 v) {
+  __shared__ float2 part[kRowThreads / 32];
+  v = make_float2(warp_max(v.x), warp_max(v.y));
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
   __syncthreads();
-  return warp_max(threadIdx.x % 32 < kRowThreads / 32 ? part[threadIdx.x % 32] : 0.0f);
+  v = threadIdx.x % 32 < kRowThreads / 32 ? part[threadIdx.x % 32] : make_float2(0.0f, 0.0f);
+  return make_float2(warp_max(v.x), warp_max(v.y));
 }
 
 __global__ void __launch_bounds__(kRowThreads) size_kernel(const RowArgs a) {
   grid_launch_dependents();
   grid_wait();
-  float v = 0.0f;
+  const HeadSource& s = a.source;
+  float2 v = make_float2(0.0f, 0.0f);  // |dloss| (1 + 2 c |lse|), |dloss|
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; t < a.T;
-       t += static_cast<int64_t>(gridDim.x) * kRowThreads)
-    if (bounds_ok(a.bounds, SITE_ROWS, t, 1, a.T)) v = fmaxf(v, size_of(a, t));
+       t += static_cast<int64_t>(gridDim.x) * kRowThreads) {
+    if (!bounds_ok(a.bounds, SITE_ROWS, t, 1, a.T) || s.target[t] == s.ignore_index) continue;
+    const float g = fabsf(s.dloss[t]);
+    v.x = fmaxf(v.x, finite(g * (1.0f + 2.0f * s.z_loss * fabsf(s.lse[t]))));
+    v.y = fmaxf(v.y, finite(g));
+  }
   v = cta_max(v);
-  if (threadIdx.x == 0) a.amax[blockIdx.x] = v;
+  if (threadIdx.x == 0) {
+    a.amax[blockIdx.x] = v.x;
+    a.amax[kMaxCtas + blockIdx.x] = v.y;
+  }
 }
 
-// The tokens' factors of D.  From `ctas` maxima: D's scale is the power of two
-// that brings the largest to [2^13, 2^14): fp16 then keeps its eleven bits down to
+// D's scale, and what undoes it, from the largest factor of the call and its
+// largest |dloss| times 1 - s, the size of a D's entry at its target.  The scale makes
+// the latter a power of two, so that a dloss that all tokens have (a mean's 1 / T)
+// is not rounded with D, alike everywhere, and brings the largest factor to
+// [2^13, 2^14).  Both are good to 2^-24.
+struct Scale {
+  float scale, undo;
+};
+__device__ __forceinline__ Scale scale_of(float top, float hit) {
+  if (!(top > 0.0f)) return Scale{1.0f, 1.0f};
+  const float m = hit > 0.0f ? ldexpf(hit, -ilogbf(hit)) : 1.0f;  // in [1, 2)
+  const int e = max(-126, min(126, 13 - ilogbf(top / m)));
+  return Scale{ldexpf(1.0f / m, e), ldexpf(m, -e)};
+}
+
+// The tokens' factors of D, with its scale from `ctas` CTAs' maxima.  With the largest
+// factor in [2^13, 2^14) fp16 keeps its eleven bits down to
 // 2^-27 (7.5e-9) of the largest factor and one fewer for each half of that (1e-9: eight
 // or nine), and 65504 is not reached.
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowArgs a, int ctas) {
   grid_launch_dependents();
   grid_wait();
-  const float top = cta_max(static_cast<int>(threadIdx.x) < ctas ? a.amax[threadIdx.x] : 0.0f);
-  const float scale = ldexpf(1.0f, top > 0.0f ? max(-126, min(126, 13 - ilogbf(top))) : 0);
+  const bool there = static_cast<int>(threadIdx.x) < ctas;
+  const float2 top = cta_max(there ? make_float2(a.amax[threadIdx.x], a.amax[kMaxCtas + threadIdx.x])
+                                   : make_float2(0.0f, 0.0f));
+  const float at_target = 1.0f - a.source.smoothing;
+  const Scale s = scale_of(top.x, top.y * (at_target > 0.0f ? at_target : 1.0f));
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
        i < max(a.T, a.n); i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
     if (i < a.n) {
-      a.undo[i] = 1.0f / scale;
+      a.undo[i] = s.undo;
       a.ones[i] = 1.0f;
     }
     if (i >= a.T || !bounds_ok(a.bounds, SITE_ROWS, i, 1, a.T)) continue;
-    a.rows[i] = a.source.row(i, scale);
+    a.rows[i] = a.source.row(i, s.scale);
   }
 }
 
@@ -321,6 +343,20 @@ __global__ void __launch_bounds__(kRowThreads)
 //                   4096 x 1024 x 262144  4645 / 3971 / 4150 / 4162 / 4121
 //                   32768 x 1024 x 32768  5530 / 4333 / 4336 / 4407 / 3869
 constexpr int64_t kPieceBytes = int64_t(1) << 30;
+
+// Whether D is held times a scale: fp16's range wants it, and in both types dloss's
+// own digits are then not rounded away (see Scale): 1 / 1021 for all of 1021 tokens in
+// bf16, dB in fp32 off by 2.9e-3 of its norm without.  bf16 goes without where the two
+// small kernels that make it would show, in gradients of less than some 280 us: the
+// weight's passes take as long as 256 tokens' products.  Measured (bf16, us without and
+// with): 16 x 1024 x 8192 28.9 / 33, 256 x 1024 x 8192 38 / 43, 1024 x 4096 x 9000 156 / 159,
+// 256 x 4096 x 32768 205 / 213, 8192 x 1024 x 8192 274 / 276, 64 x 4096 x 131072 608 / 613,
+// 8192 x 2048 x 65536 4088 / 4098, 4096 x 4096 x 131072 7700 / 7790 (under the power cap).
+constexpr double kScaledWork = 68719476736.0;  // 2^36
+
+bool scaled(const HeadLossArgs& l) {
+  return l.dtype == DT_F16 || (l.T + 256.0) * l.K * l.V >= kScaledWork;
+}
 
 // The two products of a piece of the vocabulary.
 struct Products {
@@ -418,9 +454,9 @@ HeadGradPlan plan_head_grad(const HeadGradArgs& a, int sms) {
   const int64_t widest = std::min(l.V, p.piece);
   p.ldd = ceil_div(widest, 64) * 64;
   p.d_bytes = up256(l.T * p.ldd * 2);
-  if (l.dtype == DT_F16) {
+  if (scaled(l)) {
     p.rows_bytes = up256(l.T * static_cast<int64_t>(sizeof(HeadRow)));
-    p.scale_bytes = kMaxCtas * 4 + 2 * up256(4 * std::max({l.T, l.K, widest}));
+    p.scale_bytes = 2 * kMaxCtas * 4 + 2 * up256(4 * std::max({l.T, l.K, widest}));
   }
   const Piece first = piece_of(l, 0, widest);
   p.x_bytes = up256(padded_bytes(copy_of_x(l), 2));
@@ -459,7 +495,7 @@ cudaError_t launch_head_grad(const HeadGradArgs& args, const HeadGradPlan& p, vo
   if (p.scale_bytes) {
     r.n = std::max({l.T, l.K, std::min(l.V, p.piece)});
     r.amax = reinterpret_cast<float*>(scales);
-    r.undo = reinterpret_cast<float*>(scales + kMaxCtas * 4);
+    r.undo = reinterpret_cast<float*>(scales + 2 * kMaxCtas * 4);
     r.ones = r.undo + up256(4 * r.n) / 4;
     const int ctas = static_cast<int>(std::min<int64_t>(kMaxCtas, ceil_div(l.T, kRowThreads)));
     e = launch_dependent(size_kernel, static_cast<unsigned>(ctas), kRowThreads, stream, r);
