@@ -7,8 +7,9 @@ Importing this module registers ``torch.ops.mt.sgemm(a, b)``,
 and ``torch.ops.mt.linear_cross_entropy`` as torch custom operators: the same
 C-ABI calls as the functions of those names (``gemm(..., bias=...)``), visible
 to torch's dispatcher, graph capture and tracing (each has a shape-only fake
-implementation, so tracing needs no GPU).  All but the first two are
-differentiable, once: their gradients are the ``*_backward`` functions (for
+implementation, so tracing needs no GPU).  Tracing takes them forwards: a backward
+pass is captured in a graph but not traced (``torch.compile`` of one raises).  All
+but the first two are differentiable, once: their gradients are the ``*_backward`` functions (for
 dropout, dropout itself), which have none themselves, so a second derivative
 raises.  A seed that is advanced in place between an operator and its gradient
 raises too: torch notices it.  No gradient of zeros is made for an output that
